@@ -3,7 +3,8 @@
 // described in include/graft.h; the kernels live in assemble.cu (assembly,
 // incremental drafting, confidences), umax.cu + select.cu (the default verify
 // scan), scan.cu (single-pass scan, finishing, warm-up), scan_tma.cu,
-// sample.cu (stochastic verification), coverage.cu and noalloc.cu.
+// sample.cu (stochastic verification), coverage.cu, noalloc.cu and
+// logit_rules.cu; the paged-cache calls (graft_kv_*) are in kv.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -16,6 +17,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "graft_internal.cuh"
+#include "logit_rules.cuh"
 
 struct graft_handle {
   graft_config cfg;
@@ -750,7 +752,55 @@ int graft_verify_update_sample(graft_handle* h, int32_t batch, const int32_t* d_
                      d_out_tokens, true, temperature, d_u_accept, d_u_resid, stream);
 }
 
-
+int graft_process_logits(graft_handle* h, int32_t batch, int32_t slots, const int32_t* d_tree_tok,
+                         const uint64_t* d_tree_mask, const void* d_logits, int64_t row_stride,
+                         const graft_logit_rules* rules, void* d_out, int64_t out_stride, void* stream) {
+  NvtxRange nvtx("graft_process_logits");
+  if (!h) return GRAFT_EINVAL;
+  h->last_launches = 0;
+  const graft_config& c = h->cfg;
+  if (batch < 0 || batch > 65535) return fail(h, GRAFT_EINVAL, "batch %d outside [0, 65535]", batch);
+  if (slots < 1 || slots > graft::MAX_S) return fail(h, GRAFT_EINVAL, "slots %d outside [1, 64]", slots);
+  if (!rules) return fail(h, GRAFT_EINVAL, "null pointer");
+  const graft_logit_rules& r = *rules;
+  if (row_stride < c.vocab || out_stride < c.vocab) return fail(h, GRAFT_EINVAL, "a row stride is less than vocab");
+  if (r.hist_stride < 0 || r.hist_stride >= (1 << 19)) return fail(h, GRAFT_EINVAL, "hist_stride must be in [0, 2^19)");
+  if (r.n_bias < 0 || r.n_bias > 2046) return fail(h, GRAFT_EINVAL, "n_bias must be in [0, 2046]");
+  if (r.n_grammar < 0 || (r.d_grammar && r.grammar_stride < ((int64_t)c.vocab + 31) / 32))
+    return fail(h, GRAFT_EINVAL, "n_grammar must be >= 0 and grammar_stride hold a bit for every token");
+  if (batch == 0) return GRAFT_OK;
+  if (!d_logits || !d_out || !d_tree_tok != !d_tree_mask || (r.d_hist && !r.d_hist_len) ||
+      (r.n_bias > 0 && (!r.d_bias_tok || !r.d_bias_val)) || (r.d_grammar && !r.d_grammar_row))
+    return fail(h, GRAFT_EINVAL, "null pointer");
+  const size_t es = c.logits_dtype == GRAFT_BF16 ? 2 : 4;
+  if (graft::misaligned(d_tree_tok, 4) || graft::misaligned(d_tree_mask, 8) || graft::misaligned(d_logits, es) ||
+      graft::misaligned(d_out, es) || graft::misaligned(r.d_hist, 4) || graft::misaligned(r.d_hist_len, 4) ||
+      graft::misaligned(r.d_prompt_len, 4) || graft::misaligned(r.d_penalty, 4) || graft::misaligned(r.d_bias_tok, 4) ||
+      graft::misaligned(r.d_bias_val, 4) || graft::misaligned(r.d_grammar, 4) || graft::misaligned(r.d_grammar_row, 4))
+    return fail(h, GRAFT_EINVAL, "a buffer is not aligned to its element size");
+  // in place is element by element; rows that overlap otherwise would be read after they are written
+  const uintptr_t in0 = reinterpret_cast<uintptr_t>(d_logits), out0 = reinterpret_cast<uintptr_t>(d_out);
+  const uintptr_t last = (uintptr_t)((int64_t)batch * slots - 1);
+  const uintptr_t in1 = in0 + (last * (uintptr_t)row_stride + c.vocab) * es;
+  const uintptr_t out1 = out0 + (last * (uintptr_t)out_stride + c.vocab) * es;
+  if (in0 < out1 && out0 < in1 && !(in0 == out0 && row_stride == out_stride))
+    return fail(h, GRAFT_EINVAL, "d_out overlaps d_logits without being it at the same stride");
+  graft::LogitArgs a{};
+  a.r = r;
+  if (!a.r.d_hist) a.r.hist_stride = 0;
+  a.V = c.vocab; a.batch = batch; a.slots = slots;
+  a.tree_tok = d_tree_tok; a.tree_mask = d_tree_mask;
+  a.in = d_logits; a.out = d_out; a.in_stride = row_stride; a.out_stride = out_stride;
+  a.err = h->err;
+  cudaError_t e;
+  {
+    ProfScope ps(h, (cudaStream_t)stream, "k_logit_rules");
+    e = graft::launch_logit_rules(a, c.logits_dtype, h->num_sms, (cudaStream_t)stream);
+  }
+  if (e != cudaSuccess) return cuda_fail(h, e, "graft_process_logits launch");
+  h->last_launches = 1;
+  return GRAFT_OK;
+}
 
 int graft_get_matrix(graft_handle* h, int32_t* host_out, void* stream) {
   if (!h || !host_out) return fail(h, GRAFT_EINVAL, "null pointer");
@@ -778,9 +828,9 @@ int graft_sync(graft_handle* h, void* stream, uint32_t* out_flags) {
   if (e == cudaSuccess && flags) e = cudaMemset(h->err, 0, sizeof(uint32_t));
   if (out_flags) *out_flags = flags;
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_sync");
-  if (flags) return fail(h, GRAFT_EDEVICE, "device error flags 0x%x (token %d, nan %d, tree %d, timeout %d)", flags,
-                         !!(flags & GRAFT_ERR_TOKEN), !!(flags & GRAFT_ERR_NAN), !!(flags & GRAFT_ERR_TREE),
-                         !!(flags & GRAFT_ERR_TIMEOUT));
+  if (flags) return fail(h, GRAFT_EDEVICE, "device error flags 0x%x (token %d, nan %d, tree %d, timeout %d, rule %d)",
+                         flags, !!(flags & GRAFT_ERR_TOKEN), !!(flags & GRAFT_ERR_NAN), !!(flags & GRAFT_ERR_TREE),
+                         !!(flags & GRAFT_ERR_TIMEOUT), !!(flags & GRAFT_ERR_RULE));
   return GRAFT_OK;
 }
 

@@ -1,0 +1,80 @@
+// Declarations shared by the paged-cache translation units (kv.cu, kv_append.cu, kv_attend.cu).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "graft_internal.cuh"
+
+namespace graft {
+
+struct KvLayout {
+  int32_t q_heads, kv_heads, dim, rot, interleaved, page_size, page_shift, num_pages;
+  int64_t page_stride, head_stride, token_stride;  // elements
+};
+
+struct AppendArgs {
+  KvLayout c;
+  int32_t batch, slots;
+  int32_t vec;  // 1 = 16-byte loads and stores everywhere, and whole 16-byte pieces rotate together
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *depth, *rows;
+  const float* rope;
+  int32_t rope_len, prefix_len;
+  const int32_t* page_table;
+  int32_t table_stride;
+  const int32_t* ctx_len;
+  void *q_out, *k_cache, *v_cache;
+  uint32_t* err;
+};
+
+struct AttendArgs {
+  KvLayout c;
+  int32_t batch, slots, group;  // group = query heads per kv head
+  const void *q, *k_cache, *v_cache;
+  int64_t q_stride, out_stride;
+  const int32_t* prefix_pages;
+  int32_t prefix_len;
+  const int32_t* page_table;
+  int32_t table_stride;
+  const int32_t* ctx_len;
+  int32_t max_ctx;
+  const uint64_t* tree_mask;
+  float scale;
+  void* out;
+  float* lse;
+  uint32_t* err;
+};
+
+// 16-bit element types of the cache: packed pairs to and from fp32.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 get(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t put(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 get(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t put(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  static __device__ __forceinline__ float one(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half round(float x) { return __float2half_rn(x); }
+};
+
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_kv_attend(const AttendArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace graft

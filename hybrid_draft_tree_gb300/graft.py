@@ -21,8 +21,9 @@ from . import _build
 
 GRAFT_OK, GRAFT_EINVAL, GRAFT_ENOMEM, GRAFT_ECUDA, GRAFT_EDEVICE = 0, -1, -2, -3, -4
 GRAFT_ERR_TOKEN, GRAFT_ERR_NAN, GRAFT_ERR_TREE, GRAFT_ERR_TIMEOUT = 1, 2, 4, 8
+GRAFT_ERR_RANGE, GRAFT_ERR_RULE = 16, 32
 GRAFT_MODE_CHECKPOINT, GRAFT_MODE_STATIC, GRAFT_MODE_TAIL = 0, 1, 2
-GRAFT_F32, GRAFT_BF16 = 0, 1
+GRAFT_F32, GRAFT_BF16, GRAFT_F16 = 0, 1, 2
 K = 8
 
 # Entry points declared in include/graft.h (checked by the CPU tests).
@@ -31,7 +32,9 @@ EXPORTS = ("graft_default_config", "graft_init", "graft_destroy", "graft_warmup"
            "graft_sync", "graft_last_error", "graft_last_launch_count", "graft_verify_update_noalloc",
            "graft_profile_enable", "graft_profile_read", "graft_check", "graft_retrieve", "graft_assemble_staged",
            "graft_confidence", "graft_calibrate_thresholds", "graft_set_thresholds", "graft_coverage",
-           "graft_verify_update_sample", "graft_template", "graft_set_wait_limit")
+           "graft_verify_update_sample", "graft_template", "graft_set_wait_limit", "graft_process_logits",
+           "graft_kv_default_config", "graft_kv_init", "graft_kv_destroy", "graft_kv_append", "graft_kv_attend",
+           "graft_kv_sync", "graft_kv_last_error", "graft_kv_last_launch_count", "graft_kv_set_wait_limit")
 
 
 def calibrate_thresholds(best: np.ndarray, quantile: float) -> np.ndarray:
@@ -71,6 +74,22 @@ class graft_config(ctypes.Structure):
                 ("ckpt_draft", ctypes.c_int32 * 3), ("tpl_depth", ctypes.c_int32), ("tpl_width", ctypes.c_int32),
                 ("static_thr", ctypes.c_float), ("tail_thr", ctypes.c_float), ("max_draft_nodes", ctypes.c_int32),
                 ("scan_kernel", ctypes.c_int32), ("ablation", ctypes.c_int32), ("fixed_draft", ctypes.c_int32)]
+
+
+class graft_kv_config(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("rot_interleaved", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_batch", ctypes.c_int32), ("max_slots", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class graft_logit_rules(ctypes.Structure):
+    _fields_ = [("d_hist", ctypes.c_void_p), ("hist_stride", ctypes.c_int64), ("d_hist_len", ctypes.c_void_p),
+                ("d_prompt_len", ctypes.c_void_p), ("d_penalty", ctypes.c_void_p), ("d_bias_tok", ctypes.c_void_p),
+                ("d_bias_val", ctypes.c_void_p), ("n_bias", ctypes.c_int32), ("n_grammar", ctypes.c_int32),
+                ("d_grammar", ctypes.c_void_p), ("grammar_stride", ctypes.c_int64),
+                ("d_grammar_row", ctypes.c_void_p)]
 
 
 _lib = None
@@ -124,6 +143,21 @@ def load(build_if_missing: bool = True):
     L.graft_profile_read.restype = ctypes.c_int
     L.graft_verify_update_noalloc.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.graft_verify_update_noalloc.restype = ctypes.c_int
+    L.graft_process_logits.argtypes = [vp, i32, i32, vp, vp, vp, i64, ctypes.POINTER(graft_logit_rules), vp, i64, vp]
+    L.graft_kv_default_config.argtypes = [ctypes.POINTER(graft_kv_config), *([i32] * 8)]
+    L.graft_kv_default_config.restype = None
+    L.graft_kv_init.argtypes = [ctypes.POINTER(graft_kv_config), ctypes.POINTER(vp)]
+    L.graft_kv_destroy.argtypes = [vp]
+    L.graft_kv_append.argtypes = [vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i32, vp, vp, i64,
+                                  vp, vp, vp]
+    L.graft_kv_attend.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, i64,
+                                  vp, vp]
+    L.graft_kv_sync.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
+    L.graft_kv_last_error.argtypes = [vp]
+    L.graft_kv_last_error.restype = ctypes.c_char_p
+    L.graft_kv_last_launch_count.argtypes = [vp]
+    L.graft_kv_last_launch_count.restype = i32
+    L.graft_kv_set_wait_limit.argtypes = [vp, ctypes.c_uint32]
     for name in ("graft_init", "graft_destroy", "graft_warmup", "graft_assemble", "graft_assemble_src",
                  "graft_verify_update", "graft_get_matrix", "graft_set_matrix", "graft_sync"):
         getattr(L, name).restype = ctypes.c_int
@@ -186,6 +220,38 @@ def _rows(t, name, dtype, rows, vocab):
     if not _on_device(t):
         raise GraftError(GRAFT_EINVAL, f"{name}: expected a CUDA tensor (device buffer), got {t.device}")
     return vp(t.data_ptr()), (t2.stride(0) if t2.shape[0] > 1 else max(t2.stride(0), t.shape[-1]))
+
+
+def _ptr32(t, name, numel):
+    return _buf(t, name, _dtypes("int32"), numel)
+
+
+def _table(t, name, dtype, rows):
+    """(pointer, row length) of a contiguous 2-d buffer of at least `rows` rows."""
+    if t is None:
+        return None, 0
+    if not hasattr(t, "dim") or t.dim() != 2:
+        raise GraftError(GRAFT_EINVAL, f"{name}: expected a 2-d torch tensor")
+    return _buf(t, name, _dtypes(dtype), rows * t.shape[1]), t.shape[1]
+
+
+def _cache(t, name, dtype, cfg):
+    """Pointer to a cache buffer: a tensor whose storage, from its first
+    element on, holds every element the handle's strides reach."""
+    if t is None:
+        return None
+    if not hasattr(t, "data_ptr") or not hasattr(t, "is_cuda"):
+        raise GraftError(GRAFT_EINVAL, f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise GraftError(GRAFT_EINVAL, f"{name}: dtype {t.dtype}, the handle's cache is {dtype}")
+    span = ((cfg.num_pages - 1) * cfg.page_stride + (cfg.kv_heads - 1) * cfg.head_stride +
+            (cfg.page_size - 1) * cfg.token_stride + cfg.head_dim)
+    held = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    if held < span:
+        raise GraftError(GRAFT_EINVAL, f"{name}: {held} elements, the handle's pages reach {span}")
+    if not _on_device(t):
+        raise GraftError(GRAFT_EINVAL, f"{name}: expected a CUDA tensor (device buffer), got {t.device}")
+    return vp(t.data_ptr())
 
 
 def _stream(stream):
@@ -347,6 +413,34 @@ class Graft:
                                                       _buf(out_tokens, "out_tokens", _dtypes("int32"), b * self.S),
                                                       _stream(stream)))
 
+    def process_logits(self, batch, slots, logits, out, tree_tok=None, tree_mask=None, hist=None, hist_len=None,
+                       prompt_len=None, penalty=None, bias_tok=None, bias_val=None, grammar=None, grammar_row=None,
+                       stream=None):
+        """Penalties, biases and grammar masks on batch * slots rows of logits,
+        into out (which may be logits): see graft_process_logits in
+        include/graft.h.  hist: int32 [batch, longest]; penalty: float32
+        [batch, 3] (repetition, frequency, presence); bias_tok, bias_val:
+        [batch, entries]; grammar: int32 [rows, >= ceil(V / 32)] bits;
+        grammar_row: int32 [batch, slots].  A rule that is None is off."""
+        b, n = max(batch, 0), max(batch, 0) * slots
+        ldt, V = self._logits_dtype(), self.cfg.vocab
+        pl, stride = _rows(logits, "logits", ldt, n, V)
+        po, out_stride = _rows(out, "out", ldt, n, V)
+        r = graft_logit_rules()
+        r.d_hist, r.hist_stride = _table(hist, "hist", "int32", b)
+        r.d_hist_len = _ptr32(hist_len, "hist_len", b)
+        r.d_prompt_len = _ptr32(prompt_len, "prompt_len", b)
+        r.d_penalty = _buf(penalty, "penalty", _dtypes("float32"), 3 * b)
+        r.d_bias_tok, n_bias = _table(bias_tok, "bias_tok", "int32", b)
+        r.n_bias = n_bias
+        r.d_bias_val = _buf(bias_val, "bias_val", _dtypes("float32"), b * n_bias)
+        r.d_grammar, r.grammar_stride = _table(grammar, "grammar", "int32", 0)
+        r.n_grammar = 0 if grammar is None else grammar.shape[0]
+        r.d_grammar_row = _ptr32(grammar_row, "grammar_row", n)
+        self._check(self.L.graft_process_logits(self.h, batch, slots, _ptr32(tree_tok, "tree_tok", n),
+                                                _buf(tree_mask, "tree_mask", _dtypes("int64", "uint64"), n), pl, stride,
+                                                ctypes.byref(r), po, out_stride, _stream(stream)))
+
     def get_matrix(self, stream=None) -> np.ndarray:
         out = np.empty((self.cfg.vocab, K), np.int32)
         self._check(self.L.graft_get_matrix(self.h, out.ctypes.data_as(vp), _stream(stream)))
@@ -389,6 +483,112 @@ class Graft:
     def set_wait_limit(self, polls: int):
         """Poll limit of the bulk-copy kernels' mbarrier waits (0 = the default)."""
         self._check(self.L.graft_set_wait_limit(self.h, int(polls)))
+
+
+def graft_kv_default_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_slots, dtype=GRAFT_BF16,
+                            layout="head", **overrides):
+    """layout: "head" for pages of [kv_heads, page_size, head_dim], "token" for
+    [page_size, kv_heads, head_dim]; other strides through the overrides."""
+    cfg = graft_kv_config()
+    load().graft_kv_default_config(ctypes.byref(cfg), q_heads, kv_heads, head_dim, page_size, num_pages, max_batch,
+                                   max_slots, dtype)
+    if layout not in ("head", "token"):
+        raise GraftError(GRAFT_EINVAL, f"layout {layout!r}, expected 'head' or 'token'")
+    if layout == "token":
+        cfg.head_stride, cfg.token_stride = head_dim, kv_heads * head_dim
+    for k, v in overrides.items():
+        setattr(cfg, k, v)
+    return cfg
+
+
+class GraftKV:
+    """One libgraft paged-cache handle (graft_kv in include/graft.h): the
+    target's keys, values and attention around a draft tree.  The caches are
+    the caller's tensors."""
+
+    def __init__(self, cfg: graft_kv_config):
+        import torch
+        self.L = load()
+        self.cfg = cfg
+        self.dtype = torch.float16 if cfg.dtype == GRAFT_F16 else torch.bfloat16
+        h = vp()
+        rc = self.L.graft_kv_init(ctypes.byref(cfg), ctypes.byref(h))
+        if rc != GRAFT_OK:
+            raise GraftError(rc, "graft_kv_init failed (bad config, no CUDA device, or out of memory)")
+        self.h = h
+
+    def _check(self, rc):
+        if rc != GRAFT_OK:
+            raise GraftError(rc, self.L.graft_kv_last_error(self.h).decode())
+
+    def close(self):
+        if self.h:
+            self.L.graft_kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def append(self, batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len=0, pos=None,
+               rows=None, stream=None):
+        """Rotate and write the slots' keys and values into the cache, and rotate
+        the queries into q_out (both None: keys and values only).  q, k, v: rows
+        [batch * slots, heads * head_dim], any row stride; rope: float32
+        [positions, rot_dim]; page_table: int32 [batch, pages]; pos: the slots'
+        depths (tree_pos); rows: int32 [batch, slots], the slot each place takes."""
+        c, n, b = self.cfg, max(batch, 0) * slots, max(batch, 0)
+        kw, qw = c.kv_heads * c.head_dim, c.q_heads * c.head_dim
+        pq, qs = _rows(q, "q", self.dtype, n, qw)
+        pk, ks = _rows(k, "k", self.dtype, n, kw)
+        pv, vs = _rows(v, "v", self.dtype, n, kw)
+        po, qos = _rows(q_out, "q_out", self.dtype, n, qw)
+        pr, width = _table(rope, "rope", "float32", 0)
+        if rope is not None and width != c.rot_dim:
+            raise GraftError(GRAFT_EINVAL, f"rope: rows of {width}, the handle rotates {c.rot_dim}")
+        pt, ts = _table(page_table, "page_table", "int32", b)
+        self._check(self.L.graft_kv_append(self.h, batch, slots, pq, qs, pk, ks, pv, vs, _ptr32(pos, "pos", n),
+                                           _ptr32(rows, "rows", n), pr, 0 if rope is None else rope.shape[0], prefix_len,
+                                           pt, ts, _ptr32(ctx_len, "ctx_len", b), po, qos,
+                                           _cache(k_cache, "k_cache", self.dtype, c),
+                                           _cache(v_cache, "v_cache", self.dtype, c), _stream(stream)))
+
+    def attend(self, batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages=None,
+               prefix_len=0, tree_mask=None, scale=None, lse=None, stream=None):
+        """Attention of the slots' rotated queries over the prefix, each
+        request's ctx_len (<= max_ctx) tokens and the tree under tree_mask
+        (None: causal), into out and lse.  scale defaults to head_dim ** -0.5."""
+        c, n, b = self.cfg, max(batch, 0) * slots, max(batch, 0)
+        qw = c.q_heads * c.head_dim
+        pq, qs = _rows(q, "q", self.dtype, n, qw)
+        po, os_ = _rows(out, "out", self.dtype, n, qw)
+        pt, ts = _table(page_table, "page_table", "int32", b)
+        self._check(self.L.graft_kv_attend(self.h, batch, slots, pq, qs, _cache(k_cache, "k_cache", self.dtype, c),
+                                           _cache(v_cache, "v_cache", self.dtype, c),
+                                           _ptr32(prefix_pages, "prefix_pages", -(-max(prefix_len, 0) // c.page_size)),
+                                           prefix_len, pt, ts, _ptr32(ctx_len, "ctx_len", b), max_ctx,
+                                           _buf(tree_mask, "tree_mask", _dtypes("int64", "uint64"), n),
+                                           ctypes.c_float(c.head_dim ** -0.5 if scale is None else scale), po, os_,
+                                           _buf(lse, "lse", _dtypes("float32"), n * c.q_heads), _stream(stream)))
+
+    def sync(self, stream=None, raise_on_error=True) -> int:
+        flags = ctypes.c_uint32(0)
+        rc = self.L.graft_kv_sync(self.h, _stream(stream), ctypes.byref(flags))
+        if raise_on_error:
+            self._check(rc)
+        return int(flags.value)
+
+    def last_error(self) -> str:
+        return self.L.graft_kv_last_error(self.h).decode()
+
+    def last_launch_count(self) -> int:
+        return int(self.L.graft_kv_last_launch_count(self.h))
+
+    def set_wait_limit(self, polls: int):
+        """Poll limit of the attention kernel's mbarrier waits (0 = the default)."""
+        self._check(self.L.graft_kv_set_wait_limit(self.h, int(polls)))
 
 
 class TreeBuffers:

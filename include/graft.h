@@ -67,6 +67,8 @@ typedef enum {
 #define GRAFT_ERR_NAN 2u     /* NaN in a logits row or a draft probability */
 #define GRAFT_ERR_TREE 4u    /* parent index not before its child, bad position */
 #define GRAFT_ERR_TIMEOUT 8u /* a bounded wait inside a kernel expired; that call's results are invalid */
+#define GRAFT_ERR_RANGE 16u /* a cache page, a length, a row or a position outside its range (graft_kv_*) */
+#define GRAFT_ERR_RULE 32u  /* a penalty that is not a number it can be, or a grammar row outside the table */
 
 typedef enum {
   GRAFT_MODE_CHECKPOINT = 0, /* article §二: checkpoints at depths 0/1/5 */
@@ -74,7 +76,7 @@ typedef enum {
   GRAFT_MODE_TAIL = 2        /* article §七: block draft, tail replaced */
 } graft_mode;
 
-typedef enum { GRAFT_F32 = 0, GRAFT_BF16 = 1 } graft_dtype;
+typedef enum { GRAFT_F32 = 0, GRAFT_BF16 = 1, GRAFT_F16 = 2 /* graft_kv_* only */ } graft_dtype;
 
 typedef struct {
   int32_t vocab;          /* V >= 1 */
@@ -293,6 +295,63 @@ int graft_verify_update_sample(graft_handle* h, int32_t batch, const int32_t* d_
                                int64_t row_stride, float temperature, const float* d_u_accept,
                                const float* d_u_resid, int32_t* d_accept_len, int32_t* d_out_tokens, void* stream);
 
+/* Rules on the target's logits (penalties for repeated tokens, biases and
+ * grammar masks), applied to every slot's row before graft_verify_update or
+ * graft_verify_update_sample reads it.  For slot i of request b and token v let
+ *   n    = occurrences of v in hist[b][prompt_len[b] .. hist_len[b]) (the
+ *          output so far, the root's token included), plus the slots j >= 1 on
+ *          the path to i (bit j of d_tree_mask[b][i]) whose token is v: a tree
+ *          is penalised as if its path had been emitted token by token;
+ *   seen = n > 0, or v is in hist[b][0 .. prompt_len[b]);
+ * then, in fp32 and rounded to the logits' type at the end,
+ *   x = logit;  if seen: x = x > 0 ? x / r : x * r;  x -= f * n;
+ *   if n > 0: x -= p;  x += bias of v;  if v is forbidden: x = -inf
+ * with (r, f, p) = d_penalty[b], repetition, frequency and presence.  Rows of
+ * pad slots (token < 0) are neither read nor written.  A forbidden token is
+ * -inf whatever its logit was, NaN included; a row that allows nothing is -inf
+ * throughout.
+ * The struct holds DEVICE pointers; a rule whose pointer is NULL is off:
+ *   d_hist        int32 [batch][hist_stride], hist_stride < 2^19; needs d_hist_len
+ *   d_hist_len    int32 [batch], in [0, hist_stride]
+ *   d_prompt_len  int32 [batch] or NULL (no prompt); above hist_len counts as hist_len
+ *   d_penalty     float [batch][3] or NULL (1, 0, 0)
+ *   d_bias_tok, d_bias_val  [batch][n_bias], n_bias <= 2046; token -1 = no
+ *                 entry; of a token's entries the last one counts
+ *   d_grammar     uint32 [n_grammar][grammar_stride], grammar_stride >= ceil(V / 32):
+ *                 bit v % 32 of word v / 32 set = v is allowed
+ *   d_grammar_row int32 [batch][slots], the slot's row of d_grammar, -1 = all allowed
+ * Bad device data sets GRAFT_ERR_TOKEN (a token outside [0, V): it counts for
+ * nothing) or GRAFT_ERR_RULE (r not finite and > 0, f or p not finite: the
+ * request's penalties are off; a grammar row outside the table: all allowed; a
+ * length outside its range: clamped). */
+typedef struct {
+  const int32_t* d_hist;
+  int64_t hist_stride;
+  const int32_t* d_hist_len;
+  const int32_t* d_prompt_len;
+  const float* d_penalty;
+  const int32_t* d_bias_tok;
+  const float* d_bias_val;
+  int32_t n_bias;
+  int32_t n_grammar;
+  const uint32_t* d_grammar;
+  int64_t grammar_stride;
+  const int32_t* d_grammar_row;
+} graft_logit_rules;
+
+/* Apply `rules` to batch * slots rows: row (b, i) starts at element
+ * (b * slots + i) * row_stride of d_logits and out_stride of d_out, in the
+ * handle's logits type and vocabulary; slots in [1, 64], 1 for decoding
+ * without a tree (it need not be the handle's budget + 1).  d_tree_tok and
+ * d_tree_mask [batch][slots] are those graft_assemble writes; both NULL: no
+ * slot is a pad and no path counts.  d_out may be d_logits at the same stride
+ * (in place); any other overlap is refused.  Rows whose starts lie equally off
+ * a 16-byte boundary in d_logits and d_out move in 16-byte pieces, others by
+ * elements.  Asynchronous; one kernel. */
+int graft_process_logits(graft_handle* h, int32_t batch, int32_t slots, const int32_t* d_tree_tok,
+                         const uint64_t* d_tree_mask, const void* d_logits, int64_t row_stride,
+                         const graft_logit_rules* rules, void* d_out, int64_t out_stride, void* stream);
+
 /* Allocation-free variant of graft_verify_update.  It has no counterpart in
  * the paper: it is an integration entry point for callers that cannot call
  * cudaMalloc, such as an engine that records its decode step into a CUDA
@@ -374,6 +433,118 @@ int32_t graft_last_launch_count(const graft_handle* h);
  * (polls = 0 restores the default of 2^22 polls), so a test can make the
  * waits run out on purpose.  It has no counterpart in the paper. */
 int graft_set_wait_limit(graft_handle* h, uint32_t polls);
+
+/* ---------------------------------------------------------------------------
+ * The target's attention over a paged cache of keys and values: what a decode
+ * step does between graft_assemble and the logits, for the layers of a target
+ * model that the caller runs.  A layer calls, per step,
+ *   graft_kv_append   rotate the slots' queries and keys by their positions
+ *                     and write their keys and values into the cache;
+ *   graft_kv_attend   attention of the slots over the cache;
+ * and after graft_verify_update has chosen a path,
+ *   graft_kv_append   with d_rows = the accepted slots: their keys and values,
+ *                     written again at contiguous places.
+ *
+ * The cache is caller-owned: one K and one V buffer a layer, in pages of
+ * page_size tokens; element (page, kv head, token in page, d) lies at
+ * page * page_stride + head * head_stride + token * token_stride + d.  Request b
+ * holds ctx_len[b] tokens in the pages page_table[b][0], page_table[b][1], ...;
+ * place `at` of the request is token at % page_size of page_table[b][at / page_size].
+ * The slots of a step take the places ctx_len[b] + slot.  All requests may
+ * share a prefix (a system prompt): prefix_len tokens in the pages
+ * d_prefix_pages[0], ..., whose last page may be part full.  A token's
+ * position is prefix_len + ctx_len[b] + its depth below the root.
+ *
+ * A graft_kv handle owns the workspace of the calls and their error word; like
+ * a graft_handle it is not thread-safe, and its work goes on one stream at a
+ * time.  One handle serves every layer of a model. */
+typedef struct graft_kv graft_kv;
+
+typedef struct {
+  int32_t q_heads;         /* query heads, a multiple of kv_heads */
+  int32_t kv_heads;        /* key and value heads */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t rot_dim;         /* leading elements of a head that rotate: even, in [0, head_dim] */
+  int32_t rot_interleaved; /* 0: element d turns with d + rot_dim / 2; 1: 2d with 2d + 1 */
+  int32_t page_size;       /* tokens of a page: 8, 16, 32, 64 or 128 */
+  int32_t num_pages;       /* pages of each cache buffer */
+  int32_t max_batch;       /* largest batch passed to graft_kv_attend */
+  int32_t max_slots;       /* largest slots passed to graft_kv_attend, in [1, 64] */
+  int32_t dtype;           /* of queries, keys, values and outputs: GRAFT_BF16 or GRAFT_F16 */
+  int64_t page_stride;     /* elements; multiples of 8, no two tokens overlapping */
+  int64_t head_stride;
+  int64_t token_stride;
+} graft_kv_config;
+
+/* Fill *cfg: whole heads rotate in halves, pages are [kv_heads][page_size][head_dim]. */
+void graft_kv_default_config(graft_kv_config* cfg, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                             int32_t page_size, int32_t num_pages, int32_t max_batch, int32_t max_slots,
+                             int32_t dtype);
+
+/* Create / free a handle on the current device.  Both synchronous. */
+int graft_kv_init(const graft_kv_config* cfg, graft_kv** out);
+int graft_kv_destroy(graft_kv* h);
+
+/* Append.  Slot i of request b takes source row r = d_rows[b][i] (NULL: i) of
+ * the request, and is skipped when r < 0 or the depth of r is negative (a
+ * pad).  Its key row b * slots + r, rotated by the angle of position
+ * prefix_len + ctx_len[b] + depth(r), and its value row go to place
+ * ctx_len[b] + i.  With d_q, the query row of every slot that is no pad is
+ * rotated by its own position into d_q_out (d_rows does not apply to
+ * queries; rows of pads are not written).
+ *   slots        any number >= 1 (a prefill passes its prompt as slots of one
+ *                request); batch * slots < 2^31
+ *   d_q, d_q_out [batch * slots] rows of q_heads * head_dim elements, or both NULL
+ *   d_k, d_v     [batch * slots] rows of kv_heads * head_dim elements
+ *                (row strides in elements: the rows may be columns of one
+ *                projection's output)
+ *   d_depth      int32 [batch][slots] or NULL (depth of slot i = i); d_tree_pos
+ *   d_rope       float [rope_len][rot_dim]: cosines of a position's rot_dim / 2
+ *                angles, then sines; NULL when rot_dim is 0
+ *   d_page_table int32 [batch][table_stride]
+ *   d_ctx_len    int32 [batch]
+ * The rotation is computed in fp32 and rounded once.  A place outside the
+ * table, a page outside the cache, a row outside the request or a position
+ * outside d_rope skips that write and sets GRAFT_ERR_RANGE.  d_q_out may be
+ * d_q at the same stride (in place).  Asynchronous; one kernel. */
+int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride, const void* d_k,
+                    int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_depth,
+                    const int32_t* d_rows, const float* d_rope, int32_t rope_len, int32_t prefix_len,
+                    const int32_t* d_page_table, int32_t table_stride, const int32_t* d_ctx_len, void* d_q_out,
+                    int64_t q_out_stride, void* d_k_cache, void* d_v_cache, void* stream);
+
+/* Attend.  The query of slot i of request b sees the prefix, the ctx_len[b]
+ * tokens before the tree and the slots j whose bit is set in
+ * d_tree_mask[b][i]; with q head h reading kv head h / (q_heads / kv_heads),
+ *   s_j = scale * q . k_j,  lse = ln sum exp(s_j),  out = sum exp(s_j - lse) v_j
+ * over the keys it sees.  A mask of 0 is a pad slot: out = 0, lse = -inf, as for
+ * any slot that sees no key.  What is not seen has no effect, NaN and
+ * infinities included (places after the last slot are never read as numbers).
+ *   slots         in [1, max_slots]
+ *   d_q, d_out    rows of q_heads * head_dim elements, row strides in elements
+ *   d_prefix_pages int32 [ceil(prefix_len / page_size)], NULL when prefix_len is 0
+ *   max_ctx       a bound on every ctx_len[b], known to the host (it sizes the
+ *                 work; max_ctx + slots <= table_stride * page_size)
+ *   d_tree_mask   uint64 [batch][slots], NULL: slot i sees slots 0 .. i
+ *   scale         finite and > 0
+ *   d_lse         float [batch * slots][q_heads], or NULL
+ * The cache buffers must start on 16-byte boundaries.  Products are exact in
+ * fp32 and summed there, as are the softmax statistics; a key's weight is
+ * rounded to the cache's type for its product with the value.  A ctx_len
+ * outside [0, max_ctx] is clamped to it, and a page outside the cache reads as
+ * zeros; both set GRAFT_ERR_RANGE.  Asynchronous; one or two kernels. */
+int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride,
+                    const void* d_k_cache, const void* d_v_cache, const int32_t* d_prefix_pages, int32_t prefix_len,
+                    const int32_t* d_page_table, int32_t table_stride, const int32_t* d_ctx_len, int32_t max_ctx,
+                    const uint64_t* d_tree_mask, float scale, void* d_out, int64_t out_stride, float* d_lse,
+                    void* stream);
+
+/* As graft_sync, graft_last_error, graft_last_launch_count and
+ * graft_set_wait_limit, for a graft_kv handle. */
+int graft_kv_sync(graft_kv* h, void* stream, uint32_t* out_flags);
+const char* graft_kv_last_error(const graft_kv* h);
+int32_t graft_kv_last_launch_count(const graft_kv* h);
+int graft_kv_set_wait_limit(graft_kv* h, uint32_t polls);
 
 #ifdef __cplusplus
 }
