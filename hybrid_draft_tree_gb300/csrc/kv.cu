@@ -13,7 +13,10 @@ struct graft_kv {
   graft_kv_config cfg;
   graft::KvLayout layout;
   int device = 0, num_sms = 0;
-  uint32_t* err = nullptr;  // [1]
+  uint32_t* err = nullptr;      // [1]
+  float* part_o = nullptr;      // [part_rows][head_dim] partial results of the attention
+  float* part_lse = nullptr;    // [part_rows]
+  int64_t part_rows = 0;
   uint32_t wait_polls = 0;
   int32_t last_launches = 0;
   char msg[256] = {0};
@@ -74,6 +77,42 @@ int check_cache(graft_kv* h, const void* k, const void* v) {
   return GRAFT_OK;
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up through the runtime (the library links no libcuda).
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A cache buffer as [page][kv head][token][d]; a copy is 64 elements of one page's tokens of one head, in rows of 128
+// bytes under the 128-byte swizzle.
+bool cache_map(const graft::KvLayout& c, int dtype, const void* base, CUtensorMap* map) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2, (cuuint64_t)c.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)c.page_size, 1, 1}, step[4] = {1, 1, 1, 1};
+  const EncodeTiled encode = encoder();
+  return encode && encode(map, dtype == GRAFT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                          const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void free_all(graft_kv* h) {
+  cudaFree(h->err);
+  cudaFree(h->part_o);
+  cudaFree(h->part_lse);
+}
+
 }  // namespace
 
 extern "C" {
@@ -112,11 +151,15 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e != cudaSuccess) { delete h; return GRAFT_ECUDA; }
+  h->part_rows = graft::kv_attend_part_rows((int64_t)cfg->max_batch * cfg->max_slots * cfg->q_heads, h->num_sms);
   e = cudaMalloc(reinterpret_cast<void**>(&h->err), 16);
-  if (e != cudaSuccess) { delete h; return GRAFT_ENOMEM; }
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_o), (size_t)h->part_rows * cfg->head_dim * 4);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_lse), (size_t)h->part_rows * 4);
+  if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ENOMEM; }
   e = cudaMemset(h->err, 0, 16);
+  if (e == cudaSuccess) e = graft::prepare_kv_attend();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) { cudaFree(h->err); delete h; return GRAFT_ECUDA; }
+  if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ECUDA; }
   *out = h;
   return GRAFT_OK;
 }
@@ -124,7 +167,7 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
 int graft_kv_destroy(graft_kv* h) {
   if (!h) return GRAFT_EINVAL;
   cudaDeviceSynchronize();
-  cudaFree(h->err);
+  free_all(h);
   delete h;
   return GRAFT_OK;
 }
@@ -204,9 +247,16 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   a.prefix_pages = d_prefix_pages; a.prefix_len = prefix_len;
   a.page_table = d_page_table; a.table_stride = table_stride; a.ctx_len = d_ctx_len; a.max_ctx = max_ctx;
   a.tree_mask = d_tree_mask; a.scale = scale; a.out = d_out; a.lse = d_lse; a.err = h->err;
-  const cudaError_t e = graft::launch_kv_attend(a, h->cfg.dtype, (cudaStream_t)stream);
+  a.q_vec = !misaligned(d_q, 16) && q_stride % 8 == 0;
+  a.out_vec = !misaligned(d_out, 16) && out_stride % 8 == 0;
+  a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms, h->part_rows);
+  a.part_o = h->part_o; a.part_lse = h->part_lse; a.wait_polls = h->wait_polls;
+  CUtensorMap kmap, vmap;
+  if (!cache_map(c, h->cfg.dtype, d_k_cache, &kmap) || !cache_map(c, h->cfg.dtype, d_v_cache, &vmap))
+    return fail(h, GRAFT_ECUDA, "the driver refused the cache's tensor map");
+  const cudaError_t e = graft::launch_kv_attend(a, kmap, vmap, h->cfg.dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_attend launch");
-  h->last_launches = 1;
+  h->last_launches = a.plan.parts > 1 ? 2 : 1;
   return GRAFT_OK;
 }
 

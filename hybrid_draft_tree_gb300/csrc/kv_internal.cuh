@@ -1,5 +1,6 @@
 // Declarations shared by the paged-cache translation units (kv.cu, kv_append.cu, kv_attend.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,6 +29,13 @@ struct AppendArgs {
   uint32_t* err;
 };
 
+// How a call's work is cut (plan_kv_attend): items_a items of packed rows against the prefix, items_b items of a
+// request's rows; key splits and 128-row tiles of either kind; partial results of a row.
+struct AttendPlan {
+  int32_t items_a, items_b, splits_a, splits_b, nt_a, nt_b, parts;
+  int64_t rows;  // query rows times query heads
+};
+
 struct AttendArgs {
   KvLayout c;
   int32_t batch, slots, group;  // group = query heads per kv head
@@ -43,6 +51,10 @@ struct AttendArgs {
   float scale;
   void* out;
   float* lse;
+  int32_t q_vec, out_vec;  // 1 = rows start on 16-byte boundaries
+  AttendPlan plan;
+  float *part_o, *part_lse;  // [parts][rows][dim], [parts][rows] (log2)
+  uint32_t wait_polls;       // 0 = the default
   uint32_t* err;
 };
 
@@ -75,6 +87,11 @@ struct Pair<__half> {
 };
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_kv_attend(const AttendArgs& a, int dtype, cudaStream_t s);
+cudaError_t prepare_kv_attend();
+int64_t kv_attend_part_rows(int64_t rows, int num_sms);
+AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
+                          int num_sms, int64_t part_rows);
+cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype,
+                             cudaStream_t s);
 
 }  // namespace graft

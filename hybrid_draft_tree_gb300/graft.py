@@ -236,8 +236,8 @@ def _table(t, name, dtype, rows):
 
 
 def _cache(t, name, dtype, cfg):
-    """Pointer to a cache buffer: a tensor whose storage, from its first
-    element on, holds every element the handle's strides reach."""
+    """Pointer to a cache buffer: a tensor whose elements reach, from the
+    first to the last, as far as the handle's strides do."""
     if t is None:
         return None
     if not hasattr(t, "data_ptr") or not hasattr(t, "is_cuda"):
@@ -246,7 +246,7 @@ def _cache(t, name, dtype, cfg):
         raise GraftError(GRAFT_EINVAL, f"{name}: dtype {t.dtype}, the handle's cache is {dtype}")
     span = ((cfg.num_pages - 1) * cfg.page_stride + (cfg.kv_heads - 1) * cfg.head_stride +
             (cfg.page_size - 1) * cfg.token_stride + cfg.head_dim)
-    held = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+    held = sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
     if held < span:
         raise GraftError(GRAFT_EINVAL, f"{name}: {held} elements, the handle's pages reach {span}")
     if not _on_device(t):
