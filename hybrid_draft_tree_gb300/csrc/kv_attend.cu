@@ -7,7 +7,8 @@
 //                    memory, running maximum and sum, weights back into it;
 //   warp 8           keys and values by tensor map, a page a copy, into a ring;
 //   warp 9           S = Q K^T and O += P V, fp32 accumulators in tensor memory;
-//   warps 10, 11     nothing: registers move between groups of four warps.
+//   warp 10          values of places that no row may see, made harmless;
+//   warp 11          nothing: registers move between groups of four warps.
 // The groups alternate so that one's products run under the other's softmax.
 // With more than 128 rows each group has its own 128 (every block's keys and
 // values serve both); with fewer both share the rows and take the key blocks in
@@ -38,7 +39,7 @@ using namespace bulk;
 constexpr int kSoftmaxThreads = 256, kThreads = 384;
 // 384 threads start with 168 registers each; the softmax groups' 256 take 216, the rest keep 72: 64512 either way
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;              // log2 of how far a maximum may run ahead of the base
@@ -52,7 +53,7 @@ struct Smem {
 };
 
 struct Bars {
-  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], drain;
+  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty, clean, drain;
   unsigned long long bad;        // slots whose value holds an element that is not finite
   uint32_t tmem;
   volatile uint32_t abort;
@@ -117,7 +118,7 @@ __device__ __forceinline__ Item decode(const AttendArgs& a) {
 
 // Keys of block j of the item: index of the first within its segment, how many are keys.
 struct Block {
-  bool prefix;
+  bool prefix, masked;  // masked: some row does not see all 128
   int base, valid;
 };
 __device__ __forceinline__ Block block_of(const AttendArgs& a, const Item& it, int j) {
@@ -126,6 +127,7 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, const Item& it, i
   k.prefix = x < it.np;
   k.base = (k.prefix ? x : x - it.np) * BN;
   k.valid = min(BN, (k.prefix ? a.prefix_len : it.ctx + a.slots) - k.base);
+  k.masked = k.prefix ? k.valid < BN : k.base + BN > it.ctx;
   return k;
 }
 
@@ -225,101 +227,105 @@ __device__ void load_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t
       mbar_wait_drain(&sh.full[x % S::kStages], (x / S::kStages) & 1);
 }
 
-// ---- warp 9: the products ---------------------------------------------------------------------------------------
-// Values that no row may see must not reach a product as NaN or infinity (0 times them is NaN): rows past the last key
-// are zeroed, and of the tree's rows (a key that some rows see and others do not) the elements that are not finite;
-// their slots are recorded, and the rows that see them add those elements at the end.
+// ---- warp 10: values that no row may see -------------------------------------------------------------------------
+// They must not reach a product as NaN or infinity (0 times them is NaN): rows past the last key are zeroed, and of the
+// tree's rows (a key that some rows see and others do not) the elements that are not finite; their slots are recorded,
+// and the rows that see them add those elements at the end.
 template <typename T, int D>
-__device__ void clean_values(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* tile, const Block& k) {
+__device__ void clean_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* ring) {
+  using S = Smem<D>;
   const int lane = threadIdx.x & 31;
-  const int tree = k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid);  // first row that is a slot
   constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-  for (int half = 0; half < Smem<D>::kHalves; ++half) {
-    uint4* p = reinterpret_cast<uint4*>(tile + half * 128 * 128);
-    for (int x = tree * 8 + lane; x < BN * 8; x += 32) {
-      const int row = x >> 3;
-      if (row >= k.valid) {
-        p[x] = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      uint4 w = p[x];
-      uint32_t* e = &w.x;
-      bool any = false;
+  uint32_t turn = 0;
+  for (int j = 0; j < it.blocks; ++j) {
+    const Block k = block_of(a, it, j);
+    if (!k.masked) continue;
+    // the issuing thread says when the block's values are there: only then is the stage's phase this block's
+    const int x = 2 * j + 1, stage = x % S::kStages;
+    bool ok = wait_bar(sh, a, &sh.dirty, turn++ & 1);
+    ok = ok && wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
+    if (!__all_sync(~0u, ok)) return;
+    const int tree = k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid);  // first row that is a slot
+    for (int half = 0; half < S::kHalves; ++half) {
+      uint4* p = reinterpret_cast<uint4*>(ring + stage * S::kTile + half * 128 * 128);
+      for (int i = tree * 8 + lane; i < BN * 8; i += 32) {
+        const int row = i >> 3;
+        if (row >= k.valid) {
+          p[i] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const uint4 v = p[i];
+        uint32_t e[4] = {v.x, v.y, v.z, v.w};
+        bool any = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if ((e[i] & kExp) == kExp) { e[i] &= 0xFFFF0000u; any = true; }
-        if (((e[i] >> 16) & kExp) == kExp) { e[i] &= 0xFFFFu; any = true; }
-      }
-      if (any) {
-        p[x] = w;
-        atomicOr(&sh.bad, 1ull << (k.base + row - it.ctx));
+        for (int c = 0; c < 4; ++c) {
+          if ((e[c] & kExp) == kExp) { e[c] &= 0xFFFF0000u; any = true; }
+          if (((e[c] >> 16) & kExp) == kExp) { e[c] &= 0xFFFFu; any = true; }
+        }
+        if (any) {
+          p[i] = make_uint4(e[0], e[1], e[2], e[3]);
+          atomicOr(&sh.bad, 1ull << (k.base + row - it.ctx));
+        }
       }
     }
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.clean);
   }
-  tc::fence_async_smem();
-  __syncwarp();
 }
 
+// ---- warp 9: the products ---------------------------------------------------------------------------------------
+// One thread issues every product: its code has no warp-wide step in it.  Products run in the order they are issued, so
+// the scores of a group's next block may follow its O += P V at once, although they overwrite P.
 template <typename T, int D>
 __device__ void mma_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* q, uint8_t* ring) {
   using S = Smem<D>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kQK = tc::instr_desc(kBf16, 128, BN, false), kPV = tc::instr_desc(kBf16, 128, D, true);
   const uint32_t tmem = sh.tmem;
-  const bool lead = (threadIdx.x & 31) == 0;
   const int units = it.blocks * it.nt;
-  bool ok = wait_bar(sh, a, &sh.q_full, 0);
+  const uint64_t qd = tc::smem_desc(smem_u32(q), 16), kd = tc::smem_desc(smem_u32(ring), 16);
+  const uint64_t vd = tc::smem_desc(smem_u32(ring), 128 * 128);
+  constexpr int kTile16 = S::kTile / 16;
   // unit u is group u & 1 on key block u >> 1 (two tiles) or u (one)
   auto qk = [&](int u) -> bool {
-    const int t = u & 1, j = it.nt == 2 ? u >> 1 : u, x = 2 * j, stage = x % S::kStages;
+    const int t = u & 1, x = it.nt == 2 ? u & ~1 : 2 * u, stage = x % S::kStages;
     if (!wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1)) return false;
     tc::fence_after();
-    if (lead) {
-      const uint64_t qa = tc::smem_desc(smem_u32(q + (it.nt == 2 ? t : 0) * S::kTile), 16);
-      const uint64_t kb = tc::smem_desc(smem_u32(ring + stage * S::kTile), 16);
+    const uint64_t qa = qd + (it.nt == 2 ? t : 0) * kTile16, kb = kd + stage * kTile16;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
-        tc::mma_ss(tmem + t * 128, qa + step, kb + step, kQK, k > 0);
-      }
-      tc::commit(&sh.s_full[t]);
-      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
+    for (int k = 0; k < D / 16; ++k) {
+      const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+      tc::mma_ss(tmem + t * 128, qa + step, kb + step, kQK, k > 0);
     }
-    __syncwarp();
+    tc::commit(&sh.s_full[t]);
+    if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
     return true;
   };
-  ok = __all_sync(~0u, ok);
-  for (int u = 0; u < 2 && u < units && ok; ++u) ok = __all_sync(~0u, qk(u));
+  bool ok = wait_bar(sh, a, &sh.q_full, 0);
+  for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
+  uint32_t cleaned = 0;
   for (int u = 0; u < units && ok; ++u) {
-    const int t = u & 1, n = u >> 1, j = it.nt == 2 ? u >> 1 : u, x = 2 * j + 1, stage = x % S::kStages;
+    const int t = u & 1, n = u >> 1, j = it.nt == 2 ? n : u, x = 2 * j + 1, stage = x % S::kStages;
     ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
-    ok = __all_sync(~0u, ok);
-    if (!ok) break;
-    if (it.nt == 1 || t == 0) {
-      const Block k = block_of(a, it, j);
-      if (k.valid < BN || (!k.prefix && k.base + k.valid > it.ctx)) clean_values<T, D>(a, it, sh, ring + stage * S::kTile, k);
+    if (ok && (it.nt == 1 || t == 0) && block_of(a, it, j).masked) {
+      mbar_arrive(&sh.dirty);
+      ok = wait_bar(sh, a, &sh.clean, cleaned++ & 1);
     }
-    ok = wait_bar(sh, a, &sh.p_full[t], n & 1);
-    ok = __all_sync(~0u, ok);
+    ok = ok && wait_bar(sh, a, &sh.p_full[t], n & 1);
     if (!ok) break;
     tc::fence_after();
-    if (lead) {
-      const uint32_t o = tmem + 256 + t * D, p = tmem + (D == 128 ? t * 128 : 384 + t * 64);
-      const uint64_t vb = tc::smem_desc(smem_u32(ring + stage * S::kTile), 128 * 128);
+    const uint32_t o = tmem + 256 + t * D, p = tmem + (D == 128 ? t * 128 : 384 + t * 64);
+    const uint64_t vb = vd + stage * kTile16;
 #pragma unroll
-      for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, n > 0 || k > 0);
-      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
-      if (u + 2 >= units) tc::commit(&sh.o_done[t]);
-    }
-    __syncwarp();
-    if (u + 2 < units) ok = __all_sync(~0u, qk(u + 2));
+    for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, n > 0 || k > 0);
+    if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
+    if (u + 2 >= units) tc::commit(&sh.o_done[t]);
+    else ok = qk(u + 2);
   }
   if (sh.abort) {  // the products in flight finish before the tensor memory goes back
-    if (lead) {
-      tc::commit(&sh.drain);
-      mbar_wait_drain(&sh.drain, 0);
-    }
-    __syncwarp();
+    tc::commit(&sh.drain);
+    mbar_wait_drain(&sh.drain, 0);
   }
 }
 
@@ -389,7 +395,7 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
       tc::wait_ld();
-      if (k.valid < BN || (!k.prefix && k.base + k.valid > it.ctx)) {
+      if (k.masked) {
         // bit c: the row sees key c of the block
         uint64_t lo, hi;
         if (k.prefix) {
@@ -576,6 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < S::kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
     mbar_init(&sh.q_full, kSoftmaxThreads);
+    mbar_init(&sh.dirty, 1);
+    mbar_init(&sh.clean, 1);
     mbar_init(&sh.drain, 1);
     sh.bad = 0;
     sh.abort = 0;
@@ -591,7 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) load_role<D>(a, it, sh, base + S::kRing, &kmap, &vmap);
-    else if (warp == kMmaWarp) mma_role<T, D>(a, it, sh, base, base + S::kRing);
+    else if (warp == kMmaWarp) {
+      if (tc::elect()) mma_role<T, D>(a, it, sh, base, base + S::kRing);
+      __syncwarp();
+    } else if (warp == kCleanWarp) clean_role<T, D>(a, it, sh, base + S::kRing);
   }
   tc::fence_before();
   __syncthreads();
