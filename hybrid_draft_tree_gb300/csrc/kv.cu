@@ -16,6 +16,7 @@ struct graft_kv {
   uint32_t* err = nullptr;      // [1]
   float* part_o = nullptr;      // [part_rows][head_dim] partial results of the attention
   float* part_lse = nullptr;    // [part_rows]
+  int64_t* line = nullptr;      // [max_batch + 1]
   int64_t part_rows = 0;
   uint32_t wait_polls = 0;
   int32_t last_launches = 0;
@@ -111,6 +112,7 @@ void free_all(graft_kv* h) {
   cudaFree(h->err);
   cudaFree(h->part_o);
   cudaFree(h->part_lse);
+  cudaFree(h->line);
 }
 
 }  // namespace
@@ -155,6 +157,7 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
   e = cudaMalloc(reinterpret_cast<void**>(&h->err), 16);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_o), (size_t)h->part_rows * cfg->head_dim * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_lse), (size_t)h->part_rows * 4);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->line), ((size_t)cfg->max_batch + 1) * 8);
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ENOMEM; }
   e = cudaMemset(h->err, 0, 16);
   if (e == cudaSuccess) e = graft::prepare_kv_attend();
@@ -249,14 +252,14 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   a.tree_mask = d_tree_mask; a.scale = scale; a.out = d_out; a.lse = d_lse; a.err = h->err;
   a.q_vec = !misaligned(d_q, 16) && q_stride % 8 == 0;
   a.out_vec = !misaligned(d_out, 16) && out_stride % 8 == 0;
-  a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms, h->part_rows);
-  a.part_o = h->part_o; a.part_lse = h->part_lse; a.wait_polls = h->wait_polls;
+  a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms);
+  a.part_o = h->part_o; a.part_lse = h->part_lse; a.line = h->line; a.wait_polls = h->wait_polls;
   CUtensorMap kmap, vmap;
   if (!cache_map(c, h->cfg.dtype, d_k_cache, &kmap) || !cache_map(c, h->cfg.dtype, d_v_cache, &vmap))
     return fail(h, GRAFT_ECUDA, "the driver refused the cache's tensor map");
   const cudaError_t e = graft::launch_kv_attend(a, kmap, vmap, h->cfg.dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_attend launch");
-  h->last_launches = a.plan.parts > 1 ? 2 : 1;
+  h->last_launches = a.plan.cut ? 2 : 1;
   return GRAFT_OK;
 }
 

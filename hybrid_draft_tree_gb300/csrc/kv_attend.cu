@@ -22,9 +22,13 @@
 // Rows of all requests against the prefix are packed into the same tiles
 // ("packed"), so a prefix block is read once for up to 256 rows, when a
 // request's own rows would leave a tile mostly empty; otherwise an item runs
-// over prefix and own context in one pass ("joined").  Items are split along
-// the keys until the SMs are full; partial results (normalised, with their
-// log-sum-exp, fp32) are joined by a second kernel.
+// over prefix and own context in one pass ("joined").
+//
+// The items lie on a line, each as long as its key blocks cost, and every CTA
+// (one an SM) takes an equal piece of the line, cut at key blocks: however
+// ragged the lengths are, the SMs end together, and the ring of keys and values
+// runs on from item to item.  What a cut item's pieces found (normalised O and
+// log-sum-exp, fp32) is joined by a second kernel, in the order of the keys.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,69 +56,122 @@ struct Smem {
   static constexpr int kRing = 2 * kTile, kBytes = kRing + kStages * kTile + 1024;  // + alignment slack
 };
 
-struct Bars {
-  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty, clean, drain;
-  unsigned long long bad;        // slots whose value holds an element that is not finite
-  uint32_t tmem;
-  volatile uint32_t abort;
-};
-
-// One work item, the same in every thread of its CTA.
+// A piece of a work item, the same in every thread of its CTA.
 struct Item {
   int head;            // kv head
   int b;               // request, -1: rows of all requests (prefix only)
   int row0, rows;      // first row, number of rows of the row space
-  int part;            // partial index, or -1: the item's rows are complete
   int nt;              // 128-row tiles: 2, or 1 shared by both groups
-  int blocks;          // key blocks
-  int first;           // first block, prefix blocks first
+  int first, blocks;   // key blocks of the piece, prefix blocks first
   int np;              // blocks below np are the prefix's
   int ctx;             // tokens of the request before the tree
+  int dest;            // where its rows' results go: the output, their item's partial, their CTA's partial
   bool bad_ctx;
 };
+constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 
-__device__ __forceinline__ Item decode(const AttendArgs& a) {
-  const AttendPlan& p = a.plan;
-  Item it{};
-  int x = blockIdx.x;
-  const int blocks_p = (a.prefix_len + BN - 1) / BN;
-  if (x < p.items_a) {
-    const int s = x % p.splits_a;
-    x /= p.splits_a;
-    it.head = x % a.c.kv_heads;
-    const int tile = x / a.c.kv_heads;
-    it.b = -1;
-    it.nt = p.nt_a;
-    it.row0 = tile * it.nt * 128;
-    it.rows = a.batch * a.slots * a.group;
-    it.np = blocks_p;
-    const int per = (blocks_p + p.splits_a - 1) / p.splits_a;
-    it.first = s * per;
-    it.blocks = max(0, min(blocks_p, it.first + per) - it.first);
-    it.part = s;
-    return it;
-  }
-  x -= p.items_a;
-  const int s = x % p.splits_b;
-  x /= p.splits_b;
-  it.head = x % a.c.kv_heads;
-  x /= a.c.kv_heads;
-  it.b = x % a.batch;
-  const int tile = x / a.batch;
-  it.nt = p.nt_b;
-  it.row0 = tile * it.nt * 128;
-  it.rows = a.slots * a.group;
-  it.ctx = a.ctx_len[it.b];
-  it.bad_ctx = it.ctx < 0 || it.ctx > a.max_ctx;
-  it.ctx = min(max(it.ctx, 0), a.max_ctx);
-  it.np = p.items_a > 0 ? 0 : blocks_p;
-  const int total = it.np + (it.ctx + a.slots + BN - 1) / BN;
-  const int per = (total + p.splits_b - 1) / p.splits_b;
-  it.first = min(total, s * per);
-  it.blocks = min(total, it.first + per) - it.first;
-  it.part = p.parts > 1 ? (p.items_a > 0 ? p.splits_a : 0) + s : -1;
-  return it;
+// The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
+// `fixed` units before its first block's.
+struct Line {
+  int64_t chunk;       // units a CTA takes
+  int64_t at;          // start of the first item of the first request on this CTA's piece
+  int b;               // that request
+};
+
+__device__ __forceinline__ int blocks_of(const AttendArgs& a, int ctx) {
+  return (a.plan.packed ? 0 : (a.prefix_len + BN - 1) / BN) + (ctx + a.slots + BN - 1) / BN;
 }
+__device__ __forceinline__ int ctx_of(const AttendArgs& a, int b) { return min(max(a.ctx_len[b], 0), a.max_ctx); }
+__device__ __forceinline__ int64_t cost_a(const AttendArgs& a) {
+  return a.plan.fixed + (int64_t)((a.prefix_len + BN - 1) / BN) * a.plan.step_a;
+}
+__device__ __forceinline__ int64_t cost_b(const AttendArgs& a, int blocks) {
+  return a.plan.fixed + (int64_t)blocks * a.plan.step_b;
+}
+
+// Walks the pieces of a CTA.
+class Pieces {
+ public:
+  __device__ Pieces(const AttendArgs& a, const Line& line) : a_(a) {
+    const int items_b = a.plan.tiles_b * a.c.kv_heads;
+    if (!a.plan.cut) {
+      lo_ = 0; hi_ = INT64_MAX; b_ = blockIdx.x / items_b; k_ = blockIdx.x % items_b; at_ = 0; in_a_ = false; single_ = true;
+      return;
+    }
+    single_ = false;
+    lo_ = blockIdx.x * line.chunk;
+    hi_ = lo_ + line.chunk;
+    const int64_t ca = cost_a(a), ta = a.plan.items_a * ca;
+    in_a_ = lo_ < ta;
+    b_ = in_a_ ? 0 : line.b;
+    k_ = 0;
+    at_ = in_a_ ? 0 : line.at;
+    if (in_a_) {
+      k_ = (int)(lo_ / ca);
+      at_ = k_ * ca;
+    } else if (b_ < a.batch) {
+      const int64_t cb = cost_b(a, blocks_of(a, ctx_of(a, b_)));
+      k_ = (int)((lo_ - at_) / cb);
+      at_ += k_ * cb;
+    }
+  }
+  // The next piece with at least one block; false at the end of the CTA's part of the line.
+  __device__ bool next(Item& it) {
+    const AttendPlan& p = a_.plan;
+    const int items_b = p.tiles_b * a_.c.kv_heads;
+    for (;;) {
+      if (in_a_ && k_ == p.items_a) { in_a_ = false; k_ = 0; b_ = 0; }
+      if (!in_a_ && k_ == items_b) { k_ = 0; ++b_; }
+      if (!in_a_ && b_ >= a_.batch) return false;
+      if (at_ + p.fixed >= hi_) return false;
+      int total;
+      const int np = (a_.prefix_len + BN - 1) / BN, step = in_a_ ? p.step_a : p.step_b;
+      it.head = k_ % a_.c.kv_heads;
+      const int tile = k_ / a_.c.kv_heads;
+      if (in_a_) {
+        it.b = -1;
+        it.nt = p.nt_a;
+        it.rows = a_.batch * a_.slots * a_.group;
+        it.ctx = 0;
+        it.bad_ctx = false;
+        it.np = total = np;
+      } else {
+        it.b = b_;
+        it.nt = p.nt_b;
+        it.rows = a_.slots * a_.group;
+        const int ctx = a_.ctx_len[b_];
+        it.ctx = min(max(ctx, 0), a_.max_ctx);
+        it.bad_ctx = ctx != it.ctx;
+        it.np = p.packed ? 0 : np;
+        total = blocks_of(a_, it.ctx);
+      }
+      it.row0 = tile * it.nt * 128;
+      const int64_t base = at_ + p.fixed;  // place of block 0
+      it.first = base >= lo_ ? 0 : (int)((lo_ - base + step - 1) / step);
+      const int end = single_ || hi_ - base >= (int64_t)total * step ? total : (int)((hi_ - base + step - 1) / step);
+      it.blocks = end - it.first;
+      it.dest = end < total ? kCtaPart : (it.first > 0 || p.packed ? kItemPart : kFinal);
+      at_ = base + (int64_t)total * step;
+      ++k_;
+      if (single_) b_ = a_.batch;  // one item, whole
+      if (it.blocks > 0) return true;
+    }
+  }
+
+ private:
+  const AttendArgs& a_;
+  int64_t lo_, hi_, at_;
+  int b_, k_;
+  bool in_a_, single_;
+};
+
+struct Bars {
+  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty, clean, drain;
+  unsigned long long bad[2];     // slots whose value holds an element that is not finite; pieces take turns
+  Line line;
+  uint32_t tmem;
+  volatile uint32_t abort;
+};
 
 // Keys of block j of the item: index of the first within its segment, how many are keys.
 struct Block {
@@ -150,6 +207,13 @@ __device__ __forceinline__ uint64_t mask_of(const AttendArgs& a, int token) {
   return slot == 63 ? ~0ull : (1ull << (slot + 1)) - 1;
 }
 
+// Row of a partial result: of item pieces that end their item, by row and head, packed items' and the others' apart;
+// of pieces whose item goes on in the next CTA, by CTA and row of the tile.
+__device__ __forceinline__ int64_t part_row(const AttendArgs& a, int dest, bool packed, int64_t at, int cta, int in_tile) {
+  if (dest == kItemPart) return (packed ? a.plan.rows : 0) + at;
+  return 2 * a.plan.rows + (int64_t)cta * 256 + in_tile;
+}
+
 // A wait that another role's abort, or the poll limit, ends; false: the item's results are void.
 __device__ __forceinline__ bool wait_bar(Bars& sh, const AttendArgs& a, unsigned long long* bar, uint32_t parity) {
   const uint32_t limit = a.wait_polls ? a.wait_polls : SPIN;
@@ -181,48 +245,52 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // ---- warp 8: keys and values into the ring ----------------------------------------------------------------------
 template <int D>
-__device__ void load_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* ring, const CUtensorMap* kmap,
-                          const CUtensorMap* vmap) {
+__device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CUtensorMap* kmap, const CUtensorMap* vmap) {
   using S = Smem<D>;
   const int lane = threadIdx.x & 31;
   const int pages = BN >> a.c.page_shift;                   // of a block; a copy is a page's half
   const int page_bytes = a.c.page_size * 128;
   int loads = 0;
-  uint32_t bad = it.bad_ctx ? GRAFT_ERR_RANGE : 0;
-  // page of this lane's copy of block j: copy lane -> half lane % kHalves of page lane / kHalves
-  auto page_of = [&](int j) -> int {
-    const Block k = block_of(a, it, j);
-    const int q = lane / S::kHalves;
-    if (q >= pages || (q << a.c.page_shift) >= k.valid) return -1;
-    const int at = (k.base >> a.c.page_shift) + q;
-    int page = k.prefix ? a.prefix_pages[at] : a.page_table[(int64_t)it.b * a.table_stride + at];
-    if (page < 0 || page >= a.c.num_pages) {                // reads as zeros
-      bad = GRAFT_ERR_RANGE;
-      page = a.c.num_pages;
-    }
-    return page;
-  };
-  int page = it.blocks > 0 ? page_of(0) : -1;
+  uint32_t bad = 0;
   bool ok = true;
-  for (int j = 0; j < it.blocks && ok; ++j) {
-    const int here = page;
-    if (j + 1 < it.blocks) page = page_of(j + 1);
-    const int copies = __popc(__ballot_sync(~0u, here >= 0));
-    for (int v = 0; v < 2 && ok; ++v) {
-      const int stage = loads % S::kStages;
-      ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
-      ok = __all_sync(~0u, ok);
-      if (!ok) break;
-      if (lane == 0) mbar_expect_tx(&sh.full[stage], copies * page_bytes);
-      __syncwarp();
-      if (here >= 0)
-        tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + (lane / S::kHalves) * page_bytes,
-                   v ? vmap : kmap, (lane % S::kHalves) * 64, 0, it.head, here, &sh.full[stage]);
-      ++loads;
+  Pieces pieces(a, sh.line);
+  Item it;
+  while (ok && pieces.next(it)) {
+    if (it.bad_ctx) bad = GRAFT_ERR_RANGE;
+    // page of this lane's copy of block j: copy lane -> half lane % kHalves of page lane / kHalves
+    auto page_of = [&](int j) -> int {
+      const Block k = block_of(a, it, j);
+      const int q = lane / S::kHalves;
+      if (q >= pages || (q << a.c.page_shift) >= k.valid) return -1;
+      const int at = (k.base >> a.c.page_shift) + q;
+      int page = k.prefix ? a.prefix_pages[at] : a.page_table[(int64_t)it.b * a.table_stride + at];
+      if (page < 0 || page >= a.c.num_pages) {                // reads as zeros
+        bad = GRAFT_ERR_RANGE;
+        page = a.c.num_pages;
+      }
+      return page;
+    };
+    int page = page_of(0);
+    for (int j = 0; j < it.blocks && ok; ++j) {
+      const int here = page;
+      if (j + 1 < it.blocks) page = page_of(j + 1);
+      const int copies = __popc(__ballot_sync(~0u, here >= 0));
+      for (int v = 0; v < 2 && ok; ++v) {
+        const int stage = loads % S::kStages;
+        ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&sh.full[stage], copies * page_bytes);
+        __syncwarp();
+        if (here >= 0)
+          tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + (lane / S::kHalves) * page_bytes,
+                     v ? vmap : kmap, (lane % S::kHalves) * 64, 0, it.head, here, &sh.full[stage]);
+        ++loads;
+      }
     }
   }
   if (bad) atomicOr(a.err, bad);
-  if (sh.abort && lane == 0)  // the copies in flight land before the CTA ends
+  if (!ok && lane == 0)  // the copies in flight land before the CTA ends
     for (int x = max(0, loads - S::kStages); x < loads; ++x)
       mbar_wait_drain(&sh.full[x % S::kStages], (x / S::kStages) & 1);
 }
@@ -232,16 +300,20 @@ __device__ void load_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t
 // tree's rows (a key that some rows see and others do not) the elements that are not finite; their slots are recorded,
 // and the rows that see them add those elements at the end.
 template <typename T, int D>
-__device__ void clean_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* ring) {
+__device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
   using S = Smem<D>;
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
   uint32_t turn = 0;
+  int before = 0, piece = 0;
+  Pieces pieces(a, sh.line);
+  Item it;
+  for (; pieces.next(it); before += it.blocks, ++piece)
   for (int j = 0; j < it.blocks; ++j) {
     const Block k = block_of(a, it, j);
     if (!k.masked) continue;
     // the issuing thread says when the block's values are there: only then is the stage's phase this block's
-    const int x = 2 * j + 1, stage = x % S::kStages;
+    const int x = 2 * (before + j) + 1, stage = x % S::kStages;
     bool ok = wait_bar(sh, a, &sh.dirty, turn++ & 1);
     ok = ok && wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
     if (!__all_sync(~0u, ok)) return;
@@ -264,7 +336,7 @@ __device__ void clean_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_
         }
         if (any) {
           p[i] = make_uint4(e[0], e[1], e[2], e[3]);
-          atomicOr(&sh.bad, 1ull << (k.base + row - it.ctx));
+          atomicOr(&sh.bad[piece & 1], 1ull << (k.base + row - it.ctx));
         }
       }
     }
@@ -278,52 +350,59 @@ __device__ void clean_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_
 // One thread issues every product: its code has no warp-wide step in it.  Products run in the order they are issued, so
 // the scores of a group's next block may follow its O += P V at once, although they overwrite P.
 template <typename T, int D>
-__device__ void mma_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* q, uint8_t* ring) {
+__device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring) {
   using S = Smem<D>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kQK = tc::instr_desc(kBf16, 128, BN, false), kPV = tc::instr_desc(kBf16, 128, D, true);
   const uint32_t tmem = sh.tmem;
-  const int units = it.blocks * it.nt;
   const uint64_t qd = tc::smem_desc(smem_u32(q), 16), kd = tc::smem_desc(smem_u32(ring), 16);
   const uint64_t vd = tc::smem_desc(smem_u32(ring), 128 * 128);
   constexpr int kTile16 = S::kTile / 16;
-  // unit u is group u & 1 on key block u >> 1 (two tiles) or u (one)
-  auto qk = [&](int u) -> bool {
-    const int t = u & 1, x = it.nt == 2 ? u & ~1 : 2 * u, stage = x % S::kStages;
-    if (!wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1)) return false;
-    tc::fence_after();
-    const uint64_t qa = qd + (it.nt == 2 ? t : 0) * kTile16, kb = kd + stage * kTile16;
+  uint32_t cleaned = 0, weights0 = 0, weights1 = 0, before = 0, piece = 0;
+  bool ok = true;
+  Pieces pieces(a, sh.line);
+  Item it;
+  for (; ok && pieces.next(it); before += it.blocks, ++piece) {
+    const int units = it.blocks * it.nt;
+    // unit u is group u & 1 on key block u >> 1 (two tiles) or u (one)
+    auto qk = [&](int u) -> bool {
+      const int t = u & 1;
+      const uint32_t x = 2 * (before + (it.nt == 2 ? u >> 1 : u)), stage = x % S::kStages;
+      if (!wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1)) return false;
+      tc::fence_after();
+      const uint64_t qa = qd + (it.nt == 2 ? t : 0) * kTile16, kb = kd + stage * kTile16;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
-      tc::mma_ss(tmem + t * 128, qa + step, kb + step, kQK, k > 0);
-    }
-    tc::commit(&sh.s_full[t]);
-    if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
-    return true;
-  };
-  bool ok = wait_bar(sh, a, &sh.q_full, 0);
-  for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
-  uint32_t cleaned = 0;
-  for (int u = 0; u < units && ok; ++u) {
-    const int t = u & 1, n = u >> 1, j = it.nt == 2 ? n : u, x = 2 * j + 1, stage = x % S::kStages;
-    ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
-    if (ok && (it.nt == 1 || t == 0) && block_of(a, it, j).masked) {
-      mbar_arrive(&sh.dirty);
-      ok = wait_bar(sh, a, &sh.clean, cleaned++ & 1);
-    }
-    ok = ok && wait_bar(sh, a, &sh.p_full[t], n & 1);
-    if (!ok) break;
-    tc::fence_after();
-    const uint32_t o = tmem + 256 + t * D, p = tmem + (D == 128 ? t * 128 : 384 + t * 64);
-    const uint64_t vb = vd + stage * kTile16;
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
+        tc::mma_ss(tmem + t * 128, qa + step, kb + step, kQK, k > 0);
+      }
+      tc::commit(&sh.s_full[t]);
+      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
+      return true;
+    };
+    ok = wait_bar(sh, a, &sh.q_full, piece & 1);
+    for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
+    for (int u = 0; u < units && ok; ++u) {
+      const int t = u & 1, j = it.nt == 2 ? u >> 1 : u;
+      const uint32_t x = 2 * (before + j) + 1, stage = x % S::kStages;
+      ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
+      if (ok && (it.nt == 1 || t == 0) && block_of(a, it, j).masked) {
+        mbar_arrive(&sh.dirty);
+        ok = wait_bar(sh, a, &sh.clean, cleaned++ & 1);
+      }
+      ok = ok && wait_bar(sh, a, &sh.p_full[t], (t ? weights1++ : weights0++) & 1);
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t o = tmem + 256 + t * D, p = tmem + (D == 128 ? t * 128 : 384 + t * 64);
+      const uint64_t vb = vd + stage * kTile16;
 #pragma unroll
-    for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, n > 0 || k > 0);
-    if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
-    if (u + 2 >= units) tc::commit(&sh.o_done[t]);
-    else ok = qk(u + 2);
+      for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, u > 1 || k > 0);
+      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
+      if (u + 2 >= units) tc::commit(&sh.o_done[t]);
+      else ok = qk(u + 2);
+    }
   }
-  if (sh.abort) {  // the products in flight finish before the tensor memory goes back
+  if (!ok) {  // the products in flight finish before the tensor memory goes back
     tc::commit(&sh.drain);
     mbar_wait_drain(&sh.drain, 0);
   }
@@ -331,30 +410,38 @@ __device__ void mma_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t*
 
 // ---- warps 0-7: softmax and results -----------------------------------------------------------------------------
 template <typename T, int D>
-__device__ void store_row(const AttendArgs& a, const Item& it, const Row& row, float lse2, const float* o, int c0, int n) {
-  if (it.part >= 0) {
-    float* dst = a.part_o + ((int64_t)it.part * a.plan.rows + (int64_t)row.token * a.c.q_heads + row.head) * D + c0;
-    for (int c = 0; c < n; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Item& it, const Row& row, int in_tile, const float* o,
+                                          int c0) {
+  if (it.dest != kFinal) {
+    const int64_t at = part_row(a, it.dest, it.b < 0, (int64_t)row.token * a.c.q_heads + row.head, blockIdx.x, in_tile);
+    float* dst = a.part_o + at * D + c0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
     return;
   }
   T* dst = static_cast<T*>(a.out) + row.token * a.out_stride + row.head * D + c0;
   if (a.out_vec) {
 #pragma unroll
-    for (int c = 0; c < n; c += 8)
+    for (int c = 0; c < 32; c += 8)
       *reinterpret_cast<uint4*>(dst + c) = make_uint4(Pair<T>::put(o[c], o[c + 1]), Pair<T>::put(o[c + 2], o[c + 3]),
                                                       Pair<T>::put(o[c + 4], o[c + 5]), Pair<T>::put(o[c + 6], o[c + 7]));
   } else {
 #pragma unroll
-    for (int c = 0; c < n; ++c) dst[c] = Pair<T>::round(o[c]);
+    for (int c = 0; c < 32; ++c) dst[c] = Pair<T>::round(o[c]);
   }
 }
 
 template <typename T, int D>
-__device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint8_t* q) {
+__device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   using S = Smem<D>;
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
   const uint32_t tmem = sh.tmem + lanes;
+  const float scale = a.scale * kLog2e;
+  uint32_t scores = 0, results = 0, piece = 0;
+  Pieces pieces(a, sh.line);
+  Item it;
+  for (; pieces.next(it); ++piece) {
   // queries into shared memory, 16 bytes a thread, in the swizzled order the products read
   for (int x = tid; x < it.nt * 128 * (D / 8); x += kSoftmaxThreads) {
     const int r = x / (D / 8), c = x % (D / 8);
@@ -373,6 +460,7 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
     *reinterpret_cast<uint4*>(dst) = w;
   }
   tc::fence_async_smem();
+  tc::fence_before();
   mbar_arrive(&sh.q_full);
 
   const int r = it.row0 + (it.nt == 2 ? t * 128 : 0) + lane_row;
@@ -380,21 +468,20 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
   const Row row = live ? row_of(a, it, r) : Row{0, 0};
   const uint64_t mask = live ? mask_of(a, row.token) : 0;
   const bool warp_live = __any_sync(~0u, live);
-  const float scale = a.scale * kLog2e;
   const int units = it.nt == 2 ? it.blocks : (it.blocks + 1 - t) >> 1;
   float m = -INFINITY;
   float2 l2 = make_float2(0.f, 0.f);
   bool ok = true;
   for (int n = 0; n < units && ok; ++n) {
     const Block k = block_of(a, it, it.nt == 2 ? n : 2 * n + t);
-    ok = __all_sync(~0u, wait_bar(sh, a, &sh.s_full[t], n & 1));
+    ok = __all_sync(~0u, wait_bar(sh, a, &sh.s_full[t], scores++ & 1));
     if (!ok) break;
     tc::fence_after();
     if (warp_live) {
       uint32_t s[BN];
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
-      tc::wait_ld();
+      tc::wait_ld<BN>(s);
       if (k.masked) {
         // bit c: the row sees key c of the block
         uint64_t lo, hi;
@@ -440,7 +527,7 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             tc::ld32(tmem + 256 + t * D + c, o);
-            tc::wait_ld();
+            tc::wait_ld<32>(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tc::st32(tmem + 256 + t * D + c, o);
@@ -474,78 +561,59 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
     __syncwarp();
     if ((tid & 31) == 0) mbar_arrive(&sh.p_full[t]);
   }
-  if (units > 0 && ok) ok = __all_sync(~0u, wait_bar(sh, a, &sh.o_done[t], 0));
-  tc::fence_after();
+  if (units > 0 && ok) ok = __all_sync(~0u, wait_bar(sh, a, &sh.o_done[t], results++ & 1));
   float l = l2.x + l2.y;
-  const uint64_t bad = sh.bad;
-  float* joint = reinterpret_cast<float*>(q);       // the queries' space, free once every product is done
-  if (it.nt == 1) {
-    // group 1 hands its maximum, sum and O over; both groups' products are done before the space is written, and both
-    // take one decision when a wait has run out
-    int all_ok;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}"
-        : "=r"(all_ok) : "r"((int)ok) : "memory");
-    if (!all_ok) return;
-    float* ml = joint + 128 * D;
-    if (t == 1) {
-      ml[lane_row] = m;
-      ml[128 + lane_row] = l;
-      if (warp_live && units > 0) {
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc::ld32(tmem + 256 + D + c, o);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(joint + ((c + i) / 4 * 128 + lane_row) * 4) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        }
-      }
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (t == 1) return;
-  } else if (!ok) {
-    return;
+  const bool two = it.nt == 1 && it.blocks > 1;      // two sums of one row to join
+  // of a shared tile each group leaves its maximum and sum where its scores were
+  if (it.nt == 1 && units > 0 && ok) {
+    tc::fence_after();
+    tc::st2(tmem + t * 128, m, l);
+    tc::fence_before();
   }
-  if (!warp_live) return;
+  // both groups' products are done, so the queries' space is free; and both take one decision when a wait has run out
+  int all_ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(all_ok) : "r"((int)ok) : "memory");
+  if (!all_ok) return;
+  tc::fence_after();
+  if (tid == 0) sh.bad[(piece + 1) & 1] = 0;         // everybody has read the piece before this one's
+  if (!warp_live) continue;
+  const uint64_t bad = sh.bad[piece & 1];
   float f0 = 1.f, f1 = 0.f;
-  bool other = false;
-  if (it.nt == 1) {
-    const float* ml = joint + 128 * D;
-    const float m1 = ml[lane_row], l1 = ml[128 + lane_row];
-    other = it.blocks > 1;
-    const float both = fmaxf(m, m1);
-    if (both != -INFINITY) {
-      f0 = ex2(m - both);
-      f1 = ex2(m1 - both);
+  if (it.nt == 1) tc::ld2(tmem, m, l);
+  if (two) {
+    const float m0 = m;
+    float m1, l1;
+    tc::ld2(tmem + 128, m1, l1);
+    m = fmaxf(m0, m1);
+    if (m != -INFINITY) {
+      f0 = ex2(m0 - m);
+      f1 = ex2(m1 - m);
     }
-    l = l * f0 + (other ? l1 * f1 : 0.f);
-    m = both;
+    l = l * f0 + l1 * f1;
   }
-  const bool none = mask == 0 || l == 0.f;           // a pad, or a row that sees no key of the item (NaN is not none)
+  const bool none = mask == 0 || l == 0.f;           // a pad, or a row that sees no key of the piece (NaN is not none)
   const float inv = none ? 0.f : 1.f / l;
-  const float lse2 = none ? -INFINITY : m + log2f(l);
-#pragma unroll
-  for (int c = 0; c < D; c += 32) {
+  f0 *= inv;
+  f1 *= inv;
+  // of a shared tile each group writes half of the columns
+  const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
+  const uint32_t o_at = tmem + 256 + (it.nt == 1 ? 0 : t * D);
+  for (int c = c_begin; c < c_end; c += 32) {
     uint32_t o[32];
-    if (units > 0) {
-      tc::ld32(tmem + 256 + t * D + c, o);
-      tc::wait_ld();
-    }
     float f[32];
+    tc::ld32(o_at + c, o);
+    tc::wait_ld<32>(o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = units > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
-    if (other) {
+    for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : __uint_as_float(o[i]) * f0;
+    if (two) {
+      tc::ld32(o_at + D + c, o);
+      tc::wait_ld<32>(o);
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(joint + ((c + i) / 4 * 128 + lane_row) * 4);
-        f[i] += v.x * f1; f[i + 1] += v.y * f1; f[i + 2] += v.z * f1; f[i + 3] += v.w * f1;
-      }
+      for (int i = 0; i < 32; ++i) f[i] += none ? 0.f : __uint_as_float(o[i]) * f1;
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : f[i] * inv;
-    if (bad && it.b >= 0) {
+    if (bad & mask) {
       for (uint64_t w = bad & mask; w; w &= w - 1) {
         const int at = it.ctx + __ffsll((long long)w) - 1;
         const int page = a.page_table[(int64_t)it.b * a.table_stride + (at >> a.c.page_shift)];
@@ -558,12 +626,55 @@ __device__ void softmax_role(const AttendArgs& a, const Item& it, Bars& sh, uint
         }
       }
     }
-    if (live) store_row<T, D>(a, it, row, lse2, f, c, 32);
+    if (live) store_row<T, D>(a, it, row, r - it.row0, f, c);
   }
-  if (live) {
+  if (live && (it.nt == 2 || t == 0)) {
+    const float lse2 = none ? -INFINITY : m + log2f(l);
     const int64_t at = (int64_t)row.token * a.c.q_heads + row.head;
-    if (it.part >= 0) a.part_lse[(int64_t)it.part * a.plan.rows + at] = lse2;
+    if (it.dest != kFinal) a.part_lse[part_row(a, it.dest, it.b < 0, at, blockIdx.x, r - it.row0)] = lse2;
     else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
+  }
+  }
+}
+
+// Where this CTA's piece of the line begins; block 0 leaves the requests' places to the join.
+__device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int per = (a.batch + kThreads - 1) / kThreads, b0 = min(a.batch, t * per), b1 = min(a.batch, b0 + per);
+  const int items = a.plan.tiles_b * a.c.kv_heads;
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += items * cost_b(a, blocks_of(a, ctx_of(a, b)));
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  const int64_t ta = a.plan.items_a * cost_a(a);
+  int64_t start = ta + upto - sum, total = ta;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) start += sums[w];
+    total += sums[w];
+  }
+  // at least a block's length, so that every CTA between the first and the last of an item holds a piece of it
+  const int64_t chunk = max((total + gridDim.x - 1) / gridDim.x, (int64_t)max(a.plan.step_a, a.plan.step_b));
+  const int64_t lo = blockIdx.x * chunk;
+  if (t == 0) {
+    sh.line.chunk = chunk;
+    if (lo >= total) { sh.line.b = a.batch; sh.line.at = total; }
+    if (blockIdx.x == 0) a.line[a.batch] = chunk;
+  }
+  const bool here = lo >= ta && lo >= start && lo < start + sum;
+  if (here || blockIdx.x == 0) {
+    int64_t at = start;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t c = items * cost_b(a, blocks_of(a, ctx_of(a, b)));
+      if (here && lo >= at && lo < at + c) { sh.line.b = b; sh.line.at = at; }
+      if (blockIdx.x == 0) a.line[b] = at;
+      at += c;
+    }
   }
 }
 
@@ -576,7 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars sh;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5;
-  const Item it = decode(a);
   grid_dependents_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
@@ -585,24 +695,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.dirty, 1);
     mbar_init(&sh.clean, 1);
     mbar_init(&sh.drain, 1);
-    sh.bad = 0;
+    sh.bad[0] = 0;
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sh.tmem, 512);
+  if (a.plan.cut) find_line(a, sh, reinterpret_cast<int64_t*>(base));
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (warp < kTmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<T, D>(a, it, sh, base);
+    softmax_role<T, D>(a, sh, base);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kTmaWarp) load_role<D>(a, it, sh, base + S::kRing, &kmap, &vmap);
+    if (warp == kTmaWarp) load_role<D>(a, sh, base + S::kRing, &kmap, &vmap);
     else if (warp == kMmaWarp) {
-      if (tc::elect()) mma_role<T, D>(a, it, sh, base, base + S::kRing);
+      if (tc::elect()) mma_role<T, D>(a, sh, base, base + S::kRing);
       __syncwarp();
-    } else if (warp == kCleanWarp) clean_role<T, D>(a, it, sh, base + S::kRing);
+    } else if (warp == kCleanWarp) clean_role<T, D>(a, sh, base + S::kRing);
   }
   tc::fence_before();
   __syncthreads();
@@ -610,49 +721,86 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 
-// Joins the partial results of a row and head: a warp each.
+// Joins the partial results of a row and head, in the order of their keys: a warp each.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ AttendArgs a) {
   constexpr int N = D / 32;
+  const AttendPlan& p = a.plan;
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
-  if (at >= a.plan.rows) return;
-  const int64_t token = at / a.c.q_heads;
-  const int head = (int)(at - token * a.c.q_heads);
+  if (at >= p.rows) return;
+  const int token = (int)(at / a.c.q_heads), head = (int)(at - (int64_t)token * a.c.q_heads);
+  const int b = token / a.slots, kv_head = head / a.group;
+  const int64_t chunk = a.line[a.batch];
+  // the CTAs that hold pieces of the row's item(s): the last one's is the item's partial, the others' are by CTA
+  const int in_b = (token - b * a.slots) * a.group + head - kv_head * a.group;
+  const int tile_b = in_b / (p.nt_b * 128);
+  const int blocks = blocks_of(a, ctx_of(a, b));
+  const int64_t start_b = a.line[b] + (tile_b * a.c.kv_heads + kv_head) * cost_b(a, blocks) + p.fixed;
+  const int b_first = (int)(start_b / chunk), b_last = (int)((start_b + (int64_t)(blocks - 1) * p.step_b) / chunk);
+  int a_first = 0, a_last = -1, in_a = 0;
+  if (p.packed) {
+    in_a = b * a.slots * a.group + in_b;
+    const int tile_a = in_a / (p.nt_a * 128), np = (a.prefix_len + BN - 1) / BN;
+    const int64_t start = (tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
+    a_first = (int)(start / chunk);
+    a_last = (int)((start + (int64_t)(np - 1) * p.step_a) / chunk);
+    in_a -= tile_a * p.nt_a * 128;
+  } else if (b_first == b_last) {
+    return;  // whole, and written
+  }
+  const int na = a_last - a_first + 1, n = na + b_last - b_first + 1;
+  auto place = [&](int i) -> int64_t {
+    const bool of_a = i < na;
+    const int cta = of_a ? a_first + i : b_first + i - na;
+    const bool last = cta == (of_a ? a_last : b_last);
+    return part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : in_b - tile_b * p.nt_b * 128);
+  };
   float top = -INFINITY;
-  for (int p = lane; p < a.plan.parts; p += 32) top = fmaxf(top, a.part_lse[(int64_t)p * a.plan.rows + at]);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_lse[place(i)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  // fmaxf drops a NaN: the sum keeps it
+  const float base = top == -INFINITY ? 0.f : top;  // fmaxf drops a NaN: the sum keeps it
   float sum = 0.f, acc[N] = {};
-  for (int p = 0; p < a.plan.parts; ++p) {
-    const float z = a.part_lse[(int64_t)p * a.plan.rows + at];
-    const float w = z == -INFINITY ? 0.f : ex2(z - (top == -INFINITY ? 0.f : top));
-    sum += w;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const int64_t r = place(i);
+    const float z = a.part_lse[r];
+    const float* o = a.part_o + r * D + lane * N;
+    float v[N];
+    if constexpr (N == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(o);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(o);
+      v[0] = x.x; v[1] = x.y;
+    }
     if (z != -INFINITY) {
-      const float* o = a.part_o + ((int64_t)p * a.plan.rows + at) * D + lane * N;
-      if (N == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] += w * v.x; acc[1] += w * v.y; acc[N - 2] += w * v.z; acc[N - 1] += w * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] += w * v.x; acc[1] += w * v.y;
-      }
+      const float w = ex2(z - base);
+      sum += w;
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] += w * v[c];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * N;
+  if (a.out_vec) {
+    const uint32_t w0 = Pair<T>::put(acc[0] * inv, acc[1] * inv);
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w0, Pair<T>::put(acc[2] * inv, acc[3] * inv));
+    else *reinterpret_cast<uint32_t*>(out) = w0;
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) out[i] = Pair<T>::round(acc[i] * inv);
+    for (int i = 0; i < N; ++i) out[i] = Pair<T>::round(acc[i] * inv);
+  }
   if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  k_kv_attend<T, D><<<a.plan.items_a + a.plan.items_b, kThreads, Smem<D>::kBytes, s>>>(a, kmap, vmap);
+  k_kv_attend<T, D><<<a.plan.ctas, kThreads, Smem<D>::kBytes, s>>>(a, kmap, vmap);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.plan.parts > 1)
+  if (e == cudaSuccess && a.plan.cut)
     e = launch_dependent(k_kv_join<T, D>, dim3((unsigned)((a.plan.rows + 7) / 8)), dim3(256), 0, s, a);
   return e;
 }
@@ -672,53 +820,50 @@ cudaError_t prepare_kv_attend() {
   return e;
 }
 
-int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 3 * rows + 2LL * num_sms * 256; }
+int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int64_t)num_sms * 256; }
 
-// Chooses tiles and splits from the sizes alone.  Times in units of a 128 x 128
-// tile of scores and its two products: a group pair works through two tiles of
-// a block in 2 units, one tile shared in 1; a block that no other item reads
-// costs at least its 64 KB (D = 128) at the SM's share of the memory's rate,
-// about 3 units; an item costs about 10 units before and after its blocks, the
-// join of partial results about 6 and their bytes.
+// Chooses between packed and joined items, and between cut and whole ones, from the sizes alone.  Costs are in
+// nanoseconds, measured on one SM: a key block of 128 against two tiles of 128 rows, against one, and the least a block
+// takes when its keys and values come from memory (the SM's share of the copy rate) or from L2, where other items' SMs
+// read them too; before its first block an item pays for its queries, and the pipeline's start and end.
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
-                          int num_sms, int64_t part_rows) {
+                          int num_sms) {
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
+  const int two = dim == 128 ? 1600 : 1000, one = dim == 128 ? 850 : 550;
+  const int memory = dim == 128 ? 1450 : 725, l2 = dim == 128 ? 600 : 300;
   AttendPlan best{};
   double best_t = 0;
   for (int packed = 0; packed < 2; ++packed) {
     if (packed && (np == 0 || batch == 1)) break;
     AttendPlan p{};
+    p.packed = packed;
+    p.fixed = 2500;
     p.rows = all * kv_heads;
     p.nt_a = all > 128 ? 2 : 1;
     p.nt_b = R > 128 ? 2 : 1;
-    const int64_t tiles_a = (all + 128 * p.nt_a - 1) / (128 * p.nt_a), tiles_b = (R + 128 * p.nt_b - 1) / (128 * p.nt_b);
-    const int nb = packed ? no : np + no;
-    const double fill = (double)dim / 128;
-    const double step_a = p.nt_a, step_b = p.nt_b > 3 * fill ? p.nt_b : (packed || np == 0 ? 3 * fill : std::max<double>(p.nt_b, 1.5 * fill));
-    const int most = std::max(packed ? np : 0, nb);
-    for (int len = most, last_a = 0, last_b = 0; len >= 1; len = len > 64 ? len * 15 / 16 : len - 1) {
-      p.splits_a = packed ? (np + len - 1) / len : 0;
-      p.splits_b = (nb + len - 1) / len;
-      if (p.splits_a == last_a && p.splits_b == last_b) continue;
-      last_a = p.splits_a;
-      last_b = p.splits_b;
-      p.parts = p.splits_a + p.splits_b;
-      if (p.parts > 1 && p.parts * p.rows > part_rows) break;
-      const int64_t ia = packed ? tiles_a * kv_heads * p.splits_a : 0, ib = batch * tiles_b * kv_heads * p.splits_b;
-      if (ia + ib > 0x7FFFFFFF) break;
-      p.items_a = (int)ia;
-      p.items_b = (int)ib;
-      const double da = packed ? 10 + step_a * ((np + p.splits_a - 1) / p.splits_a) : 0;
-      const double db = 10 + step_b * ((nb + p.splits_b - 1) / p.splits_b);
-      double t;
-      if (packed) t = std::max(std::max(da, db), (ia * da + ib * db) / num_sms + 0.5 * std::min(da, db));
-      else t = (double)((ib + num_sms - 1) / num_sms) * db;
-      if (p.parts > 1) t += 6 + (double)p.parts * p.rows * dim * 8 / 2.0e6;
-      if (best_t == 0 || t < best_t) {
-        best_t = t;
-        best = p;
-      }
+    p.tiles_b = (int)((R + 128 * p.nt_b - 1) / (128 * p.nt_b));
+    p.items_a = packed ? (int)((all + 128 * p.nt_a - 1) / (128 * p.nt_a)) * kv_heads : 0;
+    p.step_a = std::max(p.nt_a == 2 ? two : one, l2);
+    // the share of an item's blocks that no other item reads
+    const int blocks = packed ? no : np + no;
+    const double alone = packed || batch == 1 ? 1.0 : (double)no / blocks;
+    p.step_b = std::max(p.nt_b == 2 ? two : one, (int)(p.tiles_b > 1 ? l2 : l2 + alone * (memory - l2)));
+    const int64_t items_b = (int64_t)batch * p.tiles_b * kv_heads;
+    const double whole = p.fixed + (double)blocks * p.step_b;
+    const double work = p.items_a * (p.fixed + (double)np * p.step_a) + items_b * whole;
+    const double join = 3500 + (double)(p.rows * (packed ? 2 : 1) + num_sms * 256) * dim * 8 / 5000;
+    double t = work / num_sms + p.fixed + join;
+    p.cut = 1;
+    p.ctas = num_sms;
+    if (!packed && items_b <= num_sms && whole <= t) {
+      p.cut = 0;
+      p.ctas = (int)items_b;
+      t = whole;
+    }
+    if (best_t == 0 || t < best_t) {
+      best_t = t;
+      best = p;
     }
   }
   return best;

@@ -29,11 +29,15 @@ struct AppendArgs {
   uint32_t* err;
 };
 
-// How a call's work is cut (plan_kv_attend): items_a items of packed rows against the prefix, items_b items of a
-// request's rows; key splits and 128-row tiles of either kind; partial results of a row.
+// How a call's work is laid out (plan_kv_attend): packed items' rows of all requests against the prefix, then each
+// request's rows against its own context (and, when none are packed, the prefix).
 struct AttendPlan {
-  int32_t items_a, items_b, splits_a, splits_b, nt_a, nt_b, parts;
-  int64_t rows;  // query rows times query heads
+  int32_t packed, cut;       // cut: CTAs take equal pieces of the line of items; else an item each
+  int32_t ctas, items_a;     // items_a: packed items
+  int32_t tiles_b;           // row tiles of a request and head
+  int32_t nt_a, nt_b;        // 128-row tiles of an item
+  int32_t fixed, step_a, step_b;  // cost of an item before its first block, and of a block
+  int64_t rows;              // query rows times query heads
 };
 
 struct AttendArgs {
@@ -53,7 +57,8 @@ struct AttendArgs {
   float* lse;
   int32_t q_vec, out_vec;  // 1 = rows start on 16-byte boundaries
   AttendPlan plan;
-  float *part_o, *part_lse;  // [parts][rows][dim], [parts][rows] (log2)
+  float *part_o, *part_lse;  // partial results (rows of dim) and their log-sum-exp in log2
+  int64_t* line;             // [batch] starts of the requests' items, [batch] = a CTA's share
   uint32_t wait_polls;       // 0 = the default
   uint32_t* err;
 };
@@ -90,7 +95,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t prepare_kv_attend();
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
-                          int num_sms, int64_t part_rows);
+                          int num_sms);
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype,
                              cudaStream_t s);
 
