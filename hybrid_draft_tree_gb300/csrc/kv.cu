@@ -16,7 +16,7 @@ struct graft_kv {
   uint32_t* err = nullptr;      // [1]
   float* part_o = nullptr;      // [part_rows][head_dim] partial results of the attention
   float* part_lse = nullptr;    // [part_rows]
-  int64_t* line = nullptr;      // [max_batch + 1]
+  int64_t* line = nullptr;      // [max_batch + 1 + SMs]
   int64_t part_rows = 0;
   uint32_t wait_polls = 0;
   int32_t last_launches = 0;
@@ -157,7 +157,7 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
   e = cudaMalloc(reinterpret_cast<void**>(&h->err), 16);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_o), (size_t)h->part_rows * cfg->head_dim * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part_lse), (size_t)h->part_rows * 4);
-  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->line), ((size_t)cfg->max_batch + 1) * 8);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->line), ((size_t)cfg->max_batch + 1 + h->num_sms) * 8);
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ENOMEM; }
   e = cudaMemset(h->err, 0, 16);
   if (e == cudaSuccess) e = graft::prepare_kv_attend();

@@ -7,8 +7,7 @@
 //                    memory, running maximum and sum, weights back into it;
 //   warp 8           keys and values by tensor map, a page a copy, into a ring;
 //   warp 9           S = Q K^T and O += P V, fp32 accumulators in tensor memory;
-//   warp 10          values of places that no row may see, made harmless;
-//   warp 11          nothing: registers move between groups of four warps.
+//   warps 10, 11     values of places that no row may see, made harmless.
 // The groups alternate so that one's products run under the other's softmax.
 // With more than 128 rows each group has its own 128 (every block's keys and
 // values serve both); with fewer both share the rows and take the key blocks in
@@ -71,103 +70,78 @@ struct Item {
 constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 
 // The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
-// `fixed` units before its first block's.
+// `fixed` units before its first block's.  An item is shorter than 2^32 units (its key blocks are below 2^24).
 struct Line {
-  int64_t chunk;       // units a CTA takes
-  int64_t at;          // start of the first item of the first request on this CTA's piece
-  int b;               // that request
+  int64_t lo, hi;      // this CTA's part
+  int64_t at;          // start of its first item
+  int b, k;            // that item: request (-1: packed) and index within its request (or among the packed)
 };
 
 __device__ __forceinline__ int blocks_of(const AttendArgs& a, int ctx) {
   return (a.plan.packed ? 0 : (a.prefix_len + BN - 1) / BN) + (ctx + a.slots + BN - 1) / BN;
 }
 __device__ __forceinline__ int ctx_of(const AttendArgs& a, int b) { return min(max(a.ctx_len[b], 0), a.max_ctx); }
-__device__ __forceinline__ int64_t cost_a(const AttendArgs& a) {
-  return a.plan.fixed + (int64_t)((a.prefix_len + BN - 1) / BN) * a.plan.step_a;
+__device__ __forceinline__ uint32_t cost_a(const AttendArgs& a) {
+  return a.plan.fixed + (uint32_t)((a.prefix_len + BN - 1) / BN) * a.plan.step_a;
 }
-__device__ __forceinline__ int64_t cost_b(const AttendArgs& a, int blocks) {
-  return a.plan.fixed + (int64_t)blocks * a.plan.step_b;
+__device__ __forceinline__ uint32_t cost_b(const AttendArgs& a, int blocks) {
+  return a.plan.fixed + (uint32_t)blocks * a.plan.step_b;
 }
 
 // Walks the pieces of a CTA.
 class Pieces {
  public:
-  __device__ Pieces(const AttendArgs& a, const Line& line) : a_(a) {
-    const int items_b = a.plan.tiles_b * a.c.kv_heads;
-    if (!a.plan.cut) {
-      lo_ = 0; hi_ = INT64_MAX; b_ = blockIdx.x / items_b; k_ = blockIdx.x % items_b; at_ = 0; in_a_ = false; single_ = true;
-      return;
-    }
-    single_ = false;
-    lo_ = blockIdx.x * line.chunk;
-    hi_ = lo_ + line.chunk;
-    const int64_t ca = cost_a(a), ta = a.plan.items_a * ca;
-    in_a_ = lo_ < ta;
-    b_ = in_a_ ? 0 : line.b;
-    k_ = 0;
-    at_ = in_a_ ? 0 : line.at;
-    if (in_a_) {
-      k_ = (int)(lo_ / ca);
-      at_ = k_ * ca;
-    } else if (b_ < a.batch) {
-      const int64_t cb = cost_b(a, blocks_of(a, ctx_of(a, b_)));
-      k_ = (int)((lo_ - at_) / cb);
-      at_ += k_ * cb;
-    }
-  }
+  __device__ Pieces(const AttendArgs& a, const Line& line) : a_(a), line_(line), at_(line.at), b_(line.b), k_(line.k) {}
   // The next piece with at least one block; false at the end of the CTA's part of the line.
   __device__ bool next(Item& it) {
     const AttendPlan& p = a_.plan;
-    const int items_b = p.tiles_b * a_.c.kv_heads;
     for (;;) {
-      if (in_a_ && k_ == p.items_a) { in_a_ = false; k_ = 0; b_ = 0; }
-      if (!in_a_ && k_ == items_b) { k_ = 0; ++b_; }
-      if (!in_a_ && b_ >= a_.batch) return false;
-      if (at_ + p.fixed >= hi_) return false;
-      int total;
-      const int np = (a_.prefix_len + BN - 1) / BN, step = in_a_ ? p.step_a : p.step_b;
-      it.head = k_ % a_.c.kv_heads;
-      const int tile = k_ / a_.c.kv_heads;
-      if (in_a_) {
-        it.b = -1;
-        it.nt = p.nt_a;
-        it.rows = a_.batch * a_.slots * a_.group;
-        it.ctx = 0;
-        it.bad_ctx = false;
-        it.np = total = np;
-      } else {
-        it.b = b_;
-        it.nt = p.nt_b;
-        it.rows = a_.slots * a_.group;
+      if (k_ == (b_ < 0 ? p.items_a : p.tiles_b * a_.c.kv_heads)) {
+        k_ = 0;
+        ++b_;
+      }
+      if (b_ >= a_.batch || (!p.cut && at_ > 0)) return false;
+      const int64_t base = at_ + p.fixed, hi = line_.hi, lo = line_.lo;  // base: place of block 0
+      if (base >= hi) return false;
+      const int np = (a_.prefix_len + BN - 1) / BN;
+      const bool of_a = b_ < 0;
+      int total = np;
+      it.b = b_;
+      it.np = of_a || !p.packed ? np : 0;
+      it.ctx = 0;
+      it.bad_ctx = false;
+      if (!of_a) {
         const int ctx = a_.ctx_len[b_];
         it.ctx = min(max(ctx, 0), a_.max_ctx);
         it.bad_ctx = ctx != it.ctx;
-        it.np = p.packed ? 0 : np;
         total = blocks_of(a_, it.ctx);
       }
+      it.nt = of_a ? p.nt_a : p.nt_b;
+      it.rows = (of_a ? a_.batch : 1) * a_.slots * a_.group;
+      const int tile = k_ / a_.c.kv_heads;
+      it.head = k_ - tile * a_.c.kv_heads;
       it.row0 = tile * it.nt * 128;
-      const int64_t base = at_ + p.fixed;  // place of block 0
-      it.first = base >= lo_ ? 0 : (int)((lo_ - base + step - 1) / step);
-      const int end = single_ || hi_ - base >= (int64_t)total * step ? total : (int)((hi_ - base + step - 1) / step);
+      const uint32_t step = of_a ? p.step_a : p.step_b, length = total * step;
+      it.first = base >= lo ? 0 : (int)(((uint32_t)(lo - base) + step - 1) / step);
+      const int end = hi - base >= length ? total : (int)(((uint32_t)(hi - base) + step - 1) / step);
       it.blocks = end - it.first;
       it.dest = end < total ? kCtaPart : (it.first > 0 || p.packed ? kItemPart : kFinal);
-      at_ = base + (int64_t)total * step;
+      at_ = base + length;
       ++k_;
-      if (single_) b_ = a_.batch;  // one item, whole
       if (it.blocks > 0) return true;
     }
   }
 
  private:
   const AttendArgs& a_;
-  int64_t lo_, hi_, at_;
+  const Line& line_;
+  int64_t at_;
   int b_, k_;
-  bool in_a_, single_;
 };
 
 struct Bars {
-  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty, clean, drain;
-  unsigned long long bad[2];     // slots whose value holds an element that is not finite; pieces take turns
+  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty[8], clean[8], drain;
+  unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
   Line line;
   uint32_t tmem;
   volatile uint32_t abort;
@@ -285,6 +259,8 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CU
         if (here >= 0)
           tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + (lane / S::kHalves) * page_bytes,
                      v ? vmap : kmap, (lane % S::kHalves) * 64, 0, it.head, here, &sh.full[stage]);
+        // values to clean: said once the stage's phase is this block's
+        if (v == 1 && lane == 0 && block_of(a, it, j).masked) mbar_arrive(&sh.dirty[stage]);
         ++loads;
       }
     }
@@ -295,54 +271,55 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CU
       mbar_wait_drain(&sh.full[x % S::kStages], (x / S::kStages) & 1);
 }
 
-// ---- warp 10: values that no row may see -------------------------------------------------------------------------
+// ---- warps 10, 11: values that no row may see --------------------------------------------------------------------
 // They must not reach a product as NaN or infinity (0 times them is NaN): rows past the last key are zeroed, and of the
 // tree's rows (a key that some rows see and others do not) the elements that are not finite; their slots are recorded,
-// and the rows that see them add those elements at the end.
+// and the rows that see them add those elements at the end.  It happens as soon as a block has landed, blocks ahead of
+// its products.
 template <typename T, int D>
 __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
   using S = Smem<D>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, thread = threadIdx.x - kCleanWarp * 32;
   constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-  uint32_t turn = 0;
+  uint32_t turn = 0;  // a bit a stage
   int before = 0, piece = 0;
   Pieces pieces(a, sh.line);
   Item it;
-  for (; pieces.next(it); before += it.blocks, ++piece)
-  for (int j = 0; j < it.blocks; ++j) {
-    const Block k = block_of(a, it, j);
-    if (!k.masked) continue;
-    // the issuing thread says when the block's values are there: only then is the stage's phase this block's
-    const int x = 2 * (before + j) + 1, stage = x % S::kStages;
-    bool ok = wait_bar(sh, a, &sh.dirty, turn++ & 1);
-    ok = ok && wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
-    if (!__all_sync(~0u, ok)) return;
-    const int tree = k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid);  // first row that is a slot
-    for (int half = 0; half < S::kHalves; ++half) {
-      uint4* p = reinterpret_cast<uint4*>(ring + stage * S::kTile + half * 128 * 128);
-      for (int i = tree * 8 + lane; i < BN * 8; i += 32) {
-        const int row = i >> 3;
-        if (row >= k.valid) {
-          p[i] = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        const uint4 v = p[i];
-        uint32_t e[4] = {v.x, v.y, v.z, v.w};
-        bool any = false;
+  for (; pieces.next(it); before += it.blocks, ++piece) {
+    for (int j = 0; j < it.blocks; ++j) {
+      const Block k = block_of(a, it, j);
+      if (!k.masked) continue;
+      const int x = 2 * (before + j) + 1, stage = x % S::kStages;
+      bool ok = wait_bar(sh, a, &sh.dirty[stage], (turn >> stage) & 1);
+      turn ^= 1u << stage;
+      ok = ok && wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
+      if (!__all_sync(~0u, ok)) return;
+      const int tree = k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid);  // first row that is a slot
+      uint4* p = reinterpret_cast<uint4*>(ring + stage * S::kTile);
+#pragma unroll 1
+      for (int half = 0; half < S::kHalves; ++half, p += 128 * 8) {
+#pragma unroll 4
+        for (int i = tree * 8 + thread; i < k.valid * 8; i += 64) {
+          const uint4 v = p[i];
+          uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          bool any = false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if ((e[c] & kExp) == kExp) { e[c] &= 0xFFFF0000u; any = true; }
-          if (((e[c] >> 16) & kExp) == kExp) { e[c] &= 0xFFFFu; any = true; }
+          for (int c = 0; c < 4; ++c) {
+            if ((e[c] & kExp) == kExp) { e[c] &= 0xFFFF0000u; any = true; }
+            if (((e[c] >> 16) & kExp) == kExp) { e[c] &= 0xFFFFu; any = true; }
+          }
+          if (any) {
+            p[i] = make_uint4(e[0], e[1], e[2], e[3]);
+            atomicOr(&sh.bad[piece & 7], 1ull << (k.base + (i >> 3) - it.ctx));
+          }
         }
-        if (any) {
-          p[i] = make_uint4(e[0], e[1], e[2], e[3]);
-          atomicOr(&sh.bad[piece & 1], 1ull << (k.base + row - it.ctx));
-        }
+#pragma unroll 4
+        for (int i = k.valid * 8 + thread; i < BN * 8; i += 64) p[i] = make_uint4(0, 0, 0, 0);
       }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.clean[stage]);
     }
-    tc::fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.clean);
   }
 }
 
@@ -387,8 +364,8 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       const uint32_t x = 2 * (before + j) + 1, stage = x % S::kStages;
       ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
       if (ok && (it.nt == 1 || t == 0) && block_of(a, it, j).masked) {
-        mbar_arrive(&sh.dirty);
-        ok = wait_bar(sh, a, &sh.clean, cleaned++ & 1);
+        ok = wait_bar(sh, a, &sh.clean[stage], (cleaned >> stage) & 1);
+        cleaned ^= 1u << stage;
       }
       ok = ok && wait_bar(sh, a, &sh.p_full[t], (t ? weights1++ : weights0++) & 1);
       if (!ok) break;
@@ -409,25 +386,53 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
 }
 
 // ---- warps 0-7: softmax and results -----------------------------------------------------------------------------
-template <typename T, int D>
-__device__ __forceinline__ void store_row(const AttendArgs& a, const Item& it, const Row& row, int in_tile, const float* o,
-                                          int c0) {
-  if (it.dest != kFinal) {
-    const int64_t at = part_row(a, it.dest, it.b < 0, (int64_t)row.token * a.c.q_heads + row.head, blockIdx.x, in_tile);
-    float* dst = a.part_o + at * D + c0;
+// 32 rows of 32 columns, a row a lane, to their places: through the warp's 4 KB of shared memory, so that 8 lanes (4 of
+// 16-bit output) write a row's 128 (64) bytes together.  `base`: the lane's row in the partials or the output (bytes of
+// column 0), null for no row.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint8_t* stage, uint8_t* base, bool part, bool vec, const float* f, int c0) {
+  const int lane = threadIdx.x & 31;
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(base);
+  __syncwarp();
+  if (part) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+          make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3), c = lane & 7;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(~0u, mine, r));
+      const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+      if (dst) *reinterpret_cast<float4*>(dst + c0 * 4 + c * 16) = v;
+    }
     return;
   }
-  T* dst = static_cast<T*>(a.out) + row.token * a.out_stride + row.head * D + c0;
-  if (a.out_vec) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 8)
-      *reinterpret_cast<uint4*>(dst + c) = make_uint4(Pair<T>::put(o[c], o[c + 1]), Pair<T>::put(o[c + 2], o[c + 3]),
-                                                      Pair<T>::put(o[c + 4], o[c + 5]), Pair<T>::put(o[c + 6], o[c + 7]));
-  } else {
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(Pair<T>::put(f[8 * i], f[8 * i + 1]), Pair<T>::put(f[8 * i + 2], f[8 * i + 3]),
+                   Pair<T>::put(f[8 * i + 4], f[8 * i + 5]), Pair<T>::put(f[8 * i + 6], f[8 * i + 7]));
+  __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 32; ++c) dst[c] = Pair<T>::round(o[c]);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2), c = lane & 3;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(~0u, mine, r));
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    if (!dst) continue;
+    dst += c0 * 2 + c * 16;
+    if (vec) {
+      *reinterpret_cast<uint4*>(dst) = v;
+    } else {
+      uint16_t* h = reinterpret_cast<uint16_t*>(dst);
+      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[2 * k] = (uint16_t)e[k];
+        h[2 * k + 1] = (uint16_t)(e[k] >> 16);
+      }
+    }
   }
 }
 
@@ -442,22 +447,35 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   Pieces pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); ++piece) {
-  // queries into shared memory, 16 bytes a thread, in the swizzled order the products read
-  for (int x = tid; x < it.nt * 128 * (D / 8); x += kSoftmaxThreads) {
-    const int r = x / (D / 8), c = x % (D / 8);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (it.row0 + r < it.rows) {
-      const Row row = row_of(a, it, it.row0 + r);
-      const T* src = static_cast<const T*>(a.q) + row.token * a.q_stride + row.head * D + c * 8;
-      if (a.q_vec) {
-        w = *reinterpret_cast<const uint4*>(src);
-      } else {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-        w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  if (piece > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last results have left the queries' space
+  // queries into shared memory, in the swizzled order the products read: 16 bytes a thread, 8 in flight
+  {
+    constexpr int kPer = D / 8, kRows = kSoftmaxThreads / kPer;   // threads of a row, rows at a time
+    const int c = tid % kPer, r0 = tid / kPer;
+    uint8_t* dst = q + (c >> 3) * (128 * 128);
+    for (int x = 0; x < it.nt * 128; x += 8 * kRows) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = x + i * kRows + r0;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (it.row0 + r < it.rows) {
+          const Row row = row_of(a, it, it.row0 + r);
+          const T* src = static_cast<const T*>(a.q) + row.token * a.q_stride + row.head * D + c * 8;
+          if (a.q_vec) {
+            w[i] = *reinterpret_cast<const uint4*>(src);
+          } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+            w[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = x + i * kRows + r0;
+        *reinterpret_cast<uint4*>(dst + (r >> 7) * S::kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[i];
       }
     }
-    uint8_t* dst = q + (r >> 7) * S::kTile + (c >> 3) * (128 * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4*>(dst) = w;
   }
   tc::fence_async_smem();
   tc::fence_before();
@@ -577,9 +595,13 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       : "=r"(all_ok) : "r"((int)ok) : "memory");
   if (!all_ok) return;
   tc::fence_after();
-  if (tid == 0) sh.bad[(piece + 1) & 1] = 0;         // everybody has read the piece before this one's
+  if (tid == 0 && it.dest == kCtaPart && it.first == 0 && it.b >= 0)
+    a.line[a.batch + 1 + blockIdx.x] = (int64_t)it.b * a.plan.tiles_b * a.c.kv_heads +
+                                       it.row0 / (it.nt * 128) * a.c.kv_heads + it.head;
+  // everybody has read what belonged to the piece two before; cleaning is at most the ring's 4 blocks ahead of this one
+  if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
   if (!warp_live) continue;
-  const uint64_t bad = sh.bad[piece & 1];
+  const uint64_t bad = sh.bad[piece & 7];
   float f0 = 1.f, f1 = 0.f;
   if (it.nt == 1) tc::ld2(tmem, m, l);
   if (two) {
@@ -597,6 +619,13 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const float inv = none ? 0.f : 1.f / l;
   f0 *= inv;
   f1 *= inv;
+  const int64_t at = (int64_t)row.token * a.c.q_heads + row.head;
+  const bool part = it.dest != kFinal;
+  const int64_t slot = part ? part_row(a, it.dest, it.b < 0, at, blockIdx.x, r - it.row0) : 0;
+  uint8_t* place = nullptr;
+  if (live) place = part ? reinterpret_cast<uint8_t*>(a.part_o + slot * D)
+                         : reinterpret_cast<uint8_t*>(static_cast<T*>(a.out) + row.token * a.out_stride + row.head * D);
+  uint8_t* stage = q + (tid >> 5) * 4096;            // every product is done: the queries' space is free
   // of a shared tile each group writes half of the columns
   const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
   const uint32_t o_at = tmem + 256 + (it.nt == 1 ? 0 : t * D);
@@ -626,24 +655,27 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
         }
       }
     }
-    if (live) store_row<T, D>(a, it, row, r - it.row0, f, c);
+    store_rows<T>(stage, place, part, a.out_vec, f, c);
   }
   if (live && (it.nt == 2 || t == 0)) {
     const float lse2 = none ? -INFINITY : m + log2f(l);
-    const int64_t at = (int64_t)row.token * a.c.q_heads + row.head;
-    if (it.dest != kFinal) a.part_lse[part_row(a, it.dest, it.b < 0, at, blockIdx.x, r - it.row0)] = lse2;
+    if (part) a.part_lse[slot] = lse2;
     else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
   }
   }
 }
 
-// Where this CTA's piece of the line begins; block 0 leaves the requests' places to the join.
+// Where this CTA's part of the line begins; block 0 leaves the requests' places to the join.
 __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, items = a.plan.tiles_b * a.c.kv_heads;
+  if (!a.plan.cut) {  // an item, whole
+    if (t == 0) sh.line = Line{0, INT64_MAX, 0, (int)(blockIdx.x / items), (int)(blockIdx.x % items)};
+    return;
+  }
+  const int lane = t & 31, warp = t >> 5;
   const int per = (a.batch + kThreads - 1) / kThreads, b0 = min(a.batch, t * per), b1 = min(a.batch, b0 + per);
-  const int items = a.plan.tiles_b * a.c.kv_heads;
   int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += items * cost_b(a, blocks_of(a, ctx_of(a, b)));
+  for (int b = b0; b < b1; ++b) sum += (int64_t)items * cost_b(a, blocks_of(a, ctx_of(a, b)));
   int64_t upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -652,8 +684,10 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  const int64_t ta = a.plan.items_a * cost_a(a);
+  const uint32_t ca = cost_a(a);
+  const int64_t ta = (int64_t)a.plan.items_a * ca;
   int64_t start = ta + upto - sum, total = ta;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) start += sums[w];
     total += sums[w];
@@ -662,16 +696,22 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
   const int64_t chunk = max((total + gridDim.x - 1) / gridDim.x, (int64_t)max(a.plan.step_a, a.plan.step_b));
   const int64_t lo = blockIdx.x * chunk;
   if (t == 0) {
-    sh.line.chunk = chunk;
-    if (lo >= total) { sh.line.b = a.batch; sh.line.at = total; }
     if (blockIdx.x == 0) a.line[a.batch] = chunk;
+    a.line[a.batch + 1 + blockIdx.x] = -1;
+    const int k = lo < ta ? (int)(lo / ca) : 0;
+    if (lo < ta) sh.line = Line{lo, lo + chunk, (int64_t)k * ca, -1, k};
+    if (lo >= total) sh.line = Line{lo, lo, total, a.batch, 0};
   }
   const bool here = lo >= ta && lo >= start && lo < start + sum;
   if (here || blockIdx.x == 0) {
     int64_t at = start;
     for (int b = b0; b < b1; ++b) {
-      const int64_t c = items * cost_b(a, blocks_of(a, ctx_of(a, b)));
-      if (here && lo >= at && lo < at + c) { sh.line.b = b; sh.line.at = at; }
+      const uint32_t cb = cost_b(a, blocks_of(a, ctx_of(a, b)));
+      const int64_t c = (int64_t)items * cb;
+      if (here && lo >= at && lo < at + c) {
+        const int k = (int)((lo - at) / cb);
+        sh.line = Line{lo, lo + chunk, at + (int64_t)k * cb, b, k};
+      }
       if (blockIdx.x == 0) a.line[b] = at;
       at += c;
     }
@@ -689,18 +729,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   grid_dependents_launch();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kStages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.dirty[i], 1);
+      mbar_init(&sh.clean[i], 2);
+    }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
     mbar_init(&sh.q_full, kSoftmaxThreads);
-    mbar_init(&sh.dirty, 1);
-    mbar_init(&sh.clean, 1);
     mbar_init(&sh.drain, 1);
-    sh.bad[0] = 0;
+    for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sh.tmem, 512);
-  if (a.plan.cut) find_line(a, sh, reinterpret_cast<int64_t*>(base));
+  find_line(a, sh, reinterpret_cast<int64_t*>(base));
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -713,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kMmaWarp) {
       if (tc::elect()) mma_role<T, D>(a, sh, base, base + S::kRing);
       __syncwarp();
-    } else if (warp == kCleanWarp) clean_role<T, D>(a, sh, base + S::kRing);
+    } else if (warp >= kCleanWarp) clean_role<T, D>(a, sh, base + S::kRing);
   }
   tc::fence_before();
   __syncthreads();
@@ -721,87 +764,118 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 
-// Joins the partial results of a row and head, in the order of their keys: a warp each.
+// Joins the partial results of a row and head, in the order of their keys, a warp a row at a time.  With packed items
+// every row has two items to join; else only rows of cut items have anything to, and the CTA of an item's first piece
+// has said which item that is (line[batch + 1 + CTA], -1: none).
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ AttendArgs a) {
-  constexpr int N = D / 32;
+__global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ AttendArgs a, int rows_per_warp) {
+  constexpr int N = D / 32, kBatch = 8;
   const AttendPlan& p = a.plan;
-  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, items = p.tiles_b * a.c.kv_heads;
   grid_dependency_wait();
-  if (at >= p.rows) return;
-  const int token = (int)(at / a.c.q_heads), head = (int)(at - (int64_t)token * a.c.q_heads);
-  const int b = token / a.slots, kv_head = head / a.group;
+  int b = blockIdx.z, item = blockIdx.y;
   const int64_t chunk = a.line[a.batch];
-  // the CTAs that hold pieces of the row's item(s): the last one's is the item's partial, the others' are by CTA
-  const int in_b = (token - b * a.slots) * a.group + head - kv_head * a.group;
-  const int tile_b = in_b / (p.nt_b * 128);
-  const int blocks = blocks_of(a, ctx_of(a, b));
-  const int64_t start_b = a.line[b] + (tile_b * a.c.kv_heads + kv_head) * cost_b(a, blocks) + p.fixed;
-  const int b_first = (int)(start_b / chunk), b_last = (int)((start_b + (int64_t)(blocks - 1) * p.step_b) / chunk);
-  int a_first = 0, a_last = -1, in_a = 0;
-  if (p.packed) {
-    in_a = b * a.slots * a.group + in_b;
-    const int tile_a = in_a / (p.nt_a * 128), np = (a.prefix_len + BN - 1) / BN;
-    const int64_t start = (tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
-    a_first = (int)(start / chunk);
-    a_last = (int)((start + (int64_t)(np - 1) * p.step_a) / chunk);
-    in_a -= tile_a * p.nt_a * 128;
-  } else if (b_first == b_last) {
-    return;  // whole, and written
+  if (!p.packed) {
+    const int64_t said = a.line[a.batch + 1 + blockIdx.y];
+    if (said < 0) return;
+    b = (int)(said / items);
+    item = (int)(said - (int64_t)b * items);
   }
-  const int na = a_last - a_first + 1, n = na + b_last - b_first + 1;
-  auto place = [&](int i) -> int64_t {
-    const bool of_a = i < na;
-    const int cta = of_a ? a_first + i : b_first + i - na;
-    const bool last = cta == (of_a ? a_last : b_last);
-    return part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : in_b - tile_b * p.nt_b * 128);
+  // the CTAs that hold pieces of an item: the last one's is the item's partial, the others' are by CTA; the quotients
+  // are CTA numbers, so a product with the fp32 reciprocal is right to one
+  const float inv_chunk = 1.f / (float)chunk;
+  auto cta_of = [&](int64_t x) -> int {
+    int c = (int)((float)x * inv_chunk);
+    if ((int64_t)c * chunk > x) --c;
+    if ((int64_t)(c + 1) * chunk <= x) ++c;
+    return c;
   };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_lse[place(i)]);
+  const int tile_b = item / a.c.kv_heads, kv_head = item - tile_b * a.c.kv_heads;
+  const int blocks = blocks_of(a, ctx_of(a, b)), np = (a.prefix_len + BN - 1) / BN;
+  const int64_t start_b = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed;
+  const int b_first = cta_of(start_b), b_last = cta_of(start_b + (int64_t)(blocks - 1) * p.step_b);
+  const int per = a.slots * a.group;
+  for (int k = 0; k < rows_per_warp; ++k) {
+    const int row = (blockIdx.x * rows_per_warp + k) * 8 + (threadIdx.x >> 5), in_b = tile_b * p.nt_b * 128 + row;
+    if (in_b >= per || row >= p.nt_b * 128) return;
+    const int slot = in_b / a.group;
+    const int64_t token = (int64_t)b * a.slots + slot;
+    const int head = kv_head * a.group + in_b - slot * a.group;
+    const int64_t at = token * a.c.q_heads + head;
+    int a_first = 0, a_last = -1, in_a = 0;
+    if (p.packed) {
+      in_a = b * per + in_b;
+      const int tile_a = in_a / (p.nt_a * 128);
+      in_a -= tile_a * p.nt_a * 128;
+      const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
+      a_first = cta_of(start_a);
+      a_last = cta_of(start_a + (int64_t)(np - 1) * p.step_a);
+    }
+    const int na = a_last - a_first + 1, n = na + b_last - b_first + 1;
+    float top = -INFINITY, sum = 0.f, acc[N] = {};
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float z[kBatch], v[kBatch][N];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  const float base = top == -INFINITY ? 0.f : top;  // fmaxf drops a NaN: the sum keeps it
-  float sum = 0.f, acc[N] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const int64_t r = place(i);
-    const float z = a.part_lse[r];
-    const float* o = a.part_o + r * D + lane * N;
-    float v[N];
-    if constexpr (N == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(o);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j;
+        z[j] = -INFINITY;
+        if (i >= n) continue;
+        const bool of_a = i < na;
+        const int cta = of_a ? a_first + i : b_first + i - na;
+        const bool last = cta == (of_a ? a_last : b_last);
+        const int64_t r = part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : row);
+        z[j] = a.part_lse[r];
+        const float* o = a.part_o + r * D + lane * N;
+        if constexpr (N == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o);
+          v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o);
+          v[j][0] = x.x; v[j][1] = x.y;
+        }
+      }
+      float next = top;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) next = fmaxf(next, z[j]);  // drops a NaN: the sum keeps it
+      const float base = next == -INFINITY ? 0.f : next, f = ex2(top - base);
+      sum *= f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] *= f;
+      top = next;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (z[j] == -INFINITY) continue;
+        const float w = ex2(z[j] - base);
+        sum += w;
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] += w * v[j][c];
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * N;
+    if (a.out_vec) {
+      const uint32_t w0 = Pair<T>::put(acc[0] * inv, acc[1] * inv);
+      if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w0, Pair<T>::put(acc[2] * inv, acc[3] * inv));
+      else *reinterpret_cast<uint32_t*>(out) = w0;
     } else {
-      const float2 x = *reinterpret_cast<const float2*>(o);
-      v[0] = x.x; v[1] = x.y;
-    }
-    if (z != -INFINITY) {
-      const float w = ex2(z - base);
-      sum += w;
 #pragma unroll
-      for (int c = 0; c < N; ++c) acc[c] += w * v[c];
+      for (int i = 0; i < N; ++i) out[i] = Pair<T>::round(acc[i] * inv);
     }
+    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * N;
-  if (a.out_vec) {
-    const uint32_t w0 = Pair<T>::put(acc[0] * inv, acc[1] * inv);
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w0, Pair<T>::put(acc[2] * inv, acc[3] * inv));
-    else *reinterpret_cast<uint32_t*>(out) = w0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = Pair<T>::round(acc[i] * inv);
-  }
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   k_kv_attend<T, D><<<a.plan.ctas, kThreads, Smem<D>::kBytes, s>>>(a, kmap, vmap);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.plan.cut)
-    e = launch_dependent(k_kv_join<T, D>, dim3((unsigned)((a.plan.rows + 7) / 8)), dim3(256), 0, s, a);
+  if (e == cudaSuccess && a.plan.cut) {
+    // a warp takes several rows where there are many: the item's places on the line are found once for them
+    const int rows = (std::min(a.slots * a.group, a.plan.nt_b * 128) + 7) / 8, each = a.plan.rows > 8192 ? std::min(rows, 4) : 1;
+    const int x = (rows + each - 1) / each;
+    const dim3 grid = a.plan.packed ? dim3(x, a.plan.tiles_b * a.c.kv_heads, a.batch) : dim3(x, a.plan.ctas);
+    e = launch_dependent(k_kv_join<T, D>, grid, dim3(256), 0, s, a, each);
+  }
   return e;
 }
 
@@ -823,22 +897,22 @@ cudaError_t prepare_kv_attend() {
 int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int64_t)num_sms * 256; }
 
 // Chooses between packed and joined items, and between cut and whole ones, from the sizes alone.  Costs are in
-// nanoseconds, measured on one SM: a key block of 128 against two tiles of 128 rows, against one, and the least a block
+// units of 10 ns, measured on one SM: a key block of 128 against two tiles of 128 rows, against one, and the least a block
 // takes when its keys and values come from memory (the SM's share of the copy rate) or from L2, where other items' SMs
 // read them too; before its first block an item pays for its queries, and the pipeline's start and end.
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int num_sms) {
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
-  const int two = dim == 128 ? 1600 : 1000, one = dim == 128 ? 850 : 550;
-  const int memory = dim == 128 ? 1450 : 725, l2 = dim == 128 ? 600 : 300;
+  const int two = dim == 128 ? 150 : 100, one = dim == 128 ? 80 : 60;
+  const int memory = dim == 128 ? 150 : 75, l2 = dim == 128 ? 70 : 40;
   AttendPlan best{};
   double best_t = 0;
   for (int packed = 0; packed < 2; ++packed) {
     if (packed && (np == 0 || batch == 1)) break;
     AttendPlan p{};
     p.packed = packed;
-    p.fixed = 2500;
+    p.fixed = 300;
     p.rows = all * kv_heads;
     p.nt_a = all > 128 ? 2 : 1;
     p.nt_b = R > 128 ? 2 : 1;
@@ -852,7 +926,7 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     const int64_t items_b = (int64_t)batch * p.tiles_b * kv_heads;
     const double whole = p.fixed + (double)blocks * p.step_b;
     const double work = p.items_a * (p.fixed + (double)np * p.step_a) + items_b * whole;
-    const double join = 3500 + (double)(p.rows * (packed ? 2 : 1) + num_sms * 256) * dim * 8 / 5000;
+    const double join = 400 + (double)(p.rows * (packed ? 2 : 1) + num_sms * 256) * dim * 8 / 50000;
     double t = work / num_sms + p.fixed + join;
     p.cut = 1;
     p.ctas = num_sms;

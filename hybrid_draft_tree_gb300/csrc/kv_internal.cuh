@@ -58,7 +58,7 @@ struct AttendArgs {
   int32_t q_vec, out_vec;  // 1 = rows start on 16-byte boundaries
   AttendPlan plan;
   float *part_o, *part_lse;  // partial results (rows of dim) and their log-sum-exp in log2
-  int64_t* line;             // [batch] starts of the requests' items, [batch] = a CTA's share
+  int64_t* line;             // [batch] starts of the requests' items; a CTA's share; [ctas] items that a CTA begins and does not end
   uint32_t wait_polls;       // 0 = the default
   uint32_t* err;
 };
