@@ -108,6 +108,18 @@ bool cache_map(const graft::KvLayout& c, int dtype, const void* base, CUtensorMa
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [token][head][d]; a copy is 64 elements of one group's heads of as many tokens as make a row tile.
+bool query_map(const graft::KvLayout& c, int dtype, const void* base, int64_t tokens, int64_t stride, int group, CUtensorMap* map) {
+  const cuuint64_t dims[3] = {(cuuint64_t)c.dim, (cuuint64_t)c.q_heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.dim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)}, step[3] = {1, 1, 1};
+  const EncodeTiled encode = encoder();
+  return encode && encode(map, dtype == GRAFT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void free_all(graft_kv* h) {
   cudaFree(h->err);
   cudaFree(h->part_o);
@@ -254,10 +266,16 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   a.out_vec = !misaligned(d_out, 16) && out_stride % 8 == 0;
   a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms);
   a.part_o = h->part_o; a.part_lse = h->part_lse; a.line = h->line; a.wait_polls = h->wait_polls;
-  CUtensorMap kmap, vmap;
+  a.by_group = graft::Divisor(a.group);
+  a.by_rows = graft::Divisor(slots * a.group);
+  a.by_heads = graft::Divisor(c.kv_heads);
+  a.q_map = a.q_vec && a.group <= 128 && q_stride < ((int64_t)1 << 38);
+  CUtensorMap qmap{}, kmap, vmap;
+  if (a.q_map && !query_map(c, h->cfg.dtype, d_q, (int64_t)batch * slots, q_stride, a.group, &qmap))
+    return fail(h, GRAFT_ECUDA, "the driver refused the queries' tensor map");
   if (!cache_map(c, h->cfg.dtype, d_k_cache, &kmap) || !cache_map(c, h->cfg.dtype, d_v_cache, &vmap))
     return fail(h, GRAFT_ECUDA, "the driver refused the cache's tensor map");
-  const cudaError_t e = graft::launch_kv_attend(a, kmap, vmap, h->cfg.dtype, (cudaStream_t)stream);
+  const cudaError_t e = graft::launch_kv_attend(a, qmap, kmap, vmap, h->cfg.dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_attend launch");
   h->last_launches = a.plan.cut ? 2 : 1;
   return GRAFT_OK;

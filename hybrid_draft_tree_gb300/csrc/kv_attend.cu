@@ -118,9 +118,9 @@ class Pieces {
       }
       it.nt = of_a ? p.nt_a : p.nt_b;
       it.rows = (of_a ? a_.batch : 1) * a_.slots * a_.group;
-      const int tile = k_ / a_.c.kv_heads;
+      const int tile = a_.by_heads.div(k_);
       it.head = k_ - tile * a_.c.kv_heads;
-      it.row0 = tile * it.nt * 128;
+      it.row0 = tile * it.nt * p.tile;
       const uint32_t step = of_a ? p.step_a : p.step_b, length = total * step;
       it.first = base >= lo ? 0 : (int)(((uint32_t)(lo - base) + step - 1) / step);
       const int end = hi - base >= length ? total : (int)(((uint32_t)(hi - base) + step - 1) / step);
@@ -140,7 +140,7 @@ class Pieces {
 };
 
 struct Bars {
-  unsigned long long full[8], empty[8], q_full, s_full[2], p_full[2], o_done[2], dirty[8], clean[8], drain;
+  unsigned long long full[8], empty[8], q_full, s_full[2], s_read[2], p_full[2], o_done[2], dirty[8], clean[8], drain;
   unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
   Line line;
   uint32_t tmem;
@@ -167,11 +167,9 @@ struct Row {
   int token, head;
 };
 __device__ __forceinline__ Row row_of(const AttendArgs& a, const Item& it, int r) {
-  const int per = a.slots * a.group;
-  const int b = it.b >= 0 ? it.b : r / per;
-  const int in = it.b >= 0 ? r : r - b * per;
-  const int slot = in / a.group;
-  return Row{b * a.slots + slot, it.head * a.group + in - slot * a.group};
+  // rows of all requests follow each other as those of one do: slots times the group
+  const int slot = a.by_group.div(r);
+  return Row{(it.b >= 0 ? it.b * a.slots : 0) + slot, it.head * a.group + r - slot * a.group};
 }
 
 __device__ __forceinline__ uint64_t mask_of(const AttendArgs& a, int token) {
@@ -183,9 +181,9 @@ __device__ __forceinline__ uint64_t mask_of(const AttendArgs& a, int token) {
 
 // Row of a partial result: of item pieces that end their item, by row and head, packed items' and the others' apart;
 // of pieces whose item goes on in the next CTA, by CTA and row of the tile.
-__device__ __forceinline__ int64_t part_row(const AttendArgs& a, int dest, bool packed, int64_t at, int cta, int in_tile) {
-  if (dest == kItemPart) return (packed ? a.plan.rows : 0) + at;
-  return 2 * a.plan.rows + (int64_t)cta * 256 + in_tile;
+__device__ __forceinline__ int part_row(const AttendArgs& a, int dest, bool packed, int at, int cta, int in_tile) {
+  if (dest == kItemPart) return (packed ? (int)a.plan.rows : 0) + at;
+  return 2 * (int)a.plan.rows + cta * 256 + in_tile;
 }
 
 // A wait that another role's abort, or the poll limit, ends; false: the item's results are void.
@@ -335,7 +333,8 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
   const uint64_t qd = tc::smem_desc(smem_u32(q), 16), kd = tc::smem_desc(smem_u32(ring), 16);
   const uint64_t vd = tc::smem_desc(smem_u32(ring), 128 * 128);
   constexpr int kTile16 = S::kTile / 16;
-  uint32_t cleaned = 0, weights0 = 0, weights1 = 0, before = 0, piece = 0;
+  constexpr bool kApart = D == 64;
+  uint32_t cleaned = 0, weights0 = 0, weights1 = 0, reads0 = 0, reads1 = 0, before = 0, piece = 0;
   bool ok = true;
   Pieces pieces(a, sh.line);
   Item it;
@@ -359,7 +358,17 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
     };
     ok = wait_bar(sh, a, &sh.q_full, piece & 1);
     for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
+    // With room for P beside S (D = 64) a group's next scores are computed as soon as it has read its last ones, while it
+    // turns them into weights; the products with the values follow one unit behind.
+    int scored = min(units, 2);
+    auto early = [&](int u) -> bool {  // unit u's scores have been read
+      if (!kApart || scored >= units) return true;
+      if (!wait_bar(sh, a, &sh.s_read[u & 1], (u & 1 ? reads1++ : reads0++) & 1)) return false;
+      return qk(scored++);
+    };
+    ok = ok && early(0);
     for (int u = 0; u < units && ok; ++u) {
+      if (u + 1 < units && !early(u + 1)) { ok = false; break; }
       const int t = u & 1, j = it.nt == 2 ? u >> 1 : u;
       const uint32_t x = 2 * (before + j) + 1, stage = x % S::kStages;
       ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
@@ -375,8 +384,8 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
 #pragma unroll
       for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, u > 1 || k > 0);
       if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
-      if (u + 2 >= units) tc::commit(&sh.o_done[t]);
-      else ok = qk(u + 2);
+      if (kApart || u + 2 >= units) tc::commit(&sh.o_done[t]);
+      if (!kApart && u + 2 < units) ok = qk(u + 2);
     }
   }
   if (!ok) {  // the products in flight finish before the tensor memory goes back
@@ -387,12 +396,11 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
 
 // ---- warps 0-7: softmax and results -----------------------------------------------------------------------------
 // 32 rows of 32 columns, a row a lane, to their places: through the warp's 4 KB of shared memory, so that 8 lanes (4 of
-// 16-bit output) write a row's 128 (64) bytes together.  `base`: the lane's row in the partials or the output (bytes of
-// column 0), null for no row.
-template <typename T>
-__device__ __forceinline__ void store_rows(uint8_t* stage, uint8_t* base, bool part, bool vec, const float* f, int c0) {
+// 16-bit output) write a row's 128 (64) bytes together.  `code`: the lane's row, of the partials (part) or as token *
+// 1024 + head of the output; -1 for none.
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(const AttendArgs& a, uint8_t* stage, int code, bool part, const float* f, int c0) {
   const int lane = threadIdx.x & 31;
-  const unsigned long long mine = reinterpret_cast<unsigned long long>(base);
   __syncwarp();
   if (part) {
 #pragma unroll
@@ -400,13 +408,18 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint8_t* base, bool p
       *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
           make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
     __syncwarp();
+    int at[8];
+    float4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = i * 4 + (lane >> 3), c = lane & 7;
-      uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(~0u, mine, r));
-      const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-      if (dst) *reinterpret_cast<float4*>(dst + c0 * 4 + c * 16) = v;
+      at[i] = __shfl_sync(~0u, code, r);
+      v[i] = *reinterpret_cast<const float4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
     }
+    float* dst = a.part_o + c0 + (lane & 7) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at[i] >= 0) *reinterpret_cast<float4*>(dst + (int64_t)at[i] * D) = v[i];
     return;
   }
 #pragma unroll
@@ -415,18 +428,24 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint8_t* base, bool p
         make_uint4(Pair<T>::put(f[8 * i], f[8 * i + 1]), Pair<T>::put(f[8 * i + 2], f[8 * i + 3]),
                    Pair<T>::put(f[8 * i + 4], f[8 * i + 5]), Pair<T>::put(f[8 * i + 6], f[8 * i + 7]));
   __syncwarp();
+  int at[4];
+  uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2), c = lane & 3;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(__shfl_sync(~0u, mine, r));
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-    if (!dst) continue;
-    dst += c0 * 2 + c * 16;
-    if (vec) {
-      *reinterpret_cast<uint4*>(dst) = v;
+    at[i] = __shfl_sync(~0u, code, r);
+    v[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  }
+  T* dst = static_cast<T*>(a.out) + c0 + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (at[i] < 0) continue;
+    T* p = dst + (int64_t)(at[i] >> 10) * a.out_stride + (at[i] & 1023) * D;
+    if (a.out_vec) {
+      *reinterpret_cast<uint4*>(p) = v[i];
     } else {
-      uint16_t* h = reinterpret_cast<uint16_t*>(dst);
-      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+      uint16_t* h = reinterpret_cast<uint16_t*>(p);
+      const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         h[2 * k] = (uint16_t)e[k];
@@ -437,7 +456,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint8_t* base, bool p
 }
 
 template <typename T, int D>
-__device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
+__device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CUtensorMap* qmap) {
   using S = Smem<D>;
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
@@ -447,42 +466,45 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   Pieces pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); ++piece) {
-  if (piece > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last results have left the queries' space
-  // queries into shared memory, in the swizzled order the products read: 16 bytes a thread, 8 in flight
-  {
-    constexpr int kPer = D / 8, kRows = kSoftmaxThreads / kPer;   // threads of a row, rows at a time
-    const int c = tid % kPer, r0 = tid / kPer;
-    uint8_t* dst = q + (c >> 3) * (128 * 128);
-    for (int x = 0; x < it.nt * 128; x += 8 * kRows) {
-      uint4 w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = x + i * kRows + r0;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (it.row0 + r < it.rows) {
-          const Row row = row_of(a, it, it.row0 + r);
-          const T* src = static_cast<const T*>(a.q) + row.token * a.q_stride + row.head * D + c * 8;
-          if (a.q_vec) {
-            w[i] = *reinterpret_cast<const uint4*>(src);
-          } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-            w[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = x + i * kRows + r0;
-        *reinterpret_cast<uint4*>(dst + (r >> 7) * S::kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[i];
+  if (piece > 0) {  // the last results have left tensor memory and the queries' space
+    tc::fence_async_smem();
+    tc::fence_before();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+  // queries into shared memory, in the swizzled order the products read: by tensor map, or 16 bytes a thread
+  if (a.q_map) {
+    if (tid == 0) {
+      tc::fence_after();
+      mbar_expect_tx(&sh.q_full, it.nt * S::kHalves * a.plan.tile * 128);
+      for (int x = 0; x < it.nt * S::kHalves; ++x) {
+        const int tile = x / S::kHalves, half = x % S::kHalves;
+        const Row row = row_of(a, it, it.row0 + tile * a.plan.tile);
+        tc::tma_3d(q + tile * S::kTile + half * (128 * 128), qmap, half * 64, it.head * a.group, row.token, &sh.q_full);
       }
     }
+  } else {
+    constexpr int kPer = D / 8, kRows = kSoftmaxThreads / kPer;   // threads of a row, rows at a time
+    const int c = tid % kPer;
+    for (int x = tid / kPer; x < it.nt * 128; x += kRows) {
+      const int tile = x >> 7, in = x & 127, r = it.row0 + tile * a.plan.tile + in;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (in < a.plan.tile && r < it.rows) {
+        const Row row = row_of(a, it, r);
+        const uint16_t* h = static_cast<const uint16_t*>(a.q) + row.token * a.q_stride + row.head * D + c * 8;
+        w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      }
+      *reinterpret_cast<uint4*>(q + tile * S::kTile + (c >> 3) * (128 * 128) + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = w;
+    }
+    tc::fence_async_smem();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (tid == 0) {
+      tc::fence_after();
+      mbar_arrive(&sh.q_full);
+    }
   }
-  tc::fence_async_smem();
-  tc::fence_before();
-  mbar_arrive(&sh.q_full);
 
-  const int r = it.row0 + (it.nt == 2 ? t * 128 : 0) + lane_row;
-  const bool live = r < it.rows;
+  const int r = it.row0 + (it.nt == 2 ? t * a.plan.tile : 0) + lane_row;
+  const bool live = lane_row < a.plan.tile && r < it.rows;
   const Row row = live ? row_of(a, it, r) : Row{0, 0};
   const uint64_t mask = live ? mask_of(a, row.token) : 0;
   const bool warp_live = __any_sync(~0u, live);
@@ -495,11 +517,24 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
     ok = __all_sync(~0u, wait_bar(sh, a, &sh.s_full[t], scores++ & 1));
     if (!ok) break;
     tc::fence_after();
+    // the group's scores may be overwritten once they are in registers; nobody waits for that in the last two units
+    auto read_done = [&] {
+      tc::fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0 && n + 1 < units) mbar_arrive(&sh.s_read[t]);
+    };
+    // ... and the products with the last weights are then still under way: they end before O or the weights change
+    auto settled = [&] { return n == 0 || __all_sync(~0u, wait_bar(sh, a, &sh.o_done[t], results++ & 1)); };
+    if (D == 64 && !warp_live) {
+      read_done();
+      if (!settled()) { ok = false; break; }
+    }
     if (warp_live) {
       uint32_t s[BN];
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
       tc::wait_ld<BN>(s);
+      if (D == 64) read_done();
       if (k.masked) {
         // bit c: the row sees key c of the block
         uint64_t lo, hi;
@@ -534,13 +569,17 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
         mx[3] = fmaxf(mx[3], sf[c + 3]);
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      if (D == 64) {
+        if (!settled()) { ok = false; break; }
+        tc::fence_after();
+      }
       if (__any_sync(~0u, top > m + kGrow)) {
         const float next = fmaxf(m, top);
         const float f = next == -INFINITY ? 1.f : ex2(m - next);
         m = next;
         l2.x *= f;
         l2.y *= f;
-        if (n > 0) {  // the scores' arrival implies that the products before them are done: O is at rest
+        if (n > 0) {  // O is at rest: the products before these scores are done (D = 128: the scores came after them)
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -597,7 +636,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   tc::fence_after();
   if (tid == 0 && it.dest == kCtaPart && it.first == 0 && it.b >= 0)
     a.line[a.batch + 1 + blockIdx.x] = (int64_t)it.b * a.plan.tiles_b * a.c.kv_heads +
-                                       it.row0 / (it.nt * 128) * a.c.kv_heads + it.head;
+                                       it.row0 / (it.nt * a.plan.tile) * a.c.kv_heads + it.head;
   // everybody has read what belonged to the piece two before; cleaning is at most the ring's 4 blocks ahead of this one
   if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
   if (!warp_live) continue;
@@ -619,12 +658,10 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const float inv = none ? 0.f : 1.f / l;
   f0 *= inv;
   f1 *= inv;
-  const int64_t at = (int64_t)row.token * a.c.q_heads + row.head;
+  const int at = row.token * a.c.q_heads + row.head;
   const bool part = it.dest != kFinal;
-  const int64_t slot = part ? part_row(a, it.dest, it.b < 0, at, blockIdx.x, r - it.row0) : 0;
-  uint8_t* place = nullptr;
-  if (live) place = part ? reinterpret_cast<uint8_t*>(a.part_o + slot * D)
-                         : reinterpret_cast<uint8_t*>(static_cast<T*>(a.out) + row.token * a.out_stride + row.head * D);
+  const int slot = part_row(a, it.dest, it.b < 0, at, blockIdx.x, (it.nt == 2 ? t * 128 : 0) + lane_row);
+  const int code = !live ? -1 : part ? slot : row.token << 10 | row.head;
   uint8_t* stage = q + (tid >> 5) * 4096;            // every product is done: the queries' space is free
   // of a shared tile each group writes half of the columns
   const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
@@ -655,7 +692,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
         }
       }
     }
-    store_rows<T>(stage, place, part, a.out_vec, f, c);
+    store_rows<T, D>(a, stage, code, part, f, c);
   }
   if (live && (it.nt == 2 || t == 0)) {
     const float lse2 = none ? -INFINITY : m + log2f(l);
@@ -720,8 +757,8 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_kv_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap) {
+    k_kv_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars sh;
@@ -735,8 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.dirty[i], 1);
       mbar_init(&sh.clean[i], 2);
     }
-    for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
-    mbar_init(&sh.q_full, kSoftmaxThreads);
+    for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
+    mbar_init(&sh.q_full, 1);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     sh.abort = 0;
@@ -744,12 +781,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sh.tmem, 512);
   find_line(a, sh, reinterpret_cast<int64_t*>(base));
+  tc::fence_async_smem();  // copies will land where the sums were
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (warp < kTmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<T, D>(a, sh, base);
+    softmax_role<T, D>(a, sh, base, &qmap);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) load_role<D>(a, sh, base + S::kRing, &kmap, &vmap);
@@ -764,18 +802,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 
-// Joins the partial results of a row and head, in the order of their keys, a warp a row at a time.  With packed items
-// every row has two items to join; else only rows of cut items have anything to, and the CTA of an item's first piece
-// has said which item that is (line[batch + 1 + CTA], -1: none).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ AttendArgs a, int rows_per_warp) {
-  constexpr int N = D / 32, kBatch = 8;
+// Joins the partial results of a row and head, in the order of their keys: D / 4 lanes a row, 16 bytes a lane.  Every
+// row has two items to join when items are packed; else only rows of cut items have anything to: CTA row y then is an
+// item, or (by_cta, with more items than CTAs) the CTA of an item's first piece, which has said which item that is
+// (line[batch + 1 + y], -1: none).  What it takes is latency, so P partials of a row are asked for at once, and with
+// many rows registers are kept few and CTAs many.
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(256, P == 2 ? 6 : 3) k_kv_join(const __grid_constant__ AttendArgs a, int by_cta) {
+  constexpr int kLanes = D / 4;
   const AttendPlan& p = a.plan;
-  const int lane = threadIdx.x & 31, items = p.tiles_b * a.c.kv_heads;
-  grid_dependency_wait();
+  const int lane = threadIdx.x % kLanes, items = p.tiles_b * a.c.kv_heads;
   int b = blockIdx.z, item = blockIdx.y;
+  grid_dependency_wait();
   const int64_t chunk = a.line[a.batch];
-  if (!p.packed) {
+  if (by_cta) {
     const int64_t said = a.line[a.batch + 1 + blockIdx.y];
     if (said < 0) return;
     b = (int)(said / items);
@@ -790,91 +830,86 @@ __global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ AttendA
     if ((int64_t)(c + 1) * chunk <= x) ++c;
     return c;
   };
-  const int tile_b = item / a.c.kv_heads, kv_head = item - tile_b * a.c.kv_heads;
-  const int blocks = blocks_of(a, ctx_of(a, b)), np = (a.prefix_len + BN - 1) / BN;
+  const int tile_b = a.by_heads.div(item), kv_head = item - tile_b * a.c.kv_heads;
+  const int blocks = blocks_of(a, ctx_of(a, b));
   const int64_t start_b = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed;
   const int b_first = cta_of(start_b), b_last = cta_of(start_b + (int64_t)(blocks - 1) * p.step_b);
-  const int per = a.slots * a.group;
-  for (int k = 0; k < rows_per_warp; ++k) {
-    const int row = (blockIdx.x * rows_per_warp + k) * 8 + (threadIdx.x >> 5), in_b = tile_b * p.nt_b * 128 + row;
-    if (in_b >= per || row >= p.nt_b * 128) return;
-    const int slot = in_b / a.group;
-    const int64_t token = (int64_t)b * a.slots + slot;
-    const int head = kv_head * a.group + in_b - slot * a.group;
-    const int64_t at = token * a.c.q_heads + head;
-    int a_first = 0, a_last = -1, in_a = 0;
-    if (p.packed) {
-      in_a = b * per + in_b;
-      const int tile_a = in_a / (p.nt_a * 128);
-      in_a -= tile_a * p.nt_a * 128;
-      const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
-      a_first = cta_of(start_a);
-      a_last = cta_of(start_a + (int64_t)(np - 1) * p.step_a);
-    }
-    const int na = a_last - a_first + 1, n = na + b_last - b_first + 1;
-    float top = -INFINITY, sum = 0.f, acc[N] = {};
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      float z[kBatch], v[kBatch][N];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j;
-        z[j] = -INFINITY;
-        if (i >= n) continue;
-        const bool of_a = i < na;
-        const int cta = of_a ? a_first + i : b_first + i - na;
-        const bool last = cta == (of_a ? a_last : b_last);
-        const int64_t r = part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : row);
-        z[j] = a.part_lse[r];
-        const float* o = a.part_o + r * D + lane * N;
-        if constexpr (N == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(o);
-          v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(o);
-          v[j][0] = x.x; v[j][1] = x.y;
-        }
-      }
-      float next = top;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) next = fmaxf(next, z[j]);  // drops a NaN: the sum keeps it
-      const float base = next == -INFINITY ? 0.f : next, f = ex2(top - base);
-      sum *= f;
-#pragma unroll
-      for (int c = 0; c < N; ++c) acc[c] *= f;
-      top = next;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (z[j] == -INFINITY) continue;
-        const float w = ex2(z[j] - base);
-        sum += w;
-#pragma unroll
-        for (int c = 0; c < N; ++c) acc[c] += w * v[j][c];
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * N;
-    if (a.out_vec) {
-      const uint32_t w0 = Pair<T>::put(acc[0] * inv, acc[1] * inv);
-      if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w0, Pair<T>::put(acc[2] * inv, acc[3] * inv));
-      else *reinterpret_cast<uint32_t*>(out) = w0;
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) out[i] = Pair<T>::round(acc[i] * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  if (!p.packed && b_first == b_last) return;  // whole, and written
+  int row = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  const int per = a.slots * a.group, in_b = tile_b * p.nt_b * p.tile + row;
+  if (in_b >= per || row >= p.nt_b * p.tile) return;
+  const int slot = a.by_group.div(in_b), token = b * a.slots + slot, head = kv_head * a.group + in_b - slot * a.group;
+  const int at = token * a.c.q_heads + head;
+  if (p.nt_b == 2 && row >= p.tile) row += 128 - p.tile;  // place in its CTA's partial
+  int in_a = 0, a_first = 0, na = 0;
+  if (p.packed) {
+    in_a = b * per + in_b;
+    const int tile_a = in_a / (p.nt_a * p.tile), np = (a.prefix_len + BN - 1) / BN;
+    in_a -= tile_a * p.nt_a * p.tile;
+    if (p.nt_a == 2 && in_a >= p.tile) in_a += 128 - p.tile;
+    const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
+    a_first = cta_of(start_a);
+    na = cta_of(start_a + (int64_t)(np - 1) * p.step_a) - a_first + 1;
   }
+  const int n = na + b_last - b_first + 1;
+  const float* parts = a.part_o + lane * 4;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += P) {
+    float z[P];
+    float4 v[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = i0 + j;
+      z[j] = -INFINITY;
+      if (i >= n) continue;
+      const bool of_a = i < na;
+      const int cta = of_a ? a_first + i : b_first + i - na;
+      const bool last = of_a ? i == na - 1 : cta == b_last;
+      const int r = part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : row);
+      z[j] = a.part_lse[r];
+      v[j] = *reinterpret_cast<const float4*>(parts + (int64_t)r * D);
+    }
+    float next = top;
+#pragma unroll
+    for (int j = 0; j < P; ++j) next = fmaxf(next, z[j]);  // drops a NaN: the sum keeps it
+    const float base = next == -INFINITY ? 0.f : next, f = ex2(top - base);
+    sum *= f;
+    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+    top = next;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      if (z[j] == -INFINITY) continue;
+      const float w = ex2(z[j] - base);
+      sum += w;
+      acc.x += w * v[j].x; acc.y += w * v[j].y; acc.z += w * v[j].z; acc.w += w * v[j].w;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * 4;
+  const uint2 w = make_uint2(Pair<T>::put(acc.x * inv, acc.y * inv), Pair<T>::put(acc.z * inv, acc.w * inv));
+  if (a.out_vec) {
+    *reinterpret_cast<uint2*>(out) = w;
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(out);
+    h[0] = (uint16_t)w.x; h[1] = (uint16_t)(w.x >> 16); h[2] = (uint16_t)w.y; h[3] = (uint16_t)(w.y >> 16);
+  }
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
-cudaError_t launch(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  k_kv_attend<T, D><<<a.plan.ctas, kThreads, Smem<D>::kBytes, s>>>(a, kmap, vmap);
+cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                   cudaStream_t s) {
+  const AttendPlan& p = a.plan;
+  k_kv_attend<T, D><<<p.ctas, kThreads, Smem<D>::kBytes, s>>>(a, qmap, kmap, vmap);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && a.plan.cut) {
-    // a warp takes several rows where there are many: the item's places on the line are found once for them
-    const int rows = (std::min(a.slots * a.group, a.plan.nt_b * 128) + 7) / 8, each = a.plan.rows > 8192 ? std::min(rows, 4) : 1;
-    const int x = (rows + each - 1) / each;
-    const dim3 grid = a.plan.packed ? dim3(x, a.plan.tiles_b * a.c.kv_heads, a.batch) : dim3(x, a.plan.ctas);
-    e = launch_dependent(k_kv_join<T, D>, grid, dim3(256), 0, s, a, each);
+  if (e == cudaSuccess && p.cut) {
+    // many rows have few partials each
+    const int rows = std::min(a.slots * a.group, p.nt_b * p.tile), items = p.tiles_b * a.c.kv_heads, each = 1024 / D;
+    const bool by_cta = !p.packed && (int64_t)items * a.batch > p.ctas;
+    const dim3 grid = by_cta ? dim3((rows + each - 1) / each, p.ctas) : dim3((rows + each - 1) / each, items, a.batch);
+    e = p.rows > 8192 ? launch_dependent(k_kv_join<T, D, 2>, grid, dim3(256), 0, s, a, (int)by_cta)
+                      : launch_dependent(k_kv_join<T, D, 8>, grid, dim3(256), 0, s, a, (int)by_cta);
   }
   return e;
 }
@@ -914,10 +949,11 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     p.packed = packed;
     p.fixed = 300;
     p.rows = all * kv_heads;
-    p.nt_a = all > 128 ? 2 : 1;
-    p.nt_b = R > 128 ? 2 : 1;
-    p.tiles_b = (int)((R + 128 * p.nt_b - 1) / (128 * p.nt_b));
-    p.items_a = packed ? (int)((all + 128 * p.nt_a - 1) / (128 * p.nt_a)) * kv_heads : 0;
+    p.tile = group <= 128 ? 128 / group * group : 128;
+    p.nt_a = all > p.tile ? 2 : 1;
+    p.nt_b = R > p.tile ? 2 : 1;
+    p.tiles_b = (int)((R + p.tile * p.nt_b - 1) / (p.tile * p.nt_b));
+    p.items_a = packed ? (int)((all + p.tile * p.nt_a - 1) / (p.tile * p.nt_a)) * kv_heads : 0;
     p.step_a = std::max(p.nt_a == 2 ? two : one, l2);
     // the share of an item's blocks that no other item reads
     const int blocks = packed ? no : np + no;
@@ -943,11 +979,11 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   return best;
 }
 
-cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype,
-                             cudaStream_t s) {
+cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, int dtype, cudaStream_t s) {
   if (a.c.dim == 128)
-    return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, 128>(a, kmap, vmap, s) : launch<__half, 128>(a, kmap, vmap, s);
-  return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, 64>(a, kmap, vmap, s) : launch<__half, 64>(a, kmap, vmap, s);
+    return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, 128>(a, qmap, kmap, vmap, s) : launch<__half, 128>(a, qmap, kmap, vmap, s);
+  return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, 64>(a, qmap, kmap, vmap, s) : launch<__half, 64>(a, qmap, kmap, vmap, s);
 }
 
 }  // namespace graft

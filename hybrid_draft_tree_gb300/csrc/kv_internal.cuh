@@ -29,13 +29,26 @@ struct AppendArgs {
   uint32_t* err;
 };
 
+// Quotients of numbers below 2^31 by a divisor that the host knows: with s = ceil(log2 d) and
+// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(n mul / 2^32)) / 2^s.
+struct Divisor {
+  uint32_t mul = 0, shift = 0, d = 1;
+  Divisor() = default;
+  explicit Divisor(uint32_t n) : d(n) {
+    while ((1ull << shift) < n) ++shift;
+    mul = (uint32_t)((((1ull << shift) - n) << 32) / n + 1);
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 // How a call's work is laid out (plan_kv_attend): packed items' rows of all requests against the prefix, then each
 // request's rows against its own context (and, when none are packed, the prefix).
 struct AttendPlan {
   int32_t packed, cut;       // cut: CTAs take equal pieces of the line of items; else an item each
   int32_t ctas, items_a;     // items_a: packed items
   int32_t tiles_b;           // row tiles of a request and head
-  int32_t nt_a, nt_b;        // 128-row tiles of an item
+  int32_t nt_a, nt_b;        // row tiles of an item
+  int32_t tile;              // rows of a tile: the most whole groups in 128
   int32_t fixed, step_a, step_b;  // cost of an item before its first block, and of a block
   int64_t rows;              // query rows times query heads
 };
@@ -55,7 +68,8 @@ struct AttendArgs {
   float scale;
   void* out;
   float* lse;
-  int32_t q_vec, out_vec;  // 1 = rows start on 16-byte boundaries
+  int32_t q_map, q_vec, out_vec;  // 1 = queries come by tensor map; rows start on 16-byte boundaries
+  Divisor by_group, by_rows, by_heads;  // group, slots * group, kv_heads
   AttendPlan plan;
   float *part_o, *part_lse;  // partial results (rows of dim) and their log-sum-exp in log2
   int64_t* line;             // [batch] starts of the requests' items; a CTA's share; [ctas] items that a CTA begins and does not end
@@ -96,7 +110,7 @@ cudaError_t prepare_kv_attend();
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int num_sms);
-cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype,
-                             cudaStream_t s);
+cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, int dtype, cudaStream_t s);
 
 }  // namespace graft
