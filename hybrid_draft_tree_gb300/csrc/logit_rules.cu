@@ -3,9 +3,18 @@
 // A CTA takes one chunk of one request's vocabulary and some of its slots'
 // rows.  It builds the chunk's rule table in shared memory once (occurrences in
 // the history, the bias entry, whether a slot's token falls there) and streams
-// the rows past it.  Nearly every element has no rule and is copied as it is
-// (or masked by a bit): a bitmap tells which 16-byte pieces hold one that has.
-#include "kv_internal.cuh"
+// the rows past it, so that the history is read once a chunk and not once a
+// row.  Nearly every element has no rule: a bitmap tells which 16-byte pieces
+// hold one that has, and the others are copied as they are, or masked by their
+// bits of the grammar's row.  Bound by memory: a row is read and written once.
+//
+// Rows need not start on 16-byte boundaries: the pieces are those of the row's
+// own alignment, so the table and the bits are read at the row's offset, and
+// the few elements before its first and after its last piece go one by one.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+
 #include "logit_rules.cuh"
 
 namespace graft {
@@ -18,26 +27,59 @@ constexpr int BIAS_SHIFT = 20;              // index of the bias entry + 1, 11 b
 constexpr uint32_t BIAS = 0x7FFu << BIAS_SHIFT;
 constexpr uint32_t TREE = 1u << 31;         // the token of a slot
 
+// Elements in the words of a 16-byte piece.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int N = 4;
-  static constexpr uint32_t NEG_INF = 0xFF800000u;
   static __device__ __forceinline__ float get(float x) { return x; }
   static __device__ __forceinline__ float put(float x) { return x; }
+  static __device__ __forceinline__ float at(const uint32_t* w, int e) {
+    return __uint_as_float(e & 2 ? (e & 1 ? w[3] : w[2]) : (e & 1 ? w[1] : w[0]));
+  }
+  static __device__ __forceinline__ void set(uint32_t* w, int e, float x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = i == e ? __float_as_uint(x) : w[i];
+  }
+  // words of elements whose bit of `allowed` is 0 become -inf
+  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (allowed >> i) & 1 ? w[i] : 0xFF800000u;
+  }
 };
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ float at(const uint32_t* w, int e) {
+    const uint32_t x = e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0]);
+    return __uint_as_float(e & 1 ? x & 0xFFFF0000u : x << 16);
+  }
+  static __device__ __forceinline__ void set(uint32_t* w, int e, float x) {
+    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t n = e & 1 ? (w[i] & 0xFFFFu) | h << 16 : (w[i] & 0xFFFF0000u) | h;
+      w[i] = i == e >> 1 ? n : w[i];
+    }
+  }
+  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = ((allowed >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
+      w[i] = (w[i] & m) | (0xFF80FF80u & ~m);
+    }
+  }
 };
 
 struct Shared {
   uint64_t path[MAX_S];     // ancestor masks without the root
   int32_t tok[MAX_S];       // tokens of the slots, -1 = pad
   int32_t gram[MAX_S];      // grammar row, -1 = all allowed
+  int32_t rows[MAX_S];      // the CTA's slots that are no pads
+  int32_t n_rows;
   float rep, freq, pres;
 };
 
@@ -61,8 +103,15 @@ __device__ __forceinline__ float apply(const LogitArgs& a, const Shared& sh, con
   return x;
 }
 
+// N bits from bit `at` on; `words` has at least one word more than those bits lie in, unless they end a word.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int n) {
+  const int s = at & 31;
+  const uint32_t lo = words[at >> 5], hi = s + n > 32 ? words[(at >> 5) + 1] : 0;
+  return __funnelshift_r(lo, hi, s) & ((1u << n) - 1);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_logit_rules(LogitArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
   extern __shared__ uint32_t table[];  // [chunk], then the bitmap [chunk / 32 + 1]
   __shared__ Shared sh;
   constexpr int N = Elem<T>::N;
@@ -91,6 +140,16 @@ __global__ void __launch_bounds__(kThreads) k_logit_rules(LogitArgs a) {
     sh.rep = r; sh.freq = f; sh.pres = p;
   }
   for (int k = t; k < a.chunk; k += kThreads) table[k] = 0;
+  if (t < 32) {  // the slots that are no pads, in order
+    int n = 0;
+    for (int i = i0; i < i1; i += 32) {
+      const bool live = i + t < i1 && (!a.tree_tok || a.tree_tok[(int64_t)b * a.slots + i + t] >= 0);
+      const uint32_t m = __ballot_sync(~0u, live);
+      if (live) sh.rows[n + __popc(m & ((1u << t) - 1))] = i + t;
+      n += __popc(m);
+    }
+    if (t == 0) sh.n_rows = n;
+  }
   __syncthreads();
   const bool counts = sh.rep != 1.f || sh.freq != 0.f || sh.pres != 0.f;
   const float* bias = a.r.d_bias_val + (int64_t)b * a.r.n_bias;
@@ -124,32 +183,85 @@ __global__ void __launch_bounds__(kThreads) k_logit_rules(LogitArgs a) {
     if ((t & 31) == 0) bitmap[k >> 5] = w;
   }
   __syncthreads();
-  for (int i = i0; i < i1; ++i) {
-    if (sh.tok[i] < 0) continue;
-    const int64_t row = (int64_t)b * a.slots + i;
-    const T* in = static_cast<const T*>(a.in) + row * a.in_stride + c0;
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + c0;
-    const uint32_t* gram = sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr;
-    for (int k = t; k < len; k += kThreads) {
-      float x = Elem<T>::get(in[k]);
-      if (table[k]) x = apply(a, sh, bias, table[k], i, c0 + k, x);
-      if (gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1)) x = -INFINITY;
-      out[k] = Elem<T>::put(x);
+  // one element: its rules, then the grammar
+  auto element = [&](int i, const uint32_t* gram, const T* in, T* out, int k) {
+    float x = Elem<T>::get(in[k]);
+    if (table[k]) x = apply(a, sh, bias, table[k], i, c0 + k, x);
+    if (gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1)) x = -INFINITY;
+    out[k] = Elem<T>::put(x);
+  };
+  constexpr int R = 4;  // rows in flight
+  const int n_rows = sh.n_rows;
+  for (int r0 = 0; r0 < n_rows; r0 += R) {
+    const T* in[R];
+    T* out[R];
+    const uint32_t* gram[R];
+    int slot[R], off[R], pieces[R], most = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      slot[r] = sh.rows[min(r0 + r, n_rows - 1)];
+      const int64_t row = (int64_t)b * a.slots + slot[r];
+      in[r] = static_cast<const T*>(a.in) + row * a.in_stride + c0;
+      out[r] = static_cast<T*>(a.out) + row * a.out_stride + c0;
+      gram[r] = sh.gram[slot[r]] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[slot[r]] * a.r.grammar_stride : nullptr;
+      const uint32_t from = (uint32_t)reinterpret_cast<uintptr_t>(in[r]) & 15, to = (uint32_t)reinterpret_cast<uintptr_t>(out[r]) & 15;
+      off[r] = from == to ? min(len, (int)(((16 - from) & 15) / sizeof(T))) : len;
+      pieces[r] = r0 + r < n_rows ? (len - off[r]) / N : 0;
+      most = max(most, pieces[r]);
+      // the elements around the pieces
+      const int loose = r0 + r < n_rows ? len - pieces[r] * N : 0;
+      for (int k = t; k < loose; k += kThreads)
+        element(slot[r], gram[r], in[r], out[r], k < off[r] ? k : k + pieces[r] * N);
+    }
+    for (int p = t; p < most; p += kThreads) {
+      uint4 x[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (p < pieces[r]) x[r] = __ldcs(reinterpret_cast<const uint4*>(in[r] + off[r] + p * N));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (p >= pieces[r]) continue;
+        const int k = off[r] + p * N;
+        uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        uint32_t ruled = bits_at(bitmap, k, N);
+        while (ruled) {
+          const int e = __ffs(ruled) - 1;
+          ruled &= ruled - 1;
+          Elem<T>::set(w, e, apply(a, sh, bias, table[k + e], slot[r], c0 + k + e, Elem<T>::at(w, e)));
+        }
+        if (gram[r]) Elem<T>::forbid(w, bits_at(gram[r], c0 + k, N));
+        __stcs(reinterpret_cast<uint4*>(out[r] + k), make_uint4(w[0], w[1], w[2], w[3]));
+      }
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_logit_rules(LogitArgs a, int dtype, int num_sms, cudaStream_t s) {
-  a.chunk = 4096;
-  const int chunks = (a.V + a.chunk - 1) / a.chunk;
-  a.rows_per_cta = a.slots;
-  const dim3 grid(chunks, a.batch, (a.slots + a.rows_per_cta - 1) / a.rows_per_cta);
-  const size_t smem = (size_t)a.chunk * 4 + (a.chunk / 32 + 1) * 4;
-  if (dtype == GRAFT_BF16) k_logit_rules<__nv_bfloat16><<<grid, kThreads, smem, s>>>(a);
-  else k_logit_rules<float><<<grid, kThreads, smem, s>>>(a);
+template <typename T>
+static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
+  // Every CTA reads the request's whole history: a chunk grows while that is more than an eighth of what its rows move
+  // and two CTAs an SM remain; rows are split, four at least, when the chunks alone give fewer than four.
+  const int pass = kThreads * Elem<T>::N;
+  a.chunk = pass;
+  auto ctas = [&](int chunk) { return (int64_t)a.batch * ((a.V + chunk - 1) / chunk); };
+  while (a.chunk < 32768 && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
+         ctas(2 * a.chunk) >= 2 * num_sms)
+    a.chunk *= 2;
+  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>((a.slots + 3) / 4, 4 * num_sms / ctas(a.chunk)));
+  a.rows_per_cta = (int)((a.slots + groups - 1) / groups);
+  const dim3 grid((a.V + a.chunk - 1) / a.chunk, a.batch, (a.slots + a.rows_per_cta - 1) / a.rows_per_cta);
+  const size_t smem = ((size_t)a.chunk + a.chunk / 32 + 1) * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k_logit_rules<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  k_logit_rules<T><<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s) {
+  return dtype == GRAFT_BF16 ? launch<__nv_bfloat16>(a, num_sms, s) : launch<float>(a, num_sms, s);
 }
 
 }  // namespace graft

@@ -16,6 +16,6 @@ struct LogitArgs {
   uint32_t* err;
 };
 
-cudaError_t launch_logit_rules(LogitArgs a, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s);
 
 }  // namespace graft

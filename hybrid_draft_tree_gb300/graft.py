@@ -222,36 +222,94 @@ def _rows(t, name, dtype, rows, vocab):
     return vp(t.data_ptr()), (t2.stride(0) if t2.shape[0] > 1 else max(t2.stride(0), t.shape[-1]))
 
 
-def _ptr32(t, name, numel):
-    return _buf(t, name, _dtypes("int32"), numel)
+# The calls that run once a layer take these shorter forms of the checks: what passes takes a handful of attribute
+# reads and yields the address, what does not goes to the checks above, which say what is wrong.
+class _Types:
+    """torch's dtypes by name, looked up once."""
+
+    def __getattr__(self, name):
+        import torch
+        v = (torch.int64, torch.uint64) if name == "mask" else getattr(torch, name)
+        setattr(self, name, v)
+        return v
+
+
+_T = _Types()
+
+
+def _addr(t, name, dtype, numel):
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _buf(t, name, (dtype,), numel).value
+
+
+def _mask_addr(t, name, numel):
+    return _addr(t, name, t.dtype if t is not None and getattr(t, "dtype", None) in _T.mask else _T.int64, numel)
+
+
+def _row_addr(t, name, dtype, rows, width):
+    """(address, row stride) of rows of `width` elements: see _rows."""
+    if t is None:
+        return None, width
+    try:
+        if t.dtype is dtype and t.is_cuda and t.dim() == 2:
+            (n, w), (stride, unit) = t.shape, t.stride()
+            if unit == 1 and w >= width and n >= rows and stride >= w:
+                return t.data_ptr(), stride
+    except AttributeError:
+        pass
+    p, stride = _rows(t, name, dtype, rows, width)
+    return p.value, stride
 
 
 def _table(t, name, dtype, rows):
-    """(pointer, row length) of a contiguous 2-d buffer of at least `rows` rows."""
+    """(address, row length) of a contiguous 2-d buffer of at least `rows` rows."""
     if t is None:
         return None, 0
     if not hasattr(t, "dim") or t.dim() != 2:
         raise GraftError(GRAFT_EINVAL, f"{name}: expected a 2-d torch tensor")
-    return _buf(t, name, _dtypes(dtype), rows * t.shape[1]), t.shape[1]
+    n = t.shape[1]
+    return _addr(t, name, dtype, rows * n), n
 
 
-def _cache(t, name, dtype, cfg):
-    """Pointer to a cache buffer: a tensor whose elements reach, from the
+def _cache_span(cfg):
+    """Elements from a cache's first to its last, by the handle's strides."""
+    return ((cfg.num_pages - 1) * cfg.page_stride + (cfg.kv_heads - 1) * cfg.head_stride +
+            (cfg.page_size - 1) * cfg.token_stride + cfg.head_dim)
+
+
+def _cache(t, name, dtype, span):
+    """Address of a cache buffer: a tensor whose elements reach, from the
     first to the last, as far as the handle's strides do."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= span:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not hasattr(t, "data_ptr") or not hasattr(t, "is_cuda"):
         raise GraftError(GRAFT_EINVAL, f"{name}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise GraftError(GRAFT_EINVAL, f"{name}: dtype {t.dtype}, the handle's cache is {dtype}")
-    span = ((cfg.num_pages - 1) * cfg.page_stride + (cfg.kv_heads - 1) * cfg.head_stride +
-            (cfg.page_size - 1) * cfg.token_stride + cfg.head_dim)
     held = sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
     if held < span:
         raise GraftError(GRAFT_EINVAL, f"{name}: {held} elements, the handle's pages reach {span}")
     if not _on_device(t):
         raise GraftError(GRAFT_EINVAL, f"{name}: expected a CUDA tensor (device buffer), got {t.device}")
-    return vp(t.data_ptr())
+    return t.data_ptr()
+
+
+def _stream_addr(stream):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _stream(stream):
@@ -422,24 +480,27 @@ class Graft:
         [batch, 3] (repetition, frequency, presence); bias_tok, bias_val:
         [batch, entries]; grammar: int32 [rows, >= ceil(V / 32)] bits;
         grammar_row: int32 [batch, slots].  A rule that is None is off."""
-        b, n = max(batch, 0), max(batch, 0) * slots
-        ldt, V = self._logits_dtype(), self.cfg.vocab
-        pl, stride = _rows(logits, "logits", ldt, n, V)
-        po, out_stride = _rows(out, "out", ldt, n, V)
+        b = max(batch, 0)
+        n, V, ldt, i32 = b * slots, self.cfg.vocab, self._logits_dtype(), _T.int32
+        pl, stride = _row_addr(logits, "logits", ldt, n, V)
+        po, out_stride = _row_addr(out, "out", ldt, n, V)
         r = graft_logit_rules()
-        r.d_hist, r.hist_stride = _table(hist, "hist", "int32", b)
-        r.d_hist_len = _ptr32(hist_len, "hist_len", b)
-        r.d_prompt_len = _ptr32(prompt_len, "prompt_len", b)
-        r.d_penalty = _buf(penalty, "penalty", _dtypes("float32"), 3 * b)
-        r.d_bias_tok, n_bias = _table(bias_tok, "bias_tok", "int32", b)
-        r.n_bias = n_bias
-        r.d_bias_val = _buf(bias_val, "bias_val", _dtypes("float32"), b * n_bias)
-        r.d_grammar, r.grammar_stride = _table(grammar, "grammar", "int32", 0)
-        r.n_grammar = 0 if grammar is None else grammar.shape[0]
-        r.d_grammar_row = _ptr32(grammar_row, "grammar_row", n)
-        self._check(self.L.graft_process_logits(self.h, batch, slots, _ptr32(tree_tok, "tree_tok", n),
-                                                _buf(tree_mask, "tree_mask", _dtypes("int64", "uint64"), n), pl, stride,
-                                                ctypes.byref(r), po, out_stride, _stream(stream)))
+        if hist is not None:
+            r.d_hist, r.hist_stride = _table(hist, "hist", i32, b)
+            r.d_hist_len = _addr(hist_len, "hist_len", i32, b)
+            r.d_prompt_len = _addr(prompt_len, "prompt_len", i32, b)
+        r.d_penalty = _addr(penalty, "penalty", _T.float32, 3 * b)
+        if bias_tok is not None:
+            r.d_bias_tok, n_bias = _table(bias_tok, "bias_tok", i32, b)
+            r.n_bias = n_bias
+            r.d_bias_val = _addr(bias_val, "bias_val", _T.float32, b * n_bias)
+        if grammar is not None:
+            r.d_grammar, r.grammar_stride = _table(grammar, "grammar", i32, 0)
+            r.n_grammar = grammar.shape[0]
+            r.d_grammar_row = _addr(grammar_row, "grammar_row", i32, n)
+        self._check(self.L.graft_process_logits(self.h, batch, slots, _addr(tree_tok, "tree_tok", i32, n),
+                                                _mask_addr(tree_mask, "tree_mask", n), pl, stride, ctypes.byref(r), po,
+                                                out_stride, _stream_addr(stream)))
 
     def get_matrix(self, stream=None) -> np.ndarray:
         out = np.empty((self.cfg.vocab, K), np.int32)
@@ -511,6 +572,10 @@ class GraftKV:
         self.L = load()
         self.cfg = cfg
         self.dtype = torch.float16 if cfg.dtype == GRAFT_F16 else torch.bfloat16
+        self.q_heads, self.page_size, self.rot_dim = cfg.q_heads, cfg.page_size, cfg.rot_dim
+        self.q_width, self.kv_width = cfg.q_heads * cfg.head_dim, cfg.kv_heads * cfg.head_dim
+        self.span = _cache_span(cfg)
+        self.scale = cfg.head_dim ** -0.5 if cfg.head_dim > 0 else 1.0
         h = vp()
         rc = self.L.graft_kv_init(ctypes.byref(cfg), ctypes.byref(h))
         if rc != GRAFT_OK:
@@ -539,39 +604,40 @@ class GraftKV:
         [batch * slots, heads * head_dim], any row stride; rope: float32
         [positions, rot_dim]; page_table: int32 [batch, pages]; pos: the slots'
         depths (tree_pos); rows: int32 [batch, slots], the slot each place takes."""
-        c, n, b = self.cfg, max(batch, 0) * slots, max(batch, 0)
-        kw, qw = c.kv_heads * c.head_dim, c.q_heads * c.head_dim
-        pq, qs = _rows(q, "q", self.dtype, n, qw)
-        pk, ks = _rows(k, "k", self.dtype, n, kw)
-        pv, vs = _rows(v, "v", self.dtype, n, kw)
-        po, qos = _rows(q_out, "q_out", self.dtype, n, qw)
-        pr, width = _table(rope, "rope", "float32", 0)
-        if rope is not None and width != c.rot_dim:
-            raise GraftError(GRAFT_EINVAL, f"rope: rows of {width}, the handle rotates {c.rot_dim}")
-        pt, ts = _table(page_table, "page_table", "int32", b)
-        self._check(self.L.graft_kv_append(self.h, batch, slots, pq, qs, pk, ks, pv, vs, _ptr32(pos, "pos", n),
-                                           _ptr32(rows, "rows", n), pr, 0 if rope is None else rope.shape[0], prefix_len,
-                                           pt, ts, _ptr32(ctx_len, "ctx_len", b), po, qos,
-                                           _cache(k_cache, "k_cache", self.dtype, c),
-                                           _cache(v_cache, "v_cache", self.dtype, c), _stream(stream)))
+        b, dt, i32 = max(batch, 0), self.dtype, _T.int32
+        n = b * slots
+        pq, qs = _row_addr(q, "q", dt, n, self.q_width)
+        pk, ks = _row_addr(k, "k", dt, n, self.kv_width)
+        pv, vs = _row_addr(v, "v", dt, n, self.kv_width)
+        po, qos = _row_addr(q_out, "q_out", dt, n, self.q_width)
+        pr, width = _table(rope, "rope", _T.float32, 0)
+        if rope is not None and width != self.rot_dim:
+            raise GraftError(GRAFT_EINVAL, f"rope: rows of {width}, the handle rotates {self.rot_dim}")
+        pt, ts = _table(page_table, "page_table", i32, b)
+        self._check(self.L.graft_kv_append(self.h, batch, slots, pq, qs, pk, ks, pv, vs, _addr(pos, "pos", i32, n),
+                                           _addr(rows, "rows", i32, n), pr, 0 if rope is None else rope.shape[0],
+                                           prefix_len, pt, ts, _addr(ctx_len, "ctx_len", i32, b), po, qos,
+                                           _cache(k_cache, "k_cache", dt, self.span),
+                                           _cache(v_cache, "v_cache", dt, self.span), _stream_addr(stream)))
 
     def attend(self, batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages=None,
                prefix_len=0, tree_mask=None, scale=None, lse=None, stream=None):
         """Attention of the slots' rotated queries over the prefix, each
         request's ctx_len (<= max_ctx) tokens and the tree under tree_mask
         (None: causal), into out and lse.  scale defaults to head_dim ** -0.5."""
-        c, n, b = self.cfg, max(batch, 0) * slots, max(batch, 0)
-        qw = c.q_heads * c.head_dim
-        pq, qs = _rows(q, "q", self.dtype, n, qw)
-        po, os_ = _rows(out, "out", self.dtype, n, qw)
-        pt, ts = _table(page_table, "page_table", "int32", b)
-        self._check(self.L.graft_kv_attend(self.h, batch, slots, pq, qs, _cache(k_cache, "k_cache", self.dtype, c),
-                                           _cache(v_cache, "v_cache", self.dtype, c),
-                                           _ptr32(prefix_pages, "prefix_pages", -(-max(prefix_len, 0) // c.page_size)),
-                                           prefix_len, pt, ts, _ptr32(ctx_len, "ctx_len", b), max_ctx,
-                                           _buf(tree_mask, "tree_mask", _dtypes("int64", "uint64"), n),
-                                           ctypes.c_float(c.head_dim ** -0.5 if scale is None else scale), po, os_,
-                                           _buf(lse, "lse", _dtypes("float32"), n * c.q_heads), _stream(stream)))
+        b, dt, i32 = max(batch, 0), self.dtype, _T.int32
+        n = b * slots
+        pq, qs = _row_addr(q, "q", dt, n, self.q_width)
+        po, os_ = _row_addr(out, "out", dt, n, self.q_width)
+        pt, ts = _table(page_table, "page_table", i32, b)
+        pages = -(-max(prefix_len, 0) // self.page_size)
+        self._check(self.L.graft_kv_attend(self.h, batch, slots, pq, qs, _cache(k_cache, "k_cache", dt, self.span),
+                                           _cache(v_cache, "v_cache", dt, self.span),
+                                           _addr(prefix_pages, "prefix_pages", i32, pages), prefix_len, pt, ts,
+                                           _addr(ctx_len, "ctx_len", i32, b), max_ctx,
+                                           _mask_addr(tree_mask, "tree_mask", n),
+                                           self.scale if scale is None else scale, po, os_,
+                                           _addr(lse, "lse", _T.float32, n * self.q_heads), _stream_addr(stream)))
 
     def sync(self, stream=None, raise_on_error=True) -> int:
         flags = ctypes.c_uint32(0)
