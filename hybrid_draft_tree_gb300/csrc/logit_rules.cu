@@ -2,11 +2,13 @@
 //
 // A CTA takes one chunk of one request's vocabulary and some of its slots'
 // rows.  It builds the chunk's rule table in shared memory once (occurrences in
-// the history, the bias entry, whether a slot's token falls there) and streams
-// the rows past it, so that the history is read once a chunk and not once a
-// row.  Nearly every element has no rule: a bitmap tells which 16-byte pieces
-// hold one that has, and the others are copied as they are, or masked by their
-// bits of the grammar's row.  Bound by memory: a row is read and written once.
+// the history, the bias entry, whether a slot's token falls there), so that the
+// history is read once a chunk and not once a row, and turns it into what an
+// element with a rule needs: what is taken off its logit, and whether it counts
+// as seen.  Then its warps stream the rows past the table, four 16-byte pieces
+// a lane at a time.  Nearly every element has no rule: a bitmap tells which
+// pieces hold one that has, and the others are copied, or masked by their bits
+// of the grammar's row.  Bound by memory: a row is read and written once.
 //
 // Rows need not start on 16-byte boundaries: the pieces are those of the row's
 // own alignment, so the table and the bits are read at the row's offset, and
@@ -20,12 +22,17 @@
 namespace graft {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kUnit = 128;                  // pieces a warp takes at a time: four a lane
+// a table entry while the rules are gathered
 constexpr uint32_t COUNT = (1u << 19) - 1;  // occurrences in the output (the history is shorter than 2^19)
 constexpr uint32_t PROMPT = 1u << 19;       // seen in the prompt
 constexpr int BIAS_SHIFT = 20;              // index of the bias entry + 1, 11 bits
 constexpr uint32_t BIAS = 0x7FFu << BIAS_SHIFT;
 constexpr uint32_t TREE = 1u << 31;         // the token of a slot
+// and then: the fp32 number taken off the logit, its lowest bit 1 for a token that was seen; or this NaN with the index
+// of a token that some slots' paths hold, whose count depends on the slot
+constexpr uint32_t PATH = 0xFFC00000u;
 
 // Elements in the words of a 16-byte piece.
 template <typename T>
@@ -43,7 +50,7 @@ struct Elem<float> {
     for (int i = 0; i < 4; ++i) w[i] = i == e ? __float_as_uint(x) : w[i];
   }
   // words of elements whose bit of `allowed` is 0 become -inf
-  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed) {
+  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed, const uint2*) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = (allowed >> i) & 1 ? w[i] : 0xFF800000u;
   }
@@ -65,12 +72,12 @@ struct Elem<__nv_bfloat16> {
       w[i] = i == e >> 1 ? n : w[i];
     }
   }
-  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed) {
+  // spread[b]: the words' masks of four elements' bits b
+  static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed, const uint2* spread) {
+    const uint2 lo = spread[allowed & 15], hi = spread[allowed >> 4];
+    const uint32_t m[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = ((allowed >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
-      w[i] = (w[i] & m) | (0xFF80FF80u & ~m);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = (w[i] & m[i]) | (0xFF80FF80u & ~m[i]);
   }
 };
 
@@ -79,28 +86,35 @@ struct Shared {
   int32_t tok[MAX_S];       // tokens of the slots, -1 = pad
   int32_t gram[MAX_S];      // grammar row, -1 = all allowed
   int32_t rows[MAX_S];      // the CTA's slots that are no pads
-  int32_t n_rows;
-  float rep, freq, pres;
+  uint32_t path_word[MAX_S]; // gathered entries of the tokens that some paths hold
+  uint2 spread[16];
+  int32_t n_rows, n_paths;
+  float rep, inv_rep, freq, pres;
 };
 
-// The rules of one element: word = its table entry, i = the slot.
-__device__ __forceinline__ float apply(const LogitArgs& a, const Shared& sh, const float* bias, uint32_t word, int i,
-                                       int v, float x) {
-  int n = word & COUNT;
-  if (word & TREE) {
-    uint64_t m = sh.path[i];
-    while (m) {
-      const int j = __ffsll((long long)m) - 1;
-      m &= m - 1;
-      n += sh.tok[j] == v;
-    }
-  }
-  if (n > 0 || (word & PROMPT)) x = x > 0.f ? x / sh.rep : x * sh.rep;
-  x -= sh.freq * (float)n;
-  if (n > 0) x -= sh.pres;
+// What a gathered entry takes off a logit, for a token with n occurrences.  The quotient by the repetition penalty is a
+// product with its fp32 reciprocal and the differences are taken at once: a few fp32 roundings, far below the type's.
+__device__ __forceinline__ float taken(const Shared& sh, const float* bias, uint32_t word, int n) {
+  float x = sh.freq * (float)n;
+  if (n > 0) x += sh.pres;
   const uint32_t e = (word & BIAS) >> BIAS_SHIFT;
-  if (e) x += bias[e - 1];
+  if (e) x -= bias[e - 1];
   return x;
+}
+
+// An element with a rule; i = the slot.
+__device__ __forceinline__ float apply(const Shared& sh, const float* bias, uint32_t entry, int i, int v, float x) {
+  bool seen = entry & 1;
+  float off = __uint_as_float(entry);
+  if (entry >= PATH) {
+    const uint32_t word = sh.path_word[entry - PATH];
+    int n = word & COUNT;
+    for (uint64_t m = sh.path[i]; m; m &= m - 1) n += sh.tok[__ffsll((long long)m) - 1] == v;
+    seen = n > 0 || (word & PROMPT);
+    off = taken(sh, bias, word, n);
+  }
+  if (seen) x *= x > 0.f ? sh.inv_rep : sh.rep;
+  return x - off;
 }
 
 // N bits from bit `at` on; `words` has at least one word more than those bits lie in, unless they end a word.
@@ -137,8 +151,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
       r = a.r.d_penalty[3 * b]; f = a.r.d_penalty[3 * b + 1]; p = a.r.d_penalty[3 * b + 2];
       if (!(r > 0.f) || !isfinite(r) || !isfinite(f) || !isfinite(p)) { bad |= GRAFT_ERR_RULE; r = 1.f; f = p = 0.f; }
     }
-    sh.rep = r; sh.freq = f; sh.pres = p;
+    sh.rep = r; sh.inv_rep = 1.f / r; sh.freq = f; sh.pres = p;
+    sh.n_paths = 0;
   }
+  if (t < 16) sh.spread[t] = make_uint2((t & 1 ? 0xFFFFu : 0u) | (t & 2 ? 0xFFFF0000u : 0u), (t & 4 ? 0xFFFFu : 0u) | (t & 8 ? 0xFFFF0000u : 0u));
   for (int k = t; k < a.chunk; k += kThreads) table[k] = 0;
   if (t < 32) {  // the slots that are no pads, in order
     int n = 0;
@@ -179,59 +195,69 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
   if (bad) atomicOr(a.err, bad);
   __syncthreads();
   for (int k = t; k < a.chunk + 32; k += kThreads) {
-    const uint32_t w = __ballot_sync(~0u, k < a.chunk && table[k < a.chunk ? k : 0] != 0);
-    if ((t & 31) == 0) bitmap[k >> 5] = w;
+    const uint32_t word = k < a.chunk ? table[k] : 0;
+    const uint32_t ruled = __ballot_sync(~0u, word != 0);
+    if ((t & 31) == 0) bitmap[k >> 5] = ruled;
+    if (word == 0) continue;
+    uint32_t entry;
+    if (word & TREE) {
+      const int at = atomicAdd(&sh.n_paths, 1);
+      sh.path_word[at] = word;
+      entry = PATH + at;
+    } else {
+      const int n = word & COUNT;
+      const float off = taken(sh, bias, word, n);
+      entry = isnan(off) ? 0x7FC00000u : __float_as_uint(off) & ~1u;
+      if (n > 0 || (word & PROMPT)) entry |= 1;
+    }
+    table[k] = entry;
   }
   __syncthreads();
-  // one element: its rules, then the grammar
-  auto element = [&](int i, const uint32_t* gram, const T* in, T* out, int k) {
-    float x = Elem<T>::get(in[k]);
-    if (table[k]) x = apply(a, sh, bias, table[k], i, c0 + k, x);
-    if (gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1)) x = -INFINITY;
-    out[k] = Elem<T>::put(x);
-  };
-  constexpr int R = 4;  // rows in flight
-  const int n_rows = sh.n_rows;
-  for (int r0 = 0; r0 < n_rows; r0 += R) {
-    const T* in[R];
-    T* out[R];
-    const uint32_t* gram[R];
-    int slot[R], off[R], pieces[R], most = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      slot[r] = sh.rows[min(r0 + r, n_rows - 1)];
-      const int64_t row = (int64_t)b * a.slots + slot[r];
-      in[r] = static_cast<const T*>(a.in) + row * a.in_stride + c0;
-      out[r] = static_cast<T*>(a.out) + row * a.out_stride + c0;
-      gram[r] = sh.gram[slot[r]] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[slot[r]] * a.r.grammar_stride : nullptr;
-      const uint32_t from = (uint32_t)reinterpret_cast<uintptr_t>(in[r]) & 15, to = (uint32_t)reinterpret_cast<uintptr_t>(out[r]) & 15;
-      off[r] = from == to ? min(len, (int)(((16 - from) & 15) / sizeof(T))) : len;
-      pieces[r] = r0 + r < n_rows ? (len - off[r]) / N : 0;
-      most = max(most, pieces[r]);
-      // the elements around the pieces
-      const int loose = r0 + r < n_rows ? len - pieces[r] * N : 0;
-      for (int k = t; k < loose; k += kThreads)
-        element(slot[r], gram[r], in[r], out[r], k < off[r] ? k : k + pieces[r] * N);
+  const int lane = t & 31, units = a.chunk / (kUnit * N), n_rows = sh.n_rows;
+  for (int u = t >> 5; u < n_rows * units; u += kWarps) {
+    const int r = u / units, part = u - r * units, i = sh.rows[r];
+    const int64_t row = (int64_t)b * a.slots + i;
+    const T* in = static_cast<const T*>(a.in) + row * a.in_stride + c0;
+    T* out = static_cast<T*>(a.out) + row * a.out_stride + c0;
+    const uint32_t* gram = sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr;
+    auto element = [&](int k) {
+      float x = Elem<T>::get(in[k]);
+      if ((bitmap[k >> 5] >> (k & 31)) & 1) x = apply(sh, bias, table[k], i, c0 + k, x);
+      if (gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1)) x = -INFINITY;
+      out[k] = Elem<T>::put(x);
+    };
+    const uint32_t from = (uint32_t)reinterpret_cast<uintptr_t>(in) & 15, to = (uint32_t)reinterpret_cast<uintptr_t>(out) & 15;
+    if (from != to) {
+      for (int k = part * kUnit * N + lane; k < min(len, (part + 1) * kUnit * N); k += 32) element(k);
+      continue;
     }
-    for (int p = t; p < most; p += kThreads) {
-      uint4 x[R];
+    const int off = min(len, (int)(((16 - from) & 15) / sizeof(T))), pieces = (len - off) / N;
+    if (part == 0)
+      for (int k = lane; k < len - pieces * N; k += 32) element(k < off ? k : k + pieces * N);
+    const int p0 = part * kUnit + lane;
+    const uint4* src = reinterpret_cast<const uint4*>(in + off) + p0;
+    uint4* dst = reinterpret_cast<uint4*>(out + off) + p0;
+    uint4 x[4];
+    uint32_t allowed[4];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (p < pieces[r]) x[r] = __ldcs(reinterpret_cast<const uint4*>(in[r] + off[r] + p * N));
+    for (int j = 0; j < 4; ++j)
+      if (p0 + 32 * j < pieces) x[j] = __ldcs(src + 32 * j);
+    const int k0 = off + p0 * N;
+    if (gram) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (p >= pieces[r]) continue;
-        const int k = off[r] + p * N;
-        uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-        uint32_t ruled = bits_at(bitmap, k, N);
-        while (ruled) {
-          const int e = __ffs(ruled) - 1;
-          ruled &= ruled - 1;
-          Elem<T>::set(w, e, apply(a, sh, bias, table[k + e], slot[r], c0 + k + e, Elem<T>::at(w, e)));
-        }
-        if (gram[r]) Elem<T>::forbid(w, bits_at(gram[r], c0 + k, N));
-        __stcs(reinterpret_cast<uint4*>(out[r] + k), make_uint4(w[0], w[1], w[2], w[3]));
+      for (int j = 0; j < 4; ++j) allowed[j] = p0 + 32 * j < pieces ? bits_at(gram, c0 + k0 + 32 * N * j, N) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (p0 + 32 * j >= pieces) break;
+      const int k = k0 + 32 * N * j;
+      uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      for (uint32_t ruled = bits_at(bitmap, k, N); ruled; ruled &= ruled - 1) {
+        const int e = __ffs(ruled) - 1;
+        Elem<T>::set(w, e, apply(sh, bias, table[k + e], i, c0 + k + e, Elem<T>::at(w, e)));
       }
+      if (gram) Elem<T>::forbid(w, allowed[j], sh.spread);
+      __stcs(dst + 32 * j, make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
