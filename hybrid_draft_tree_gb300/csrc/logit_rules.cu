@@ -5,14 +5,17 @@
 // the history, the bias entry, whether a slot's token falls there), so that the
 // history is read once a chunk and not once a row, and turns it into what an
 // element with a rule needs: what is taken off its logit, and whether it counts
-// as seen.  Then its warps stream the rows past the table, four 16-byte pieces
-// a lane at a time.  Nearly every element has no rule: a bitmap tells which
-// pieces hold one that has, and the others are copied, or masked by their bits
-// of the grammar's row.  Bound by memory: a row is read and written once.
+// as seen.  Then its warps take the rows in units of four 16-byte pieces a lane.
+// Nearly every element has no rule: a unit is masked by its bits of the
+// grammar's row and stored; when some of its elements have rules, it passes
+// through shared memory, where they are done a lane each (in the pieces they
+// would cost the whole warp a pass for each of a lane's).  Bound by memory: a
+// row is read and written once; in place, units without a rule or a grammar are
+// not touched.
 //
 // Rows need not start on 16-byte boundaries: the pieces are those of the row's
-// own alignment, so the table and the bits are read at the row's offset, and
-// the few elements before its first and after its last piece go one by one.
+// own alignment, so the bits are read at the row's offset, and the few elements
+// before its first and after its last piece go one by one.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -23,7 +26,7 @@ namespace graft {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kUnit = 128;                  // pieces a warp takes at a time: four a lane
+constexpr int kLane = 4, kUnit = 32 * kLane; // pieces that a lane, a warp takes at a time
 // a table entry while the rules are gathered
 constexpr uint32_t COUNT = (1u << 19) - 1;  // occurrences in the output (the history is shorter than 2^19)
 constexpr uint32_t PROMPT = 1u << 19;       // seen in the prompt
@@ -34,7 +37,7 @@ constexpr uint32_t TREE = 1u << 31;         // the token of a slot
 // of a token that some slots' paths hold, whose count depends on the slot
 constexpr uint32_t PATH = 0xFFC00000u;
 
-// Elements in the words of a 16-byte piece.
+// Elements and 16-byte pieces of them.
 template <typename T>
 struct Elem;
 template <>
@@ -42,13 +45,6 @@ struct Elem<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ float get(float x) { return x; }
   static __device__ __forceinline__ float put(float x) { return x; }
-  static __device__ __forceinline__ float at(const uint32_t* w, int e) {
-    return __uint_as_float(e & 2 ? (e & 1 ? w[3] : w[2]) : (e & 1 ? w[1] : w[0]));
-  }
-  static __device__ __forceinline__ void set(uint32_t* w, int e, float x) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = i == e ? __float_as_uint(x) : w[i];
-  }
   // words of elements whose bit of `allowed` is 0 become -inf
   static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed, const uint2*) {
 #pragma unroll
@@ -60,21 +56,9 @@ struct Elem<__nv_bfloat16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-  static __device__ __forceinline__ float at(const uint32_t* w, int e) {
-    const uint32_t x = e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0]);
-    return __uint_as_float(e & 1 ? x & 0xFFFF0000u : x << 16);
-  }
-  static __device__ __forceinline__ void set(uint32_t* w, int e, float x) {
-    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t n = e & 1 ? (w[i] & 0xFFFFu) | h << 16 : (w[i] & 0xFFFF0000u) | h;
-      w[i] = i == e >> 1 ? n : w[i];
-    }
-  }
   // spread[b]: the words' masks of four elements' bits b
   static __device__ __forceinline__ void forbid(uint32_t* w, uint32_t allowed, const uint2* spread) {
-    const uint2 lo = spread[allowed & 15], hi = spread[allowed >> 4];
+    const uint2 lo = spread[allowed & 15], hi = spread[(allowed >> 4) & 15];
     const uint32_t m[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = (w[i] & m[i]) | (0xFF80FF80u & ~m[i]);
@@ -126,13 +110,17 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int n
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
-  extern __shared__ uint32_t table[];  // [chunk], then the bitmap [chunk / 32 + 1]
+  extern __shared__ uint4 space[];  // a unit a warp; the table [chunk]; bitmap, ranks [chunk / 32 + 1]; the list [chunk] of 16 bits
   __shared__ Shared sh;
   constexpr int N = Elem<T>::N;
   const int b = blockIdx.y, t = threadIdx.x;
   const int c0 = blockIdx.x * a.chunk, c1 = min(a.V, c0 + a.chunk), len = c1 - c0;
   const int i0 = blockIdx.z * a.rows_per_cta, i1 = min(a.slots, i0 + a.rows_per_cta);
-  uint32_t* bitmap = table + a.chunk;
+  uint4* const stage = space + (t >> 5) * kUnit;
+  uint32_t* const table = reinterpret_cast<uint32_t*>(space + kWarps * kUnit);
+  uint32_t* const bitmap = table + a.chunk;            // elements with a rule
+  uint32_t* const ranks = bitmap + a.chunk / 32 + 1;   // how many lie before a word of the bitmap
+  uint16_t* const list = reinterpret_cast<uint16_t*>(ranks + a.chunk / 32 + 1);  // they, in order
   uint32_t bad = 0;
   // the slots, the request's penalties
   if (t < a.slots) {
@@ -194,16 +182,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
     atomicOr(&table[sh.tok[t] - c0], TREE);
   if (bad) atomicOr(a.err, bad);
   __syncthreads();
-  for (int k = t; k < a.chunk + 32; k += kThreads) {
-    const uint32_t word = k < a.chunk ? table[k] : 0;
-    const uint32_t ruled = __ballot_sync(~0u, word != 0);
-    if ((t & 31) == 0) bitmap[k >> 5] = ruled;
+  const int lane = t & 31, words = a.chunk / 32;
+  for (int k = t; k < a.chunk; k += kThreads) {
+    const uint32_t word = table[k], ruled = __ballot_sync(~0u, word != 0);
+    if (lane == 0) bitmap[k >> 5] = ruled;
     if (word == 0) continue;
     uint32_t entry;
     if (word & TREE) {
-      const int at = atomicAdd(&sh.n_paths, 1);
-      sh.path_word[at] = word;
-      entry = PATH + at;
+      const int path = atomicAdd(&sh.n_paths, 1);
+      sh.path_word[path] = word;
+      entry = PATH + path;
     } else {
       const int n = word & COUNT;
       const float off = taken(sh, bias, word, n);
@@ -212,19 +200,41 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
     }
     table[k] = entry;
   }
+  if (t == 0) bitmap[words] = 0;
   __syncthreads();
-  const int lane = t & 31, units = a.chunk / (kUnit * N), n_rows = sh.n_rows;
+  if (t < 32) {
+    uint32_t n = 0;
+    for (int w = lane; w < (words / 32 + 1) * 32; w += 32) {
+      const uint32_t mine = w < words ? __popc(bitmap[w]) : 0;
+      uint32_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (w <= words) ranks[w] = n + upto - mine;
+      n += __shfl_sync(~0u, upto, 31);
+    }
+  }
+  __syncthreads();
+  auto rank = [&](int k) { return (int)(ranks[k >> 5] + __popc(bitmap[k >> 5] & ((1u << (k & 31)) - 1))); };
+  for (int k = t; k < a.chunk; k += kThreads)
+    if ((bitmap[k >> 5] >> (k & 31)) & 1) list[rank(k)] = (uint16_t)k;
+  __syncthreads();
+
+  const int n_rows = sh.n_rows, units = a.chunk / (kUnit * N);
+  const bool in_place = a.in == a.out;
   for (int u = t >> 5; u < n_rows * units; u += kWarps) {
     const int r = u / units, part = u - r * units, i = sh.rows[r];
     const int64_t row = (int64_t)b * a.slots + i;
     const T* in = static_cast<const T*>(a.in) + row * a.in_stride + c0;
     T* out = static_cast<T*>(a.out) + row * a.out_stride + c0;
     const uint32_t* gram = sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr;
+    auto forbidden = [&](int k) { return gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1); };
     auto element = [&](int k) {
-      float x = Elem<T>::get(in[k]);
-      if ((bitmap[k >> 5] >> (k & 31)) & 1) x = apply(sh, bias, table[k], i, c0 + k, x);
-      if (gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1)) x = -INFINITY;
-      out[k] = Elem<T>::put(x);
+      if (forbidden(k)) out[k] = Elem<T>::put(-INFINITY);
+      else if ((bitmap[k >> 5] >> (k & 31)) & 1) out[k] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(in[k])));
+      else out[k] = in[k];
     };
     const uint32_t from = (uint32_t)reinterpret_cast<uintptr_t>(in) & 15, to = (uint32_t)reinterpret_cast<uintptr_t>(out) & 15;
     if (from != to) {
@@ -234,31 +244,48 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
     const int off = min(len, (int)(((16 - from) & 15) / sizeof(T))), pieces = (len - off) / N;
     if (part == 0)
       for (int k = lane; k < len - pieces * N; k += 32) element(k < off ? k : k + pieces * N);
-    const int p0 = part * kUnit + lane;
-    const uint4* src = reinterpret_cast<const uint4*>(in + off) + p0;
-    uint4* dst = reinterpret_cast<uint4*>(out + off) + p0;
-    uint4 x[4];
-    uint32_t allowed[4];
+    const int k0 = off + min(pieces, part * kUnit) * N, k1 = off + min(pieces, (part + 1) * kUnit) * N;  // of the unit
+    const int e0 = rank(k0), e1 = rank(k1);
+    if (in_place && !gram) {
+      for (int e = e0 + lane; e < e1; e += 32) element(list[e]);
+      continue;
+    }
+    const int n = (k1 - k0) / N;
+    const uint4* src = reinterpret_cast<const uint4*>(in + k0);
+    uint4* dst = reinterpret_cast<uint4*>(out + k0);
+    uint4 x[kLane];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (p0 + 32 * j < pieces) x[j] = __ldcs(src + 32 * j);
-    const int k0 = off + p0 * N;
+    for (int j = 0; j < kLane; ++j) x[j] = lane + 32 * j < n ? __ldcs(src + lane + 32 * j) : make_uint4(0, 0, 0, 0);
     if (gram) {
+      uint32_t allowed[kLane];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) allowed[j] = p0 + 32 * j < pieces ? bits_at(gram, c0 + k0 + 32 * N * j, N) : 0;
-    }
+      for (int j = 0; j < kLane; ++j)
+        allowed[j] = lane + 32 * j < n ? bits_at(gram, c0 + k0 + (lane + 32 * j) * N, N) : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (p0 + 32 * j >= pieces) break;
-      const int k = k0 + 32 * N * j;
-      uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-      for (uint32_t ruled = bits_at(bitmap, k, N); ruled; ruled &= ruled - 1) {
-        const int e = __ffs(ruled) - 1;
-        Elem<T>::set(w, e, apply(sh, bias, table[k + e], i, c0 + k + e, Elem<T>::at(w, e)));
+      for (int j = 0; j < kLane; ++j) {
+        uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        Elem<T>::forbid(w, allowed[j], sh.spread);
+        x[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (gram) Elem<T>::forbid(w, allowed[j], sh.spread);
-      __stcs(dst + 32 * j, make_uint4(w[0], w[1], w[2], w[3]));
     }
+    if (e0 < e1) {
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) stage[lane + 32 * j] = x[j];
+      __syncwarp();
+      T* const values = reinterpret_cast<T*>(stage);
+      for (int e = e0 + lane; e < e1; e += 32) {
+        const int k = list[e];
+        // what the grammar forbids is -inf already, and stays so whatever its rule takes off
+        if (!forbidden(k)) values[k - k0] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(values[k - k0])));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) x[j] = stage[lane + 32 * j];
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < kLane; ++j)
+      if (lane + 32 * j < n) __stcs(dst + lane + 32 * j, x[j]);
   }
 }
 
@@ -271,13 +298,13 @@ static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
   const int pass = kThreads * Elem<T>::N;
   a.chunk = pass;
   auto ctas = [&](int chunk) { return (int64_t)a.batch * ((a.V + chunk - 1) / chunk); };
-  while (a.chunk < 32768 && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
+  while (a.chunk < 16384 && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
          ctas(2 * a.chunk) >= 2 * num_sms)
     a.chunk *= 2;
   const int64_t groups = std::max<int64_t>(1, std::min<int64_t>((a.slots + 3) / 4, 4 * num_sms / ctas(a.chunk)));
   a.rows_per_cta = (int)((a.slots + groups - 1) / groups);
   const dim3 grid((a.V + a.chunk - 1) / a.chunk, a.batch, (a.slots + a.rows_per_cta - 1) / a.rows_per_cta);
-  const size_t smem = ((size_t)a.chunk + a.chunk / 32 + 1) * 4;
+  const size_t smem = kWarps * kUnit * 16 + (size_t)a.chunk * 6 + 2 * (a.chunk / 32 + 1) * 4;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_logit_rules<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
