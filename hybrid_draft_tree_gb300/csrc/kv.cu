@@ -224,6 +224,9 @@ int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
                       (!d_q || (!misaligned(d_q, 16) && !misaligned(d_q_out, 16) && q_stride % 8 == 0 &&
                                 q_out_stride % 8 == 0));
   a.vec = rows16 && c.rot % (c.interleaved ? 8 : 16) == 0 && !misaligned(d_rope, 16);
+  a.by_slots = graft::Divisor(slots);
+  a.by_turn = graft::Divisor(c.dim / 8 - (c.interleaved ? 0 : c.rot / 16));
+  a.by_value = graft::Divisor(c.dim / 8);
   const cudaError_t e = graft::launch_kv_append(a, h->cfg.dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_append launch");
   h->last_launches = 1;

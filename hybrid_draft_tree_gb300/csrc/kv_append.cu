@@ -11,36 +11,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Where token (b, i) comes from and goes to.  Its source rows are known before its place: their loads do not wait for
+// the page table.  Bad data sets the error bit and drops the write.
 struct Token {
-  int64_t k_src, q_row;  // source row of the key and value (-1: none), row of the query (-1: a pad)
   int64_t dst;           // element offset of the place's first head in the caches
-  int32_t k_pos, q_pos;
+  int32_t k_pos, q_pos;  // positions, -1: no key and value to write, no query
 };
 
-// Where token (b, i) comes from and goes to; bad data sets the error bit and drops the write.
-__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i) {
-  Token t{-1, -1, 0, 0, 0};
+__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r) {
+  Token t{0, -1, -1};
   const int64_t first = (int64_t)b * a.slots;
   const int64_t ctx = a.ctx_len[b];
   const int64_t base = a.prefix_len + ctx;
-  const int64_t limit = a.c.rot > 0 ? a.rope_len : INT64_MAX;
-  uint32_t bad = ctx < 0 ? GRAFT_ERR_RANGE : 0;
-  if (!bad && a.q) {
+  const int64_t limit = a.c.rot > 0 ? a.rope_len : INT32_MAX;
+  uint32_t bad = ctx < 0 || r >= a.slots ? GRAFT_ERR_RANGE : 0;
+  if (ctx >= 0 && a.q) {
     const int32_t d = a.depth ? a.depth[first + i] : i;
-    if (d >= 0) {
-      if (base + d < limit) { t.q_row = first + i; t.q_pos = (int32_t)(base + d); }
-      else bad = GRAFT_ERR_RANGE;
-    }
+    if (d >= 0 && base + d >= limit) bad = GRAFT_ERR_RANGE;
+    else if (d >= 0) t.q_pos = (int32_t)(base + d);
   }
-  const int32_t r = a.rows ? a.rows[first + i] : i;
-  if (ctx >= 0 && r >= a.slots) bad = GRAFT_ERR_RANGE;
-  else if (ctx >= 0 && r >= 0) {
+  if (ctx >= 0 && r >= 0 && r < a.slots) {
     const int32_t d = a.depth ? a.depth[first + r] : r;
     if (d >= 0) {
       const int64_t at = ctx + i, p = at >> a.c.page_shift;
       const int32_t page = p < a.table_stride ? a.page_table[(int64_t)b * a.table_stride + p] : -1;
       if (page >= 0 && page < a.c.num_pages && base + d < limit) {
-        t.k_src = first + r;
         t.k_pos = (int32_t)(base + d);
         t.dst = page * a.c.page_stride + (at & (a.c.page_size - 1)) * a.c.token_stride;
       } else {
@@ -52,52 +47,36 @@ __device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i) {
   return t;
 }
 
-// One head in 16-byte pieces: piece u < rot / 16 of the halves form turns with
-// its partner rot / 16 pieces on (two loads, two stores); of the interleaved
-// form each piece turns within itself; the rest is copied.
+// 16-byte pieces of a head.  Halves form: piece u < rot / 16 turns with its partner rot / 16 pieces on; interleaved form:
+// a piece turns within itself; the rest is copied.  x: the piece, y: its partner.
 template <typename T>
-__device__ __forceinline__ void head_piece(const AppendArgs& a, const T* src, T* dst, const float* cs, int u) {
-  const int half = a.c.rot >> 1;
-  if (!a.c.interleaved) {
-    const int pairs = half >> 3;
-    if (u >= pairs) {
-      const int at = (u + pairs) << 3;
-      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
-      return;
-    }
-    const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
-    const uint4 y = *reinterpret_cast<const uint4*>(src + half + 8 * u);
-    const float4 c0 = *reinterpret_cast<const float4*>(cs + 8 * u), c1 = *reinterpret_cast<const float4*>(cs + 8 * u + 4);
-    const float4 s0 = *reinterpret_cast<const float4*>(cs + half + 8 * u);
-    const float4 s1 = *reinterpret_cast<const float4*>(cs + half + 8 * u + 4);
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    uint32_t ow[4], pw[4];
+__device__ __forceinline__ void turn_halves(const float* cs, int half, int u, uint4& x, uint4& y) {
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + 8 * u), c1 = *reinterpret_cast<const float4*>(cs + 8 * u + 4);
+  const float4 s0 = *reinterpret_cast<const float4*>(cs + half + 8 * u);
+  const float4 s1 = *reinterpret_cast<const float4*>(cs + half + 8 * u + 4);
+  uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = Pair<T>::get(xw[j]), q = Pair<T>::get(yw[j]);
-      ow[j] = Pair<T>::put(p.x * c[2 * j] - q.x * s[2 * j], p.y * c[2 * j + 1] - q.y * s[2 * j + 1]);
-      pw[j] = Pair<T>::put(q.x * c[2 * j] + p.x * s[2 * j], q.y * c[2 * j + 1] + p.y * s[2 * j + 1]);
-    }
-    *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-    *reinterpret_cast<uint4*>(dst + half + 8 * u) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
-    return;
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = Pair<T>::get(xw[j]), q = Pair<T>::get(yw[j]);
+    xw[j] = Pair<T>::put(p.x * c[2 * j] - q.x * s[2 * j], p.y * c[2 * j + 1] - q.y * s[2 * j + 1]);
+    yw[j] = Pair<T>::put(q.x * c[2 * j] + p.x * s[2 * j], q.y * c[2 * j + 1] + p.y * s[2 * j + 1]);
   }
-  uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
-  if (8 * u < a.c.rot) {
-    const float4 c0 = *reinterpret_cast<const float4*>(cs + 4 * u);
-    const float4 s0 = *reinterpret_cast<const float4*>(cs + half + 4 * u);
-    const float c[4] = {c0.x, c0.y, c0.z, c0.w}, s[4] = {s0.x, s0.y, s0.z, s0.w};
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  x = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+  y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+}
+template <typename T>
+__device__ __forceinline__ void turn_pairs(const float* cs, int half, int u, uint4& x) {
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + 4 * u), s0 = *reinterpret_cast<const float4*>(cs + half + 4 * u);
+  const float c[4] = {c0.x, c0.y, c0.z, c0.w}, s[4] = {s0.x, s0.y, s0.z, s0.w};
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = Pair<T>::get(w[j]);
-      w[j] = Pair<T>::put(p.x * c[j] - p.y * s[j], p.y * c[j] + p.x * s[j]);
-    }
-    x = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = Pair<T>::get(w[j]);
+    w[j] = Pair<T>::put(p.x * c[j] - p.y * s[j], p.y * c[j] + p.x * s[j]);
   }
-  *reinterpret_cast<uint4*>(dst + 8 * u) = x;
+  x = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Any alignment and any rot_dim: one element, or one rotating pair (u < rot / 2).
@@ -114,39 +93,93 @@ __device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, 
   dst[j] = Pair<T>::round(y * c + x * s);
 }
 
-// One CTA a token.  A lane takes one piece of one head: the heads of q, then
-// those of k, then those of v.
-template <typename T, bool VEC>
+// One CTA a token.  A thread takes pieces of heads: those of q, of k and of v, in turn.
+template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kThreads) k_kv_append(AppendArgs a) {
   const int64_t n = blockIdx.x;
-  const int b = (int)(n / a.slots), i = (int)(n - (int64_t)b * a.slots);
-  const Token t = locate(a, b, i);
-  const int dim = a.c.dim;
-  // pieces of a rotating head and of a value head
-  const int ru = VEC ? (a.c.interleaved ? dim >> 3 : (dim >> 3) - (a.c.rot >> 4)) : dim - (a.c.rot >> 1);
-  const int vu = VEC ? dim >> 3 : dim;
-  const int nq = t.q_row >= 0 ? a.c.q_heads * ru : 0;
-  const int nk = t.k_src >= 0 ? a.c.kv_heads * ru : 0;
-  const int nv = t.k_src >= 0 ? a.c.kv_heads * vu : 0;
+  const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
+  const int r = a.rows ? a.rows[n] : i;
+  const int half = a.c.rot >> 1, pairs = HALVES ? half >> 3 : 0;
+  const int ru = (dim >> 3) - pairs, vu = dim >> 3;  // pieces of a rotating head, each with its partner, and of a value head
+  const bool has_k = r >= 0 && r < a.slots;
+  const int nq = a.q ? a.c.q_heads * ru : 0, nk = has_k ? a.c.kv_heads * ru : 0, nv = has_k ? a.c.kv_heads * vu : 0;
+  const int64_t k_row = (int64_t)b * a.slots + r;
+  constexpr int kPer = 2;  // pieces in flight
+  Token t;
+  bool located = false;
+  for (int w0 = threadIdx.x; w0 < nq + nk + nv || !located; w0 += kPer * kThreads) {
+    uint4 x[kPer], y[kPer];
+    int kind[kPer], head[kPer], u[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      int w = w0 + j * kThreads;
+      kind[j] = w < nq ? 0 : w < nq + nk ? 1 : w < nq + nk + nv ? 2 : 3;
+      if (kind[j] == 3) continue;
+      const Divisor& by = kind[j] == 2 ? a.by_value : a.by_turn;
+      w -= kind[j] == 0 ? 0 : kind[j] == 1 ? nq : nq + nk;
+      head[j] = by.div(w);
+      u[j] = w - head[j] * (int)by.d;
+      const T* src = kind[j] == 0 ? static_cast<const T*>(a.q) + n * a.q_stride
+                                  : kind[j] == 1 ? static_cast<const T*>(a.k) + k_row * a.k_stride : static_cast<const T*>(a.v) + k_row * a.v_stride;
+      src += head[j] * dim;
+      const int at = HALVES && kind[j] < 2 && u[j] >= pairs ? u[j] + pairs : u[j];
+      x[j] = __ldcs(reinterpret_cast<const uint4*>(src) + at);
+      if (HALVES && kind[j] < 2 && u[j] < pairs) y[j] = __ldcs(reinterpret_cast<const uint4*>(src) + u[j] + pairs);
+    }
+    if (!located) {
+      t = locate(a, b, i, r);
+      located = true;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (kind[j] == 3 || (kind[j] == 0 ? t.q_pos : t.k_pos) < 0) continue;
+      T* dst = kind[j] == 0 ? static_cast<T*>(a.q_out) + n * a.q_out_stride + head[j] * dim
+                            : static_cast<T*>(kind[j] == 1 ? a.k_cache : a.v_cache) + t.dst + head[j] * a.c.head_stride;
+      uint4* out = reinterpret_cast<uint4*>(dst);
+      if (kind[j] == 2) {
+        out[u[j]] = x[j];
+        continue;
+      }
+      const float* cs = a.rope + (int64_t)(kind[j] == 0 ? t.q_pos : t.k_pos) * a.c.rot;
+      if (HALVES) {
+        if (u[j] < pairs) {
+          turn_halves<T>(cs, half, u[j], x[j], y[j]);
+          out[u[j]] = x[j];
+          out[u[j] + pairs] = y[j];
+        } else {
+          out[u[j] + pairs] = x[j];
+        }
+      } else {
+        if (8 * u[j] < a.c.rot) turn_pairs<T>(cs, half, u[j], x[j]);
+        out[u[j]] = x[j];
+      }
+    }
+  }
+}
+
+// The same by elements and rotating pairs, for any alignment and any rot_dim.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_kv_append_elements(AppendArgs a) {
+  const int64_t n = blockIdx.x;
+  const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
+  const int r = a.rows ? a.rows[n] : i;
+  const Token t = locate(a, b, i, r);
+  const int64_t k_row = (int64_t)b * a.slots + r;
+  const int ru = dim - (a.c.rot >> 1);
+  const int nq = t.q_pos >= 0 ? a.c.q_heads * ru : 0, nk = t.k_pos >= 0 ? a.c.kv_heads * ru : 0;
+  const int nv = t.k_pos >= 0 ? a.c.kv_heads * dim : 0;
   for (int w = threadIdx.x; w < nq + nk + nv; w += kThreads) {
-    const T* src;
-    T* dst;
     if (w < nq + nk) {
       const bool is_q = w < nq;
       const int x = is_q ? w : w - nq, head = x / ru, u = x - head * ru;
-      src = is_q ? static_cast<const T*>(a.q) + t.q_row * a.q_stride + head * dim
-                 : static_cast<const T*>(a.k) + t.k_src * a.k_stride + head * dim;
-      dst = is_q ? static_cast<T*>(a.q_out) + t.q_row * a.q_out_stride + head * dim
-                 : static_cast<T*>(a.k_cache) + t.dst + head * a.c.head_stride;
-      const float* cs = a.rope + (int64_t)(is_q ? t.q_pos : t.k_pos) * a.c.rot;
-      if (VEC) head_piece<T>(a, src, dst, cs, u);
-      else head_element<T>(a, src, dst, cs, u);
+      const T* src = is_q ? static_cast<const T*>(a.q) + n * a.q_stride + head * dim
+                          : static_cast<const T*>(a.k) + k_row * a.k_stride + head * dim;
+      T* dst = is_q ? static_cast<T*>(a.q_out) + n * a.q_out_stride + head * dim
+                    : static_cast<T*>(a.k_cache) + t.dst + head * a.c.head_stride;
+      head_element<T>(a, src, dst, a.rope + (int64_t)(is_q ? t.q_pos : t.k_pos) * a.c.rot, u);
     } else {
-      const int x = w - nq - nk, head = x / vu, u = x - head * vu;
-      src = static_cast<const T*>(a.v) + t.k_src * a.v_stride + head * dim;
-      dst = static_cast<T*>(a.v_cache) + t.dst + head * a.c.head_stride;
-      if (VEC) *reinterpret_cast<uint4*>(dst + 8 * u) = *reinterpret_cast<const uint4*>(src + 8 * u);
-      else dst[u] = src[u];
+      const int x = w - nq - nk, head = x / dim, u = x - head * dim;
+      static_cast<T*>(a.v_cache)[t.dst + head * a.c.head_stride + u] = static_cast<const T*>(a.v)[k_row * a.v_stride + head * dim + u];
     }
   }
 }
@@ -154,8 +187,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(AppendArgs a) {
 template <typename T>
 cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((int64_t)a.batch * a.slots);
-  if (a.vec) k_kv_append<T, true><<<grid, kThreads, 0, s>>>(a);
-  else k_kv_append<T, false><<<grid, kThreads, 0, s>>>(a);
+  if (!a.vec) k_kv_append_elements<T><<<grid, kThreads, 0, s>>>(a);
+  else if (a.c.interleaved) k_kv_append<T, false><<<grid, kThreads, 0, s>>>(a);
+  else k_kv_append<T, true><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

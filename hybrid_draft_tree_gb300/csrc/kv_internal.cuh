@@ -13,6 +13,18 @@ struct KvLayout {
   int64_t page_stride, head_stride, token_stride;  // elements
 };
 
+// Quotients of numbers below 2^31 by a divisor that the host knows: with s = ceil(log2 d) and
+// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(n mul / 2^32)) / 2^s.
+struct Divisor {
+  uint32_t mul = 0, shift = 0, d = 1;
+  Divisor() = default;
+  explicit Divisor(uint32_t n) : d(n) {
+    while ((1ull << shift) < n) ++shift;
+    mul = (uint32_t)((((1ull << shift) - n) << 32) / n + 1);
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 struct AppendArgs {
   KvLayout c;
   int32_t batch, slots;
@@ -26,19 +38,8 @@ struct AppendArgs {
   int32_t table_stride;
   const int32_t* ctx_len;
   void *q_out, *k_cache, *v_cache;
+  Divisor by_slots, by_turn, by_value;  // slots; 16-byte pieces of a rotating head (each with its partner), of a head
   uint32_t* err;
-};
-
-// Quotients of numbers below 2^31 by a divisor that the host knows: with s = ceil(log2 d) and
-// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (n + floor(n mul / 2^32)) / 2^s.
-struct Divisor {
-  uint32_t mul = 0, shift = 0, d = 1;
-  Divisor() = default;
-  explicit Divisor(uint32_t n) : d(n) {
-    while ((1ull << shift) < n) ++shift;
-    mul = (uint32_t)((((1ull << shift) - n) << 32) / n + 1);
-  }
-  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
 };
 
 // How a call's work is laid out (plan_kv_attend): packed items' rows of all requests against the prefix, then each

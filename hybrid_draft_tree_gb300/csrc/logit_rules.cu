@@ -5,7 +5,7 @@
 // the history, the bias entry, whether a slot's token falls there), so that the
 // history is read once a chunk and not once a row, and turns it into what an
 // element with a rule needs: what is taken off its logit, and whether it counts
-// as seen.  Then its warps take the rows in units of four 16-byte pieces a lane.
+// as seen.  Then its warps take the rows in units of eight 16-byte pieces a lane.
 // Nearly every element has no rule: a unit is masked by its bits of the
 // grammar's row and stored; when some of its elements have rules, it passes
 // through shared memory, where they are done a lane each (in the pieces they
@@ -26,7 +26,8 @@ namespace graft {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kLane = 4, kUnit = 32 * kLane; // pieces that a lane, a warp takes at a time
+constexpr int kLane = 8, kUnit = 32 * kLane; // pieces that a lane, a warp takes at a time
+constexpr int kHeld = 8;                     // tokens of the history that a thread has in flight
 // a table entry while the rules are gathered
 constexpr uint32_t COUNT = (1u << 19) - 1;  // occurrences in the output (the history is shorter than 2^19)
 constexpr uint32_t PROMPT = 1u << 19;       // seen in the prompt
@@ -122,6 +123,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
   uint32_t* const ranks = bitmap + a.chunk / 32 + 1;   // how many lie before a word of the bitmap
   uint16_t* const list = reinterpret_cast<uint16_t*>(ranks + a.chunk / 32 + 1);  // they, in order
   uint32_t bad = 0;
+  // the first of the history on its way while the table is cleared
+  const int32_t* const hist = a.r.d_hist + (int64_t)b * a.r.hist_stride;
+  int n_hist = 0, prompt = 0;
+  if (a.r.d_hist) {
+    n_hist = a.r.d_hist_len[b];
+    if (n_hist < 0 || n_hist > a.r.hist_stride) { bad |= GRAFT_ERR_RULE; n_hist = n_hist < 0 ? 0 : (int)a.r.hist_stride; }
+    prompt = a.r.d_prompt_len ? a.r.d_prompt_len[b] : 0;
+    if (prompt < 0) { bad |= GRAFT_ERR_RULE; prompt = 0; }
+  }
+  int32_t held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) held[j] = t + j * kThreads < n_hist ? hist[t + j * kThreads] : -1;
   // the slots, the request's penalties
   if (t < a.slots) {
     const int64_t at = (int64_t)b * a.slots + t;
@@ -163,19 +176,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
     else if (v >= c0 && v < c1) atomicMax(&table[v - c0], (uint32_t)(k + 1) << BIAS_SHIFT);
   }
   __syncthreads();
-  if (a.r.d_hist) {
-    int64_t n = a.r.d_hist_len[b];
-    if (n < 0 || n > a.r.hist_stride) { bad |= GRAFT_ERR_RULE; n = n < 0 ? 0 : a.r.hist_stride; }
-    int64_t prompt = a.r.d_prompt_len ? a.r.d_prompt_len[b] : 0;
-    if (prompt < 0) { bad |= GRAFT_ERR_RULE; prompt = 0; }
-    const int32_t* hist = a.r.d_hist + (int64_t)b * a.r.hist_stride;
-    for (int64_t k = t; k < n; k += kThreads) {
-      const int32_t v = hist[k];
+  for (int k0 = 0; k0 < n_hist; k0 += kHeld * kThreads) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int k = k0 + t + j * kThreads, v = held[j];
+      if (k >= n_hist) break;
       if (v < 0 || v >= a.V) bad |= GRAFT_ERR_TOKEN;
       else if (counts && v >= c0 && v < c1) {
         if (k >= prompt) atomicAdd(&table[v - c0], 1u);
         else if (!(table[v - c0] & PROMPT)) atomicOr(&table[v - c0], PROMPT);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int k = k0 + t + (kHeld + j) * kThreads;
+      if (k < n_hist) held[j] = hist[k];
     }
   }
   if (a.tree_tok && counts && t >= 1 && t < a.slots && sh.tok[t] >= c0 && sh.tok[t] < c1)
