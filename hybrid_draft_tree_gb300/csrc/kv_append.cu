@@ -9,7 +9,7 @@
 namespace graft {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Where token (b, i) comes from and goes to.  Its source rows are known before its place: their loads do not wait for
 // the page table.  Bad data sets the error bit and drops the write.
