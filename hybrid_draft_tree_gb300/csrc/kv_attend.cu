@@ -188,8 +188,9 @@ __device__ __forceinline__ int part_row(const AttendArgs& a, int dest, bool pack
 
 // A wait that another role's abort, or the poll limit, ends; false: the item's results are void.
 __device__ __forceinline__ bool wait_bar(Bars& sh, const AttendArgs& a, unsigned long long* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint32_t limit = a.wait_polls ? a.wait_polls : SPIN;
-  for (uint32_t n = 0; n < limit; ++n) {
+  for (uint32_t n = 1; n < limit; ++n) {
     if (mbar_try_wait(bar, parity)) return true;
     if (sh.abort) return false;
   }
@@ -202,6 +203,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;
@@ -324,68 +330,87 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
 // ---- warp 9: the products ---------------------------------------------------------------------------------------
 // One thread issues every product: its code has no warp-wide step in it.  Products run in the order they are issued, so
 // the scores of a group's next block may follow its O += P V at once, although they overwrite P.
+// What it does between products is on every unit's path, so it keeps the ring's places instead of computing them, and
+// waits once for what both groups use.
 template <typename T, int D>
 __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring) {
   using S = Smem<D>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kQK = tc::instr_desc(kBf16, 128, BN, false), kPV = tc::instr_desc(kBf16, 128, D, true);
+  constexpr int kTile16 = S::kTile / 16;
+  // With room for P beside S (D = 64) a group's next scores are computed as soon as it has read its last ones, while it
+  // turns them into weights; the products with the values follow one unit behind.
+  constexpr bool kApart = D == 64;
   const uint32_t tmem = sh.tmem;
   const uint64_t qd = tc::smem_desc(smem_u32(q), 16), kd = tc::smem_desc(smem_u32(ring), 16);
   const uint64_t vd = tc::smem_desc(smem_u32(ring), 128 * 128);
-  constexpr int kTile16 = S::kTile / 16;
-  constexpr bool kApart = D == 64;
-  uint32_t cleaned = 0, weights0 = 0, weights1 = 0, reads0 = 0, reads1 = 0, before = 0, piece = 0;
+  // stage and phase of the next keys and of the next values; phases of the groups' barriers, a bit each
+  int ks = 0, vs = 1;
+  uint32_t kp = 0, vp = 0, cleaned = 0, weights = 0, reads = 0, piece = 0;
   bool ok = true;
   Pieces pieces(a, sh.line);
   Item it;
-  for (; ok && pieces.next(it); before += it.blocks, ++piece) {
-    const int units = it.blocks * it.nt;
+  for (; ok && pieces.next(it); ++piece) {
+    const bool two = it.nt == 2;
+    const int units = two ? 2 * it.blocks : it.blocks;
+    // masked blocks: the prefix's last when part full, and the request's own from where the tree begins
+    const int part_full = !(a.prefix_len & (BN - 1)) ? -1 : it.np - 1 - it.first;
+    const int tree = it.b < 0 ? INT32_MAX : it.np + it.ctx / BN - it.first;
     // unit u is group u & 1 on key block u >> 1 (two tiles) or u (one)
-    auto qk = [&](int u) -> bool {
-      const int t = u & 1;
-      const uint32_t x = 2 * (before + (it.nt == 2 ? u >> 1 : u)), stage = x % S::kStages;
-      if (!wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1)) return false;
+    auto qk = [&](int t) -> bool {
+      if ((!two || t == 0) && !wait_bar(sh, a, &sh.full[ks], kp)) return false;
       tc::fence_after();
-      const uint64_t qa = qd + (it.nt == 2 ? t : 0) * kTile16, kb = kd + stage * kTile16;
+      const uint64_t qa = qd + (two && t ? kTile16 : 0), kb = kd + ks * kTile16;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
         tc::mma_ss(tmem + t * 128, qa + step, kb + step, kQK, k > 0);
       }
       tc::commit(&sh.s_full[t]);
-      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
+      if (!two || t) {
+        tc::commit(&sh.empty[ks]);
+        ks += 2;
+        if (ks >= S::kStages) { ks -= S::kStages; kp ^= 1; }
+      }
       return true;
     };
     ok = wait_bar(sh, a, &sh.q_full, piece & 1);
     for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
-    // With room for P beside S (D = 64) a group's next scores are computed as soon as it has read its last ones, while it
-    // turns them into weights; the products with the values follow one unit behind.
     int scored = min(units, 2);
-    auto early = [&](int u) -> bool {  // unit u's scores have been read
-      if (!kApart || scored >= units) return true;
-      if (!wait_bar(sh, a, &sh.s_read[u & 1], (u & 1 ? reads1++ : reads0++) & 1)) return false;
-      return qk(scored++);
+    auto early = [&](int t) -> bool {  // the group has read its scores
+      if (scored >= units) return true;
+      if (!wait_bar(sh, a, &sh.s_read[t], (reads >> t) & 1)) return false;
+      reads ^= 1u << t;
+      ++scored;
+      return qk(t);
     };
-    ok = ok && early(0);
+    if (kApart) ok = ok && early(0);
     for (int u = 0; u < units && ok; ++u) {
-      if (u + 1 < units && !early(u + 1)) { ok = false; break; }
-      const int t = u & 1, j = it.nt == 2 ? u >> 1 : u;
-      const uint32_t x = 2 * (before + j) + 1, stage = x % S::kStages;
-      ok = wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
-      if (ok && (it.nt == 1 || t == 0) && block_of(a, it, j).masked) {
-        ok = wait_bar(sh, a, &sh.clean[stage], (cleaned >> stage) & 1);
-        cleaned ^= 1u << stage;
+      const int t = u & 1;
+      if (kApart && !early(t ^ 1)) { ok = false; break; }
+      if (!two || t == 0) {
+        ok = wait_bar(sh, a, &sh.full[vs], vp);
+        const int j = two ? u >> 1 : u;
+        if (ok && (j >= tree || j == part_full)) {
+          ok = wait_bar(sh, a, &sh.clean[vs], (cleaned >> vs) & 1);
+          cleaned ^= 1u << vs;
+        }
       }
-      ok = ok && wait_bar(sh, a, &sh.p_full[t], (t ? weights1++ : weights0++) & 1);
+      ok = ok && wait_bar(sh, a, &sh.p_full[t], (weights >> t) & 1);
+      weights ^= 1u << t;
       if (!ok) break;
       tc::fence_after();
       const uint32_t o = tmem + 256 + t * D, p = tmem + (D == 128 ? t * 128 : 384 + t * 64);
-      const uint64_t vb = vd + stage * kTile16;
+      const uint64_t vb = vd + vs * kTile16;
 #pragma unroll
       for (int k = 0; k < BN / 16; ++k) tc::mma_ts(o, p + k * 8, vb + k * (16 * 128 / 16), kPV, u > 1 || k > 0);
-      if (it.nt == 1 || t == 1) tc::commit(&sh.empty[stage]);
       if (kApart || u + 2 >= units) tc::commit(&sh.o_done[t]);
-      if (!kApart && u + 2 < units) ok = qk(u + 2);
+      if (!two || t) {
+        tc::commit(&sh.empty[vs]);
+        vs += 2;
+        if (vs >= S::kStages) { vs -= S::kStages; vp ^= 1; }
+      }
+      if (!kApart && u + 2 < units) ok = qk(t);
     }
   }
   if (!ok) {  // the products in flight finish before the tensor memory goes back
@@ -562,12 +587,11 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
       const float* sf = reinterpret_cast<const float*>(s);
       float mx[4] = {sf[0], sf[1], sf[2], sf[3]};
 #pragma unroll
-      for (int c = 4; c < BN; c += 4) {
-        mx[0] = fmaxf(mx[0], sf[c]);
-        mx[1] = fmaxf(mx[1], sf[c + 1]);
-        mx[2] = fmaxf(mx[2], sf[c + 2]);
-        mx[3] = fmaxf(mx[3], sf[c + 3]);
-      }
+      for (int c = 4; c < BN - 4; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], sf[c + i], sf[c + 4 + i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], sf[BN - 4 + i]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
       if (D == 64) {
         if (!settled()) { ok = false; break; }
