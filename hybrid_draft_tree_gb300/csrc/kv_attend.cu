@@ -14,9 +14,11 @@
 // turn, and their results are joined at the end.
 //
 // The online softmax keeps, per row, a base m, l = sum 2^(s-m) and O = sum
-// 2^(s-m) v, s in units of log2.  m follows the maximum only when that has
-// grown by 2^8: until then weights above 1 are as exact as below, and O, which
-// lives in tensor memory, is not read and written back for every block.
+// 2^(s-m) v, s in units of log2.  m is the maximum of the row's first keys and
+// moves only when a later one exceeds it by 2^60 (2^12 with f16): until then
+// weights above 1 are as exact as below, O, which lives in tensor memory, is
+// not read and written back for every block, and the weights need not wait for
+// the block's maximum.
 //
 // Rows of all requests against the prefix are packed into the same tiles
 // ("packed"), so a prefix block is read once for up to 256 rows, when a
@@ -45,7 +47,11 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.f;              // log2 of how far a maximum may run ahead of the base
+// log2 of how far a maximum may run ahead of the base: weights stay inside the type and their sums inside fp32
+template <typename T>
+constexpr float kGrowth = 60.f;
+template <>
+constexpr float kGrowth<__half> = 12.f;
 
 template <int D>
 struct Smem {
@@ -82,10 +88,10 @@ __device__ __forceinline__ int blocks_of(const AttendArgs& a, int ctx) {
 }
 __device__ __forceinline__ int ctx_of(const AttendArgs& a, int b) { return min(max(a.ctx_len[b], 0), a.max_ctx); }
 __device__ __forceinline__ uint32_t cost_a(const AttendArgs& a) {
-  return a.plan.fixed + (uint32_t)((a.prefix_len + BN - 1) / BN) * a.plan.step_a;
+  return a.plan.fixed_a + (uint32_t)((a.prefix_len + BN - 1) / BN) * a.plan.step_a;
 }
 __device__ __forceinline__ uint32_t cost_b(const AttendArgs& a, int blocks) {
-  return a.plan.fixed + (uint32_t)blocks * a.plan.step_b;
+  return a.plan.fixed_b + (uint32_t)blocks * a.plan.step_b;
 }
 
 // Walks the pieces of a CTA.
@@ -101,7 +107,7 @@ class Pieces {
         ++b_;
       }
       if (b_ >= a_.batch || (!p.cut && at_ > 0)) return false;
-      const int64_t base = at_ + p.fixed, hi = line_.hi, lo = line_.lo;  // base: place of block 0
+      const int64_t base = at_ + (b_ < 0 ? p.fixed_a : p.fixed_b), hi = line_.hi, lo = line_.lo;  // base: place of block 0
       if (base >= hi) return false;
       const int np = (a_.prefix_len + BN - 1) / BN;
       const bool of_a = b_ < 0;
@@ -486,6 +492,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
   const uint32_t tmem = sh.tmem + lanes;
+  constexpr float kGrow = kGrowth<T>;
   const float scale = a.scale * kLog2e;
   uint32_t scores = 0, results = 0, piece = 0;
   Pieces pieces(a, sh.line);
@@ -534,7 +541,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
   const uint64_t mask = live ? mask_of(a, row.token) : 0;
   const bool warp_live = __any_sync(~0u, live);
   const int units = it.nt == 2 ? it.blocks : (it.blocks + 1 - t) >> 1;
-  float m = -INFINITY;
+  float m = live ? -INFINITY : 0.f;                 // lanes without a row never wait
   float2 l2 = make_float2(0.f, 0.f);
   bool ok = true;
   for (int n = 0; n < units && ok; ++n) {
@@ -597,43 +604,52 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
         if (!settled()) { ok = false; break; }
         tc::fence_after();
       }
-      if (__any_sync(~0u, top > m + kGrow)) {
-        const float next = fmaxf(m, top);
-        const float f = next == -INFINITY ? 1.f : ex2(m - next);
-        m = next;
-        l2.x *= f;
-        l2.y *= f;
-        if (n > 0) {  // O is at rest: the products before these scores are done (D = 128: the scores came after them)
+      // A row's first keys set its base, so the weights wait for their maximum; later the weights are computed with the
+      // base there is, beside the maximum, and again if that has run away from it.
+      bool known = __all_sync(~0u, m != -INFINITY);
+      float2 sum0, sum1;
+      for (;;) {
+        if (!known) {
+          const float next = top > m + kGrow ? top : m;
+          const float f = next == -INFINITY ? 1.f : ex2(m - next);
+          m = next;
+          l2.x *= f;
+          l2.y *= f;
+          if (n > 0) {  // O is at rest: the products before these scores are done (D = 128: the scores came after them)
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc::ld32(tmem + 256 + t * D + c, o);
-            tc::wait_ld<32>(o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc::ld32(tmem + 256 + t * D + c, o);
+              tc::wait_ld<32>(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc::st32(tmem + 256 + t * D + c, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::st32(tmem + 256 + t * D + c, o);
+            }
           }
         }
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      const float2 sc = make_float2(scale, scale), mb = make_float2(-base, -base);
-      float2 sum0 = l2, sum1 = make_float2(0.f, 0.f);
-      const uint32_t p_at = tmem + (D == 128 ? t * 128 : 384 + t * 64);
+        const float base = m == -INFINITY ? 0.f : m;
+        const float2 sc = make_float2(scale, scale), mb = make_float2(-base, -base);
+        const uint32_t p_at = tmem + (D == 128 ? t * 128 : 384 + t * 64);
+        sum0 = l2;
+        sum1 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t p[16];
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float2 x = fma2(make_float2(sf[c + i], sf[c + i + 1]), sc, mb);
-          float2 y = fma2(make_float2(sf[c + i + 2], sf[c + i + 3]), sc, mb);
-          x = make_float2(ex2(x.x), ex2(x.y));
-          y = make_float2(ex2(y.x), ex2(y.y));
-          sum0 = add2(sum0, x);
-          sum1 = add2(sum1, y);
-          p[i / 2] = Pair<T>::put(x.x, x.y);
-          p[i / 2 + 1] = Pair<T>::put(y.x, y.y);
+          for (int i = 0; i < 32; i += 4) {
+            float2 x = fma2(make_float2(sf[c + i], sf[c + i + 1]), sc, mb);
+            float2 y = fma2(make_float2(sf[c + i + 2], sf[c + i + 3]), sc, mb);
+            x = make_float2(ex2(x.x), ex2(x.y));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum0 = add2(sum0, x);
+            sum1 = add2(sum1, y);
+            p[i / 2] = Pair<T>::put(x.x, x.y);
+            p[i / 2 + 1] = Pair<T>::put(y.x, y.y);
+          }
+          tc::st16(p_at + c / 2, p);
         }
-        tc::st16(p_at + c / 2, p);
+        if (!known || !__any_sync(~0u, live && top > m + kGrow)) break;
+        known = false;
       }
       l2 = add2(sum0, sum1);
       tc::wait_st();
@@ -829,10 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of a row and head, in the order of their keys: D / 4 lanes a row, 16 bytes a lane.  Every
 // row has two items to join when items are packed; else only rows of cut items have anything to: CTA row y then is an
 // item, or (by_cta, with more items than CTAs) the CTA of an item's first piece, which has said which item that is
-// (line[batch + 1 + y], -1: none).  What it takes is latency, so P partials of a row are asked for at once, and with
-// many rows registers are kept few and CTAs many.
-template <typename T, int D, int P>
-__global__ void __launch_bounds__(256, P == 2 ? 6 : 3) k_kv_join(const __grid_constant__ AttendArgs a, int by_cta) {
+// (line[batch + 1 + y], -1: none).  What it takes is latency: a thread asks for P partials of R rows at once.
+template <typename T, int D, int R, int P>
+__global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_constant__ AttendArgs a, int by_cta) {
   constexpr int kLanes = D / 4;
   const AttendPlan& p = a.plan;
   const int lane = threadIdx.x % kLanes, items = p.tiles_b * a.c.kv_heads;
@@ -856,69 +871,92 @@ __global__ void __launch_bounds__(256, P == 2 ? 6 : 3) k_kv_join(const __grid_co
   };
   const int tile_b = a.by_heads.div(item), kv_head = item - tile_b * a.c.kv_heads;
   const int blocks = blocks_of(a, ctx_of(a, b));
-  const int64_t start_b = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed;
+  const int64_t start_b = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed_b;
   const int b_first = cta_of(start_b), b_last = cta_of(start_b + (int64_t)(blocks - 1) * p.step_b);
   if (!p.packed && b_first == b_last) return;  // whole, and written
-  int row = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const int per = a.slots * a.group, in_b = tile_b * p.nt_b * p.tile + row;
-  if (in_b >= per || row >= p.nt_b * p.tile) return;
-  const int slot = a.by_group.div(in_b), token = b * a.slots + slot, head = kv_head * a.group + in_b - slot * a.group;
-  const int at = token * a.c.q_heads + head;
-  if (p.nt_b == 2 && row >= p.tile) row += 128 - p.tile;  // place in its CTA's partial
-  int in_a = 0, a_first = 0, na = 0;
-  if (p.packed) {
-    in_a = b * per + in_b;
-    const int tile_a = in_a / (p.nt_a * p.tile), np = (a.prefix_len + BN - 1) / BN;
-    in_a -= tile_a * p.nt_a * p.tile;
-    if (p.nt_a == 2 && in_a >= p.tile) in_a += 128 - p.tile;
-    const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed;
-    a_first = cta_of(start_a);
-    na = cta_of(start_a + (int64_t)(np - 1) * p.step_a) - a_first + 1;
+  const int per = a.slots * a.group;
+  int row[R], at[R], in_a[R], a_first[R], na[R], n[R], most = 0;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    row[k] = (blockIdx.x * R + k) * (256 / kLanes) + threadIdx.x / kLanes;
+    const int in_b = tile_b * p.nt_b * p.tile + row[k];
+    at[k] = -1;
+    n[k] = na[k] = in_a[k] = a_first[k] = 0;
+    if (in_b >= per || row[k] >= p.nt_b * p.tile) continue;
+    const int slot = a.by_group.div(in_b);
+    at[k] = (b * a.slots + slot) * a.c.q_heads + kv_head * a.group + in_b - slot * a.group;
+    if (p.nt_b == 2 && row[k] >= p.tile) row[k] += 128 - p.tile;  // place in its CTA's partial
+    if (p.packed) {
+      in_a[k] = b * per + in_b;
+      const int tile_a = in_a[k] / (p.nt_a * p.tile), np = (a.prefix_len + BN - 1) / BN;
+      in_a[k] -= tile_a * p.nt_a * p.tile;
+      if (p.nt_a == 2 && in_a[k] >= p.tile) in_a[k] += 128 - p.tile;
+      const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed_a;
+      a_first[k] = cta_of(start_a);
+      na[k] = cta_of(start_a + (int64_t)(np - 1) * p.step_a) - a_first[k] + 1;
+    }
+    n[k] = na[k] + b_last - b_first + 1;
+    most = max(most, n[k]);
   }
-  const int n = na + b_last - b_first + 1;
   const float* parts = a.part_o + lane * 4;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += P) {
-    float z[P];
-    float4 v[P];
+  float top[R], sum[R];
+  float4 acc[R];
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const int i = i0 + j;
-      z[j] = -INFINITY;
-      if (i >= n) continue;
-      const bool of_a = i < na;
-      const int cta = of_a ? a_first + i : b_first + i - na;
-      const bool last = of_a ? i == na - 1 : cta == b_last;
-      const int r = part_row(a, last ? kItemPart : kCtaPart, of_a, at, cta, of_a ? in_a : row);
-      z[j] = a.part_lse[r];
-      v[j] = *reinterpret_cast<const float4*>(parts + (int64_t)r * D);
-    }
-    float next = top;
+  for (int k = 0; k < R; ++k) {
+    top[k] = -INFINITY;
+    sum[k] = 0.f;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int i0 = 0; i0 < most; i0 += P) {
+    float z[R][P];
+    float4 v[R][P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) next = fmaxf(next, z[j]);  // drops a NaN: the sum keeps it
-    const float base = next == -INFINITY ? 0.f : next, f = ex2(top - base);
-    sum *= f;
-    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-    top = next;
+    for (int k = 0; k < R; ++k)
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      if (z[j] == -INFINITY) continue;
-      const float w = ex2(z[j] - base);
-      sum += w;
-      acc.x += w * v[j].x; acc.y += w * v[j].y; acc.z += w * v[j].z; acc.w += w * v[j].w;
+      for (int j = 0; j < P; ++j) {
+        const int i = i0 + j;
+        z[k][j] = -INFINITY;
+        if (i >= n[k]) continue;
+        const bool of_a = i < na[k];
+        const int cta = of_a ? a_first[k] + i : b_first + i - na[k];
+        const bool last = of_a ? i == na[k] - 1 : cta == b_last;
+        const int r = part_row(a, last ? kItemPart : kCtaPart, of_a, at[k], cta, of_a ? in_a[k] : row[k]);
+        z[k][j] = a.part_lse[r];
+        v[k][j] = *reinterpret_cast<const float4*>(parts + (int64_t)r * D);
+      }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float next = top[k];
+#pragma unroll
+      for (int j = 0; j < P; ++j) next = fmaxf(next, z[k][j]);  // drops a NaN: the sum keeps it
+      const float base = next == -INFINITY ? 0.f : next, f = ex2(top[k] - base);
+      sum[k] *= f;
+      acc[k].x *= f; acc[k].y *= f; acc[k].z *= f; acc[k].w *= f;
+      top[k] = next;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        if (z[k][j] == -INFINITY) continue;
+        const float w = ex2(z[k][j] - base);
+        sum[k] += w;
+        acc[k].x += w * v[k][j].x; acc[k].y += w * v[k][j].y; acc[k].z += w * v[k][j].z; acc[k].w += w * v[k][j].w;
+      }
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * 4;
-  const uint2 w = make_uint2(Pair<T>::put(acc.x * inv, acc.y * inv), Pair<T>::put(acc.z * inv, acc.w * inv));
-  if (a.out_vec) {
-    *reinterpret_cast<uint2*>(out) = w;
-  } else {
-    uint16_t* h = reinterpret_cast<uint16_t*>(out);
-    h[0] = (uint16_t)w.x; h[1] = (uint16_t)(w.x >> 16); h[2] = (uint16_t)w.y; h[3] = (uint16_t)(w.y >> 16);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (at[k] < 0) continue;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+    const int token = at[k] / a.c.q_heads, head = at[k] - token * a.c.q_heads;
+    T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * 4;
+    const uint2 w = make_uint2(Pair<T>::put(acc[k].x * inv, acc[k].y * inv), Pair<T>::put(acc[k].z * inv, acc[k].w * inv));
+    if (a.out_vec) {
+      *reinterpret_cast<uint2*>(out) = w;
+    } else {
+      uint16_t* h = reinterpret_cast<uint16_t*>(out);
+      h[0] = (uint16_t)w.x; h[1] = (uint16_t)(w.x >> 16); h[2] = (uint16_t)w.y; h[3] = (uint16_t)(w.y >> 16);
+    }
+    if (lane == 0 && a.lse) a.lse[at[k]] = sum[k] == 0.f ? -INFINITY : (top[k] + log2f(sum[k])) * 0.6931471805599453f;
   }
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D>
@@ -929,11 +967,13 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.cut) {
     // many rows have few partials each
-    const int rows = std::min(a.slots * a.group, p.nt_b * p.tile), items = p.tiles_b * a.c.kv_heads, each = 1024 / D;
+    const bool many = p.rows > 8192;
+    const int rows = std::min(a.slots * a.group, p.nt_b * p.tile), items = p.tiles_b * a.c.kv_heads;
+    const int each = (many ? 2 : 1) * 1024 / D;
     const bool by_cta = !p.packed && (int64_t)items * a.batch > p.ctas;
     const dim3 grid = by_cta ? dim3((rows + each - 1) / each, p.ctas) : dim3((rows + each - 1) / each, items, a.batch);
-    e = p.rows > 8192 ? launch_dependent(k_kv_join<T, D, 2>, grid, dim3(256), 0, s, a, (int)by_cta)
-                      : launch_dependent(k_kv_join<T, D, 8>, grid, dim3(256), 0, s, a, (int)by_cta);
+    e = many ? launch_dependent(k_kv_join<T, D, 2, 2>, grid, dim3(256), 0, s, a, (int)by_cta)
+             : launch_dependent(k_kv_join<T, D, 1, 8>, grid, dim3(256), 0, s, a, (int)by_cta);
   }
   return e;
 }
@@ -963,15 +1003,15 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
                           int num_sms) {
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
-  const int two = dim == 128 ? 150 : 100, one = dim == 128 ? 80 : 60;
-  const int memory = dim == 128 ? 150 : 75, l2 = dim == 128 ? 70 : 40;
+  const bool wide = dim == 128;
+  const int two = wide ? 152 : 145, one = wide ? 85 : 125, fixed_two = wide ? 650 : 480, fixed_one = wide ? 350 : 310;
+  const int memory = wide ? 120 : 60, l2 = wide ? 70 : 35;
   AttendPlan best{};
   double best_t = 0;
   for (int packed = 0; packed < 2; ++packed) {
     if (packed && (np == 0 || batch == 1)) break;
     AttendPlan p{};
     p.packed = packed;
-    p.fixed = 300;
     p.rows = all * kv_heads;
     p.tile = group <= 128 ? 128 / group * group : 128;
     p.nt_a = all > p.tile ? 2 : 1;
@@ -979,15 +1019,17 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     p.tiles_b = (int)((R + p.tile * p.nt_b - 1) / (p.tile * p.nt_b));
     p.items_a = packed ? (int)((all + p.tile * p.nt_a - 1) / (p.tile * p.nt_a)) * kv_heads : 0;
     p.step_a = std::max(p.nt_a == 2 ? two : one, l2);
+    p.fixed_a = p.nt_a == 2 ? fixed_two : fixed_one;
+    p.fixed_b = p.nt_b == 2 ? fixed_two : fixed_one;
     // the share of an item's blocks that no other item reads
     const int blocks = packed ? no : np + no;
     const double alone = packed || batch == 1 ? 1.0 : (double)no / blocks;
     p.step_b = std::max(p.nt_b == 2 ? two : one, (int)(p.tiles_b > 1 ? l2 : l2 + alone * (memory - l2)));
     const int64_t items_b = (int64_t)batch * p.tiles_b * kv_heads;
-    const double whole = p.fixed + (double)blocks * p.step_b;
-    const double work = p.items_a * (p.fixed + (double)np * p.step_a) + items_b * whole;
+    const double whole = p.fixed_b + (double)blocks * p.step_b;
+    const double work = p.items_a * (p.fixed_a + (double)np * p.step_a) + items_b * whole;
     const double join = 400 + (double)(p.rows * (packed ? 2 : 1) + num_sms * 256) * dim * 8 / 50000;
-    double t = work / num_sms + p.fixed + join;
+    double t = work / num_sms + p.fixed_b + join;
     p.cut = 1;
     p.ctas = num_sms;
     if (!packed && items_b <= num_sms && whole <= t) {

@@ -50,7 +50,7 @@ struct AttendPlan {
   int32_t tiles_b;           // row tiles of a request and head
   int32_t nt_a, nt_b;        // row tiles of an item
   int32_t tile;              // rows of a tile: the most whole groups in 128
-  int32_t fixed, step_a, step_b;  // cost of an item before its first block, and of a block
+  int32_t fixed_a, fixed_b, step_a, step_b;  // cost of an item before its first block, and of a block
   int64_t rows;              // query rows times query heads
 };
 
