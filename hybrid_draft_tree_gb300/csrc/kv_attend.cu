@@ -53,12 +53,15 @@ constexpr float kGrowth = 60.f;
 template <>
 constexpr float kGrowth<__half> = 12.f;
 
+// Shared memory: two query tiles, the ring, where results pass on their way out, and the barriers.  A tile is stored in
+// column halves of 64 elements (128 bytes).  With D = 128 results pass through the query tile they belong to.
 template <int D>
 struct Smem {
-  static constexpr int kHalves = D / 64;              // tiles are stored in column halves of 64 elements (128 bytes)
+  static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * 128 * 128;   // bytes of 128 rows
   static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kRing = 2 * kTile, kBytes = kRing + kStages * kTile + 1024;  // + alignment slack
+  static constexpr int kRing = 2 * kTile, kStage = D == 128 ? 0 : kRing + kStages * kTile;
+  static constexpr int kBars = kRing + kStages * kTile + (D == 128 ? 0 : 8 * 4096);
 };
 
 // A piece of a work item, the same in every thread of its CTA.
@@ -146,8 +149,10 @@ class Pieces {
 };
 
 struct Bars {
-  unsigned long long full[8], empty[8], q_full, s_full[2], s_read[2], p_full[2], o_done[2], dirty[8], clean[8], drain;
+  unsigned long long full[8], empty[8], q_full[2], q_free[2], s_full[2], s_read[2], p_full[2], o_done[2], o_free;
+  unsigned long long dirty[8], clean[8], drain;
   unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
+  float2 ml[2][128];             // a shared tile's maxima and sums
   Line line;
   uint32_t tmem;
   volatile uint32_t abort;
@@ -229,18 +234,42 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // ---- warp 8: keys and values into the ring ----------------------------------------------------------------------
 template <int D>
-__device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CUtensorMap* kmap, const CUtensorMap* vmap) {
+__device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
+                          const CUtensorMap* vmap) {
   using S = Smem<D>;
   const int lane = threadIdx.x & 31;
   const int pages = BN >> a.c.page_shift;                   // of a block; a copy is a page's half
   const int page_bytes = a.c.page_size * 128;
   int loads = 0;
-  uint32_t bad = 0;
-  bool ok = true;
+  uint32_t bad = 0, piece = 0;
+  bool ok = true, last_two = false;
+  int q_last = -1;  // the last piece whose queries were asked for
   Pieces pieces(a, sh.line);
   Item it;
-  while (ok && pieces.next(it)) {
+  for (; ok && pieces.next(it); ++piece) {
     if (it.bad_ctx) bad = GRAFT_ERR_RANGE;
+    const bool two = it.nt == 2;
+    // A shared tile takes the query tiles in turn, so its queries come while the piece before runs; two tiles wait for
+    // that piece's end, after the first blocks are on their way.
+    auto queries = [&]() -> bool {
+      if (!a.q_map) return true;
+      const uint32_t before = two || last_two ? 1 : 2;  // pieces back: the last user of the space
+      if (piece >= before) {
+        const uint32_t user = piece - before;
+        if (!__all_sync(~0u, wait_bar(sh, a, &sh.q_free[user & 1], (user >> 1) & 1))) return false;
+      }
+      if (lane == 0) mbar_expect_tx(&sh.q_full[piece & 1], it.nt * S::kHalves * a.plan.tile * 128);
+      __syncwarp();
+      if (lane < it.nt * S::kHalves) {
+        const int tile = lane / S::kHalves, half = lane % S::kHalves;
+        const Row row = row_of(a, it, it.row0 + tile * a.plan.tile);
+        tc::tma_3d(q + (two ? tile : piece & 1) * S::kTile + half * (128 * 128), qmap, half * 64, it.head * a.group, row.token,
+                   &sh.q_full[piece & 1]);
+      }
+      q_last = (int)piece;
+      return true;
+    };
+    const int q_at = two && piece > 0 ? min(2, it.blocks - 1) : 0;
     // page of this lane's copy of block j: copy lane -> half lane % kHalves of page lane / kHalves
     auto page_of = [&](int j) -> int {
       const Block k = block_of(a, it, j);
@@ -256,6 +285,8 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CU
     };
     int page = page_of(0);
     for (int j = 0; j < it.blocks && ok; ++j) {
+      if (j == q_at) ok = queries();
+      if (!ok) break;
       const int here = page;
       if (j + 1 < it.blocks) page = page_of(j + 1);
       const int copies = __popc(__ballot_sync(~0u, here >= 0));
@@ -274,11 +305,14 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* ring, const CU
         ++loads;
       }
     }
+    last_two = two;
   }
   if (bad) atomicOr(a.err, bad);
-  if (!ok && lane == 0)  // the copies in flight land before the CTA ends
+  if (!ok && lane == 0) {  // the copies in flight land before the CTA ends
     for (int x = max(0, loads - S::kStages); x < loads; ++x)
       mbar_wait_drain(&sh.full[x % S::kStages], (x / S::kStages) & 1);
+    for (int x = max(0, q_last - 1); x <= q_last; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
+  }
 }
 
 // ---- warps 10, 11: values that no row may see --------------------------------------------------------------------
@@ -345,7 +379,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
   constexpr uint32_t kQK = tc::instr_desc(kBf16, 128, BN, false), kPV = tc::instr_desc(kBf16, 128, D, true);
   constexpr int kTile16 = S::kTile / 16;
   // With room for P beside S (D = 64) a group's next scores are computed as soon as it has read its last ones, while it
-  // turns them into weights; the products with the values follow one unit behind.
+  // turns them into weights.  A piece's first scores are computed while the last piece's results go out.
   constexpr bool kApart = D == 64;
   const uint32_t tmem = sh.tmem;
   const uint64_t qd = tc::smem_desc(smem_u32(q), 16), kd = tc::smem_desc(smem_u32(ring), 16);
@@ -366,7 +400,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
     auto qk = [&](int t) -> bool {
       if ((!two || t == 0) && !wait_bar(sh, a, &sh.full[ks], kp)) return false;
       tc::fence_after();
-      const uint64_t qa = qd + (two && t ? kTile16 : 0), kb = kd + ks * kTile16;
+      const uint64_t qa = qd + ((two ? t : piece & 1) ? kTile16 : 0), kb = kd + ks * kTile16;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint64_t step = (k >> 2) * (128 * 128 / 16) + (k & 3) * 2;
@@ -380,20 +414,17 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       }
       return true;
     };
-    ok = wait_bar(sh, a, &sh.q_full, piece & 1);
+    ok = wait_bar(sh, a, &sh.q_full[piece & 1], (piece >> 1) & 1);
     for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
-    int scored = min(units, 2);
-    auto early = [&](int t) -> bool {  // the group has read its scores
-      if (scored >= units) return true;
-      if (!wait_bar(sh, a, &sh.s_read[t], (reads >> t) & 1)) return false;
-      reads ^= 1u << t;
-      ++scored;
-      return qk(t);
-    };
-    if (kApart) ok = ok && early(0);
     for (int u = 0; u < units && ok; ++u) {
       const int t = u & 1;
-      if (kApart && !early(t ^ 1)) { ok = false; break; }
+      if (kApart && u + 2 < units) {  // the group has read its scores
+        ok = wait_bar(sh, a, &sh.s_read[t], (reads >> t) & 1) && qk(t);
+        reads ^= 1u << t;
+        if (!ok) break;
+      }
+      if (u == 0 && piece > 0) ok = wait_bar(sh, a, &sh.o_free, (piece - 1) & 1);  // the last piece's results are out
+      if (!ok) break;
       if (!two || t == 0) {
         ok = wait_bar(sh, a, &sh.full[vs], vp);
         const int j = two ? u >> 1 : u;
@@ -487,7 +518,7 @@ __device__ __forceinline__ void store_rows(const AttendArgs& a, uint8_t* stage, 
 }
 
 template <typename T, int D>
-__device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CUtensorMap* qmap) {
+__device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   using S = Smem<D>;
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
@@ -498,25 +529,12 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
   Pieces pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); ++piece) {
-  if (piece > 0) {  // the last results have left tensor memory and the queries' space
-    tc::fence_async_smem();
-    tc::fence_before();
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-  }
-  // queries into shared memory, in the swizzled order the products read: by tensor map, or 16 bytes a thread
-  if (a.q_map) {
-    if (tid == 0) {
-      tc::fence_after();
-      mbar_expect_tx(&sh.q_full, it.nt * S::kHalves * a.plan.tile * 128);
-      for (int x = 0; x < it.nt * S::kHalves; ++x) {
-        const int tile = x / S::kHalves, half = x % S::kHalves;
-        const Row row = row_of(a, it, it.row0 + tile * a.plan.tile);
-        tc::tma_3d(q + tile * S::kTile + half * (128 * 128), qmap, half * 64, it.head * a.group, row.token, &sh.q_full);
-      }
-    }
-  } else {
+  // queries that no tensor map can bring: elements, into the swizzled order the products read
+  if (!a.q_map) {
+    if (piece > 0) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last results have left the queries' space
     constexpr int kPer = D / 8, kRows = kSoftmaxThreads / kPer;   // threads of a row, rows at a time
     const int c = tid % kPer;
+    uint8_t* dst = q + (it.nt == 1 ? (piece & 1) * S::kTile : 0);
     for (int x = tid / kPer; x < it.nt * 128; x += kRows) {
       const int tile = x >> 7, in = x & 127, r = it.row0 + tile * a.plan.tile + in;
       uint4 w = make_uint4(0, 0, 0, 0);
@@ -525,14 +543,11 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
         const uint16_t* h = static_cast<const uint16_t*>(a.q) + row.token * a.q_stride + row.head * D + c * 8;
         w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
       }
-      *reinterpret_cast<uint4*>(q + tile * S::kTile + (c >> 3) * (128 * 128) + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = w;
+      *reinterpret_cast<uint4*>(dst + tile * S::kTile + (c >> 3) * (128 * 128) + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = w;
     }
     tc::fence_async_smem();
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (tid == 0) {
-      tc::fence_after();
-      mbar_arrive(&sh.q_full);
-    }
+    if (tid == 0) mbar_arrive(&sh.q_full[piece & 1]);
   }
 
   const int r = it.row0 + (it.nt == 2 ? t * a.plan.tile : 0) + lane_row;
@@ -588,8 +603,11 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
         }
         const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (!((w[c >> 5] >> (c & 31)) & 1)) s[c] = 0xFF800000u;  // -inf
+        for (int c = 0; c < BN; c += 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((w[c >> 5] >> i) & 1)) s[c + i] = 0xFF800000u;  // -inf
+        }
       }
       const float* sf = reinterpret_cast<const float*>(s);
       float mx[4] = {sf[0], sf[1], sf[2], sf[3]};
@@ -661,12 +679,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
   if (units > 0 && ok) ok = __all_sync(~0u, wait_bar(sh, a, &sh.o_done[t], results++ & 1));
   float l = l2.x + l2.y;
   const bool two = it.nt == 1 && it.blocks > 1;      // two sums of one row to join
-  // of a shared tile each group leaves its maximum and sum where its scores were
-  if (it.nt == 1 && units > 0 && ok) {
-    tc::fence_after();
-    tc::st2(tmem + t * 128, m, l);
-    tc::fence_before();
-  }
+  if (it.nt == 1 && units > 0) sh.ml[t][lane_row] = make_float2(m, l);
   // both groups' products are done, so the queries' space is free; and both take one decision when a wait has run out
   int all_ok;
   asm volatile(
@@ -679,14 +692,26 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
                                        it.row0 / (it.nt * a.plan.tile) * a.c.kv_heads + it.head;
   // everybody has read what belonged to the piece two before; cleaning is at most the ring's 4 blocks ahead of this one
   if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
-  if (!warp_live) continue;
+  // a warp's last words on a piece: its reads of tensor memory are over; so are its writes to the queries' space
+  auto released = [&](unsigned long long* bar) {
+    tc::fence_before();
+    tc::fence_async_smem();
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(bar);
+  };
+  if (!warp_live) {
+    released(&sh.o_free);
+    released(&sh.q_free[piece & 1]);
+    continue;
+  }
   const uint64_t bad = sh.bad[piece & 7];
   float f0 = 1.f, f1 = 0.f;
-  if (it.nt == 1) tc::ld2(tmem, m, l);
+  if (it.nt == 1) {
+    m = sh.ml[0][lane_row].x;
+    l = sh.ml[0][lane_row].y;
+  }
   if (two) {
-    const float m0 = m;
-    float m1, l1;
-    tc::ld2(tmem + 128, m1, l1);
+    const float m0 = m, m1 = sh.ml[1][lane_row].x, l1 = sh.ml[1][lane_row].y;
     m = fmaxf(m0, m1);
     if (m != -INFINITY) {
       f0 = ex2(m0 - m);
@@ -702,7 +727,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
   const bool part = it.dest != kFinal;
   const int slot = part_row(a, it.dest, it.b < 0, at, blockIdx.x, (it.nt == 2 ? t * 128 : 0) + lane_row);
   const int code = !live ? -1 : part ? slot : row.token << 10 | row.head;
-  uint8_t* stage = q + (tid >> 5) * 4096;            // every product is done: the queries' space is free
+  // every product is done: the piece's queries are no longer needed
+  uint8_t* stage = q + (D == 128 ? (it.nt == 1 ? (piece & 1) * S::kTile : 0) : S::kStage) + (tid >> 5) * 4096;
   // of a shared tile each group writes half of the columns
   const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
   const uint32_t o_at = tmem + 256 + (it.nt == 1 ? 0 : t * D);
@@ -732,6 +758,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
         }
       }
     }
+    if (c + 32 == c_end) released(&sh.o_free);
     store_rows<T, D>(a, stage, code, part, f, c);
   }
   if (live && (it.nt == 2 || t == 0)) {
@@ -739,6 +766,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q, const CU
     if (part) a.part_lse[slot] = lse2;
     else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
   }
+  released(&sh.q_free[piece & 1]);
   }
 }
 
@@ -800,9 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_kv_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D>;
-  extern __shared__ uint8_t raw[];
-  __shared__ Bars sh;
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t base[];  // all of the kernel's: it starts where swizzled tiles may
+  Bars& sh = *reinterpret_cast<Bars*>(base + S::kBars);
   const int warp = threadIdx.x >> 5;
   grid_dependents_launch();
   if (threadIdx.x == 0) {
@@ -813,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.clean[i], 2);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
-    mbar_init(&sh.q_full, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); }
+    mbar_init(&sh.o_free, 8);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 8; ++i) sh.bad[i] = 0;
     sh.abort = 0;
@@ -827,10 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   if (warp < kTmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<T, D>(a, sh, base, &qmap);
+    softmax_role<T, D>(a, sh, base);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kTmaWarp) load_role<D>(a, sh, base + S::kRing, &kmap, &vmap);
+    if (warp == kTmaWarp) load_role<D>(a, sh, base, base + S::kRing, &qmap, &kmap, &vmap);
     else if (warp == kMmaWarp) {
       if (tc::elect()) mma_role<T, D>(a, sh, base, base + S::kRing);
       __syncwarp();
@@ -842,58 +870,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 
+template <int D>
+constexpr int kSmem = Smem<D>::kBars + (int)sizeof(Bars);
+
 // Joins the partial results of a row and head, in the order of their keys: D / 4 lanes a row, 16 bytes a lane.  Every
 // row has two items to join when items are packed; else only rows of cut items have anything to: CTA row y then is an
 // item, or (by_cta, with more items than CTAs) the CTA of an item's first piece, which has said which item that is
 // (line[batch + 1 + y], -1: none).  What it takes is latency: a thread asks for P partials of R rows at once.
 template <typename T, int D, int R, int P>
 __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_constant__ AttendArgs a, int by_cta) {
-  constexpr int kLanes = D / 4;
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+  __shared__ int held[8];  // the CTAs that hold the first and the last piece: of the item, of the packed item, of the next
   const AttendPlan& p = a.plan;
   const int lane = threadIdx.x % kLanes, items = p.tiles_b * a.c.kv_heads;
+  const int per = a.slots * a.group, rows_a = p.nt_a * p.tile, rows_b = p.nt_b * p.tile;
   int b = blockIdx.z, item = blockIdx.y;
   grid_dependency_wait();
-  const int64_t chunk = a.line[a.batch];
   if (by_cta) {
     const int64_t said = a.line[a.batch + 1 + blockIdx.y];
     if (said < 0) return;
     b = (int)(said / items);
     item = (int)(said - (int64_t)b * items);
   }
-  // the CTAs that hold pieces of an item: the last one's is the item's partial, the others' are by CTA; the quotients
-  // are CTA numbers, so a product with the fp32 reciprocal is right to one
-  const float inv_chunk = 1.f / (float)chunk;
-  auto cta_of = [&](int64_t x) -> int {
-    int c = (int)((float)x * inv_chunk);
-    if ((int64_t)c * chunk > x) --c;
-    if ((int64_t)(c + 1) * chunk <= x) ++c;
-    return c;
-  };
   const int tile_b = a.by_heads.div(item), kv_head = item - tile_b * a.c.kv_heads;
-  const int blocks = blocks_of(a, ctx_of(a, b));
-  const int64_t start_b = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed_b;
-  const int b_first = cta_of(start_b), b_last = cta_of(start_b + (int64_t)(blocks - 1) * p.step_b);
+  const int first = tile_b * rows_b + blockIdx.x * R * kRows;  // the CTA's first row of the request
+  const int tile_a = p.packed ? (b * per + first) / rows_a : 0;
+  if (threadIdx.x < 6) {
+    const int np = (a.prefix_len + BN - 1) / BN, which = threadIdx.x >> 1;
+    const int64_t chunk = a.line[a.batch];
+    int64_t at;
+    if (which == 0) {
+      const int blocks = blocks_of(a, ctx_of(a, b));
+      at = a.line[b] + (int64_t)item * cost_b(a, blocks) + p.fixed_b + (threadIdx.x & 1 ? (int64_t)(blocks - 1) * p.step_b : 0);
+    } else {
+      at = (int64_t)((tile_a + which - 1) * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed_a;
+      if (threadIdx.x & 1) at += (int64_t)(np - 1) * p.step_a;
+    }
+    // a CTA's number, so a product with the fp32 reciprocal is right to one
+    int c = (int)((float)at * (1.f / (float)chunk));
+    if ((int64_t)c * chunk > at) --c;
+    if ((int64_t)(c + 1) * chunk <= at) ++c;
+    held[threadIdx.x] = c;
+  }
+  __syncthreads();
+  const int b_first = held[0], b_last = held[1];
   if (!p.packed && b_first == b_last) return;  // whole, and written
-  const int per = a.slots * a.group;
-  int row[R], at[R], in_a[R], a_first[R], na[R], n[R], most = 0;
+  int row[R], token[R], head[R], in_a[R], a_first[R], na[R], n[R], most = 0;
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    row[k] = (blockIdx.x * R + k) * (256 / kLanes) + threadIdx.x / kLanes;
-    const int in_b = tile_b * p.nt_b * p.tile + row[k];
-    at[k] = -1;
+    row[k] = (blockIdx.x * R + k) * kRows + threadIdx.x / kLanes;
+    const int in_b = tile_b * rows_b + row[k];
     n[k] = na[k] = in_a[k] = a_first[k] = 0;
-    if (in_b >= per || row[k] >= p.nt_b * p.tile) continue;
+    token[k] = head[k] = 0;
+    if (in_b >= per || row[k] >= rows_b) continue;
     const int slot = a.by_group.div(in_b);
-    at[k] = (b * a.slots + slot) * a.c.q_heads + kv_head * a.group + in_b - slot * a.group;
+    token[k] = b * a.slots + slot;
+    head[k] = kv_head * a.group + in_b - slot * a.group;
     if (p.nt_b == 2 && row[k] >= p.tile) row[k] += 128 - p.tile;  // place in its CTA's partial
     if (p.packed) {
-      in_a[k] = b * per + in_b;
-      const int tile_a = in_a[k] / (p.nt_a * p.tile), np = (a.prefix_len + BN - 1) / BN;
-      in_a[k] -= tile_a * p.nt_a * p.tile;
+      in_a[k] = b * per + in_b - tile_a * rows_a;
+      const bool next = in_a[k] >= rows_a;
+      if (next) in_a[k] -= rows_a;
       if (p.nt_a == 2 && in_a[k] >= p.tile) in_a[k] += 128 - p.tile;
-      const int64_t start_a = (int64_t)(tile_a * a.c.kv_heads + kv_head) * cost_a(a) + p.fixed_a;
-      a_first[k] = cta_of(start_a);
-      na[k] = cta_of(start_a + (int64_t)(np - 1) * p.step_a) - a_first[k] + 1;
+      a_first[k] = held[next ? 4 : 2];
+      na[k] = held[next ? 5 : 3] - a_first[k] + 1;
     }
     n[k] = na[k] + b_last - b_first + 1;
     most = max(most, n[k]);
@@ -920,7 +960,7 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
         const bool of_a = i < na[k];
         const int cta = of_a ? a_first[k] + i : b_first + i - na[k];
         const bool last = of_a ? i == na[k] - 1 : cta == b_last;
-        const int r = part_row(a, last ? kItemPart : kCtaPart, of_a, at[k], cta, of_a ? in_a[k] : row[k]);
+        const int r = part_row(a, last ? kItemPart : kCtaPart, of_a, token[k] * a.c.q_heads + head[k], cta, of_a ? in_a[k] : row[k]);
         z[k][j] = a.part_lse[r];
         v[k][j] = *reinterpret_cast<const float4*>(parts + (int64_t)r * D);
       }
@@ -944,10 +984,9 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
   }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    if (at[k] < 0) continue;
+    if (n[k] == 0) continue;
     const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
-    const int token = at[k] / a.c.q_heads, head = at[k] - token * a.c.q_heads;
-    T* out = static_cast<T*>(a.out) + token * a.out_stride + head * D + lane * 4;
+    T* out = static_cast<T*>(a.out) + token[k] * a.out_stride + head[k] * D + lane * 4;
     const uint2 w = make_uint2(Pair<T>::put(acc[k].x * inv, acc[k].y * inv), Pair<T>::put(acc[k].z * inv, acc[k].w * inv));
     if (a.out_vec) {
       *reinterpret_cast<uint2*>(out) = w;
@@ -955,7 +994,8 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
       uint16_t* h = reinterpret_cast<uint16_t*>(out);
       h[0] = (uint16_t)w.x; h[1] = (uint16_t)(w.x >> 16); h[2] = (uint16_t)w.y; h[3] = (uint16_t)(w.y >> 16);
     }
-    if (lane == 0 && a.lse) a.lse[at[k]] = sum[k] == 0.f ? -INFINITY : (top[k] + log2f(sum[k])) * 0.6931471805599453f;
+    if (lane == 0 && a.lse)
+      a.lse[token[k] * a.c.q_heads + head[k]] = sum[k] == 0.f ? -INFINITY : (top[k] + log2f(sum[k])) * 0.6931471805599453f;
   }
 }
 
@@ -963,7 +1003,7 @@ template <typename T, int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t s) {
   const AttendPlan& p = a.plan;
-  k_kv_attend<T, D><<<p.ctas, kThreads, Smem<D>::kBytes, s>>>(a, qmap, kmap, vmap);
+  k_kv_attend<T, D><<<p.ctas, kThreads, kSmem<D>, s>>>(a, qmap, kmap, vmap);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.cut) {
     // many rows have few partials each
@@ -980,7 +1020,7 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
 
 template <typename T, int D>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(k_kv_attend<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  return cudaFuncSetAttribute(k_kv_attend<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
 }
 
 }  // namespace
@@ -1004,8 +1044,8 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
   const bool wide = dim == 128;
-  const int two = wide ? 152 : 145, one = wide ? 85 : 125, fixed_two = wide ? 650 : 480, fixed_one = wide ? 350 : 310;
-  const int memory = wide ? 120 : 60, l2 = wide ? 70 : 35;
+  const int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 440, fixed_one = wide ? 350 : 450;
+  const int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
   AttendPlan best{};
   double best_t = 0;
   for (int packed = 0; packed < 2; ++packed) {
