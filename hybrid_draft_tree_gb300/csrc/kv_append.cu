@@ -96,6 +96,8 @@ __device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, 
 // One CTA a token.  A thread takes pieces of heads: those of q, of k and of v, in turn.
 template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kThreads) k_kv_append(AppendArgs a) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int64_t n = blockIdx.x;
   const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
   const int r = a.rows ? a.rows[n] : i;
@@ -160,6 +162,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(AppendArgs a) {
 // The same by elements and rotating pairs, for any alignment and any rot_dim.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_kv_append_elements(AppendArgs a) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   const int64_t n = blockIdx.x;
   const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
   const int r = a.rows ? a.rows[n] : i;
@@ -186,11 +190,9 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_elements(AppendArgs a) {
 
 template <typename T>
 cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((int64_t)a.batch * a.slots);
-  if (!a.vec) k_kv_append_elements<T><<<grid, kThreads, 0, s>>>(a);
-  else if (a.c.interleaved) k_kv_append<T, false><<<grid, kThreads, 0, s>>>(a);
-  else k_kv_append<T, true><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((int64_t)a.batch * a.slots));
+  if (!a.vec) return launch_dependent(k_kv_append_elements<T>, grid, dim3(kThreads), 0, s, a);
+  return launch_dependent(a.c.interleaved ? k_kv_append<T, false> : k_kv_append<T, true>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

@@ -848,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sh.tmem, 512);
+  grid_dependency_wait();
   find_line(a, sh, reinterpret_cast<int64_t*>(base));
   tc::fence_async_smem();  // copies will land where the sums were
   tc::fence_before();
@@ -885,6 +886,7 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
   const int lane = threadIdx.x % kLanes, items = p.tiles_b * a.c.kv_heads;
   const int per = a.slots * a.group, rows_a = p.nt_a * p.tile, rows_b = p.nt_b * p.tile;
   int b = blockIdx.z, item = blockIdx.y;
+  grid_dependents_launch();
   grid_dependency_wait();
   if (by_cta) {
     const int64_t said = a.line[a.batch + 1 + blockIdx.y];
@@ -1003,8 +1005,7 @@ template <typename T, int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t s) {
   const AttendPlan& p = a.plan;
-  k_kv_attend<T, D><<<p.ctas, kThreads, kSmem<D>, s>>>(a, qmap, kmap, vmap);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(k_kv_attend<T, D>, dim3(p.ctas), dim3(kThreads), kSmem<D>, s, a, qmap, kmap, vmap);
   if (e == cudaSuccess && p.cut) {
     // many rows have few partials each
     const bool many = p.rows > 8192;

@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
   uint32_t* const ranks = bitmap + a.chunk / 32 + 1;   // how many lie before a word of the bitmap
   uint16_t* const list = reinterpret_cast<uint16_t*>(ranks + a.chunk / 32 + 1);  // they, in order
   uint32_t bad = 0;
+  grid_dependents_launch();
+  grid_dependency_wait();
   // the first of the history on its way while the table is cleared
   const int32_t* const hist = a.r.d_hist + (int64_t)b * a.r.hist_stride;
   int n_hist = 0, prompt = 0;
@@ -324,8 +326,7 @@ static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(k_logit_rules<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
   }
-  k_logit_rules<T><<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(k_logit_rules<T>, grid, dim3(kThreads), smem, s, a);
 }
 
 cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s) {
