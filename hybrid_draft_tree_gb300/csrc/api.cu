@@ -28,6 +28,7 @@ struct graft_handle {
   int warm_ctas = 0;        // resident CTAs of the warm-up scan
   int scan_ctas_target = 0; // CTAs wanted per verify launch
   bool tma_ready = false;   // the TMA scan's shared-memory opt-in succeeded
+  bool rules_ready = false; // the logit rules' did
   int32_t* C = nullptr;           // [V][8]
   int32_t* winner = nullptr;      // [V]
   int32_t* tpl = nullptr;         // [3][tpl_len]: parent, rank, depth; then [tpl_len + 1]: depth maxima of prefixes
@@ -298,6 +299,7 @@ int graft_init(const graft_config* cfg, graft_handle** out) {
   h->warm_ctas = h->num_sms * 4;
   h->scan_ctas_target = h->num_sms * 8;
   h->tma_ready = graft::prepare_verify_tma() == cudaSuccess;
+  h->rules_ready = graft::prepare_logit_rules() == cudaSuccess;
   h->cluster_max_active = graft::cluster_select_max_active(cfg->vocab, cfg->logits_dtype);
   cudaGetLastError();
   *out = h;
@@ -785,6 +787,7 @@ int graft_process_logits(graft_handle* h, int32_t batch, int32_t slots, const in
   const uintptr_t out1 = out0 + (last * (uintptr_t)out_stride + c.vocab) * es;
   if (in0 < out1 && out0 < in1 && !(in0 == out0 && row_stride == out_stride))
     return fail(h, GRAFT_EINVAL, "d_out overlaps d_logits without being it at the same stride");
+  if (!h->rules_ready) return fail(h, GRAFT_ECUDA, "the logit rules' shared memory is not available on this device");
   graft::LogitArgs a{};
   a.r = r;
   if (!a.r.d_hist) a.r.hist_stride = 0;

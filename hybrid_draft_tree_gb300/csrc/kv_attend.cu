@@ -886,7 +886,6 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
   const int lane = threadIdx.x % kLanes, items = p.tiles_b * a.c.kv_heads;
   const int per = a.slots * a.group, rows_a = p.nt_a * p.tile, rows_b = p.nt_b * p.tile;
   int b = blockIdx.z, item = blockIdx.y;
-  grid_dependents_launch();
   grid_dependency_wait();
   if (by_cta) {
     const int64_t said = a.line[a.batch + 1 + blockIdx.y];

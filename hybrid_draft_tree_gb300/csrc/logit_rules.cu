@@ -308,6 +308,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
 
 }  // namespace
 
+constexpr int kMaxChunk = 16384;
+
+static size_t smem_bytes(int chunk) { return kWarps * kUnit * 16 + (size_t)chunk * 6 + 2 * (chunk / 32 + 1) * 4; }
+
+cudaError_t prepare_logit_rules() {
+  const int most = (int)smem_bytes(kMaxChunk);
+  cudaError_t e = cudaFuncSetAttribute(k_logit_rules<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_logit_rules<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return e;
+}
+
 template <typename T>
 static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
   // Every CTA reads the request's whole history: a chunk grows while that is more than an eighth of what its rows move
@@ -315,18 +326,13 @@ static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
   const int pass = kThreads * Elem<T>::N;
   a.chunk = pass;
   auto ctas = [&](int chunk) { return (int64_t)a.batch * ((a.V + chunk - 1) / chunk); };
-  while (a.chunk < 16384 && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
+  while (a.chunk < kMaxChunk && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
          ctas(2 * a.chunk) >= 2 * num_sms)
     a.chunk *= 2;
   const int64_t groups = std::max<int64_t>(1, std::min<int64_t>((a.slots + 3) / 4, 4 * num_sms / ctas(a.chunk)));
   a.rows_per_cta = (int)((a.slots + groups - 1) / groups);
   const dim3 grid((a.V + a.chunk - 1) / a.chunk, a.batch, (a.slots + a.rows_per_cta - 1) / a.rows_per_cta);
-  const size_t smem = kWarps * kUnit * 16 + (size_t)a.chunk * 6 + 2 * (a.chunk / 32 + 1) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_logit_rules<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_dependent(k_logit_rules<T>, grid, dim3(kThreads), smem, s, a);
+  return launch_dependent(k_logit_rules<T>, grid, dim3(kThreads), smem_bytes(a.chunk), s, a);
 }
 
 cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s) {

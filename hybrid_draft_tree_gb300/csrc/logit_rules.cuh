@@ -16,6 +16,7 @@ struct LogitArgs {
   uint32_t* err;
 };
 
+cudaError_t prepare_logit_rules();  // once a device: the shared-memory opt-in
 cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s);
 
 }  // namespace graft

@@ -293,6 +293,10 @@ ATTEND = [
     ("bf16", 1, 2, 2500, [600], 2, 2, 64, 64, "token"),
     ("bf16", 20, 1, 700, list(range(0, 600, 30)), 8, 2, 128, 16, "head"),
     ("f16", 1, 64, 0, [0], 96, 1, 128, 64, "head"),             # 6144 rows of one head
+    ("bf16", 1, 3, 200, [150], 130, 1, 128, 16, "head"),        # a group of more than 128 query heads
+    ("bf16", 2, 2, 0, [5, 140], 300, 2, 64, 32, "token"),
+    ("f16", 500, 1, 140, [b % 37 for b in range(500)], 2, 1, 64, 16, "head"),   # more requests than a CTA has threads
+    ("bf16", 3, 50, 260, [513, 40, 128], 21, 7, 128, 8, "token"),   # rows that fill no tile: 126 of 128
 ]
 
 
@@ -467,6 +471,32 @@ def test_attend_repeats_bit_for_bit_and_from_a_graph_and_another_stream():
     graph.replay()
     assert kv.sync() == 0
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_attend_waits_are_bounded():
+    """With a limit of one poll the kernel's waits run out: the call ends, says so, and the handle works on."""
+    rng, gen = np.random.default_rng(4), torch.Generator(device="cuda").manual_seed(4)
+    pre, table, pages = tables(rng, 3, 700, 300, 16)
+    k, v = (make_cache(gen, pages, 2, 16, 128, torch.bfloat16, "head") for _ in range(2))
+    kv = g.GraftKV(g.graft_kv_default_config(8, 2, 128, 16, pages, 3, 40))
+    table, pre, ctx = cuda(table), cuda(pre), cuda(np.array([600, 1, 300], np.int32))
+    for slots in (1, 40):
+        q = torch.randn((3 * slots, 8 * 128), generator=gen, device="cuda", dtype=torch.bfloat16)
+        outs = [torch.zeros_like(q) for _ in range(2)]
+        call = lambda o: kv.attend(3, slots, q, k, v, table, ctx, 600, o, prefix_pages=pre, prefix_len=300)  # noqa: E731
+        call(outs[0])
+        assert kv.sync() == 0
+        kv.set_wait_limit(1)
+        call(outs[1])
+        assert kv.sync(raise_on_error=False) == gb.GRAFT_ERR_TIMEOUT
+        with pytest.raises(g.GraftError, match="timeout 1"):
+            call(outs[1])
+            kv.sync()
+        kv.set_wait_limit(0)
+        outs[1].zero_()
+        call(outs[1])
+        assert kv.sync() == 0
+        assert torch.equal(outs[0], outs[1])
 
 
 def test_offsets_beyond_32_bits():
