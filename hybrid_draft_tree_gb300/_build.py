@@ -4,13 +4,16 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgraft.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")   # the binding's per-layer calls, a CPython extension
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ("api.cu", "assemble.cu", "scan.cu", "umax.cu", "select.cu", "coverage.cu", "sample.cu", "scan_tma.cu", "noalloc.cu",
            "cluster_select.cu", "logit_rules.cu", "kv.cu", "kv_append.cu", "kv_attend.cu")
@@ -23,7 +26,25 @@ def _newest_input() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_fastcall(force: bool = False) -> str | None:
+    """The extension, or None where Python's headers or a C compiler are missing (the binding then makes those calls
+    itself)."""
+    include = sysconfig.get_paths()["include"]
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    src = os.path.join(CSRC, "fastcall.c")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "graft.h")))
+    if not force and os.path.exists(FASTCALL) and os.path.getmtime(FASTCALL) >= newest:
+        return FASTCALL
+    tmp = FASTCALL + f".tmp{os.getpid()}"
+    subprocess.check_call([cc, "-O2", "-fPIC", "-shared", "-I" + include, "-I" + INCLUDE, src, "-o", tmp])
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_fastcall(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

@@ -229,7 +229,16 @@ class _Types:
 
     def __getattr__(self, name):
         import torch
-        v = (torch.int64, torch.uint64) if name == "mask" else getattr(torch, name)
+        if name == "mask":
+            v = (torch.int64, torch.uint64)
+        elif name == "current_stream":
+            device, stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+            def v():
+                return stream(device())
+            torch.cuda.init()
+        else:
+            v = getattr(torch, name)
         setattr(self, name, v)
         return v
 
@@ -307,9 +316,35 @@ def _cache(t, name, dtype, span):
 
 def _stream_addr(stream):
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _T.current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _load_fastcall():
+    """The extension that makes the per-layer calls, or None when it is not built."""
+    import importlib.machinery
+    import importlib.util
+    if not os.path.exists(_build.FASTCALL):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_fastcall", _build.FASTCALL)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
+    loader.exec_module(module)
+    return module
+
+
+class _Entry:
+    """The extension, the address of the library's entry point and the handle's, for one handle's fast calls."""
+
+    def __init__(self, lib, name, handle):
+        global _fastcall
+        if _fastcall is False:
+            _fastcall = _load_fastcall()
+        self.module = _fastcall
+        self.at = ctypes.cast(getattr(lib, name), vp).value
+        self.handle = handle.value
+
+
+_fastcall = False
 
 
 def _stream(stream):
@@ -337,6 +372,8 @@ def graft_default_config(vocab, max_batch, mode=GRAFT_MODE_CHECKPOINT, logits_dt
 class Graft:
     """One libgraft handle (owns the continuation matrix on the current device)."""
 
+    _fast = None
+
     def __init__(self, cfg: graft_config):
         self.L = load()
         self.cfg = cfg
@@ -346,12 +383,14 @@ class Graft:
         if rc != GRAFT_OK:
             raise GraftError(rc, "graft_init failed (bad config, no CUDA device, or out of memory)")
         self.h = h
+        self._fast = _Entry(self.L, "graft_process_logits", h)
 
     def _check(self, rc):
         if rc != GRAFT_OK:
             raise GraftError(rc, self.L.graft_last_error(self.h).decode())
 
     def close(self):
+        self._fast = None
         if self.h:
             self.L.graft_destroy(self.h)
             self.h = None
@@ -480,6 +519,13 @@ class Graft:
         [batch, 3] (repetition, frequency, presence); bias_tok, bias_val:
         [batch, entries]; grammar: int32 [rows, >= ceil(V / 32)] bits;
         grammar_row: int32 [batch, slots].  A rule that is None is off."""
+        f = self._fast
+        if f is not None and f.module is not None:
+            rc = f.module.logits(f.at, f.handle, _stream_addr(stream), self._logits_dtype(), _T.float32, _T.int32, _T.int64,
+                                 self.cfg.vocab, batch, slots, logits, out, tree_tok, tree_mask, hist, hist_len, prompt_len,
+                                 penalty, bias_tok, bias_val, grammar, grammar_row)
+            if rc is not NotImplemented:
+                return self._check(rc)
         b = max(batch, 0)
         n, V, ldt, i32 = b * slots, self.cfg.vocab, self._logits_dtype(), _T.int32
         pl, stride = _row_addr(logits, "logits", ldt, n, V)
@@ -567,6 +613,8 @@ class GraftKV:
     target's keys, values and attention around a draft tree.  The caches are
     the caller's tensors."""
 
+    _append = _attend = None
+
     def __init__(self, cfg: graft_kv_config):
         import torch
         self.L = load()
@@ -581,12 +629,14 @@ class GraftKV:
         if rc != GRAFT_OK:
             raise GraftError(rc, "graft_kv_init failed (bad config, no CUDA device, or out of memory)")
         self.h = h
+        self._append, self._attend = _Entry(self.L, "graft_kv_append", h), _Entry(self.L, "graft_kv_attend", h)
 
     def _check(self, rc):
         if rc != GRAFT_OK:
             raise GraftError(rc, self.L.graft_kv_last_error(self.h).decode())
 
     def close(self):
+        self._append = self._attend = None
         if self.h:
             self.L.graft_kv_destroy(self.h)
             self.h = None
@@ -604,6 +654,13 @@ class GraftKV:
         [batch * slots, heads * head_dim], any row stride; rope: float32
         [positions, rot_dim]; page_table: int32 [batch, pages]; pos: the slots'
         depths (tree_pos); rows: int32 [batch, slots], the slot each place takes."""
+        f = self._append
+        if f is not None and f.module is not None:
+            rc = f.module.append(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, self.q_width,
+                                 self.kv_width, self.rot_dim, self.span, batch, slots, prefix_len, q, k, v, rope, page_table,
+                                 ctx_len, k_cache, v_cache, q_out, pos, rows)
+            if rc is not NotImplemented:
+                return self._check(rc)
         b, dt, i32 = max(batch, 0), self.dtype, _T.int32
         n = b * slots
         pq, qs = _row_addr(q, "q", dt, n, self.q_width)
@@ -625,6 +682,14 @@ class GraftKV:
         """Attention of the slots' rotated queries over the prefix, each
         request's ctx_len (<= max_ctx) tokens and the tree under tree_mask
         (None: causal), into out and lse.  scale defaults to head_dim ** -0.5."""
+        f = self._attend
+        if f is not None and f.module is not None:
+            rc = f.module.attend(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, _T.int64,
+                                 self.q_width, self.q_heads, self.page_size, self.span, batch, slots, prefix_len, max_ctx,
+                                 self.scale if scale is None else scale, q, k_cache, v_cache, page_table, ctx_len, out,
+                                 prefix_pages, tree_mask, lse)
+            if rc is not NotImplemented:
+                return self._check(rc)
         b, dt, i32 = max(batch, 0), self.dtype, _T.int32
         n = b * slots
         pq, qs = _row_addr(q, "q", dt, n, self.q_width)

@@ -761,6 +761,39 @@ def test_process_logits_then_verify():
     assert emitted[0, :21].tolist() == list(range(1, 21)) + [999]
 
 
+def test_calls_are_the_same_without_the_extension():
+    """The binding's own form of a call (when the extension is not built, or an argument is not its usual kind) does what
+    the extension's does; a closed handle refuses."""
+    rng, gen = np.random.default_rng(8), torch.Generator(device="cuda").manual_seed(8)
+    pre, table, pages = tables(rng, 2, 120, 40, 16)
+    q, k, v = (torch.randn((10, w * 64), generator=gen, device="cuda", dtype=torch.bfloat16) for w in (4, 2, 2))
+    rope, mask = torch.rand((300, 64), generator=gen, device="cuda"), torch.full((2, 5), 31, device="cuda")
+    table, pre, ctx = cuda(table), cuda(pre), cuda(np.array([100, 3], np.int32))
+    kv = g.GraftKV(g.graft_kv_default_config(4, 2, 64, 16, pages, 2, 5))
+    x = torch.randn((10, 700), generator=gen, device="cuda").bfloat16()
+    eng = g.Graft(g.graft_default_config(700, 2, g.GRAFT_MODE_STATIC, g.GRAFT_BF16))
+    hist = cuda(rng.integers(0, 700, (2, 9)).astype(np.int32))
+    results = []
+    for fast in (True, False):
+        if not fast:
+            kv._append = kv._attend = eng._fast = None
+        kc, vc = (make_cache(torch.Generator(device="cuda").manual_seed(1), pages, 2, 16, 64, torch.bfloat16, "head") for _ in range(2))
+        qo, out, lse, y = torch.empty_like(q), torch.empty_like(q), torch.empty((10, 4), device="cuda"), torch.empty_like(x)
+        kv.append(2, 5, q, k, v, rope, table, ctx, kc, vc, qo, prefix_len=40)
+        kv.attend(2, 5, qo, kc, vc, table, ctx, 100, out, prefix_pages=pre, prefix_len=40, tree_mask=mask, lse=lse)
+        kv.attend(2, 5, qo, kc, vc, table, ctx, 100, out, prefix_pages=pre, prefix_len=40, tree_mask=mask.view(torch.uint64), lse=lse)
+        eng.process_logits(2, 5, x, y, hist=hist, hist_len=cuda(np.array([9, 4], np.int32)),
+                           penalty=torch.full((2, 3), 1.5, device="cuda"))
+        results.append((kc, vc, qo, out, lse, y))
+        assert kv.sync() == 0 and eng.sync() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    for h, f in ((kv, lambda: kv.attend(2, 5, q, kc, vc, table, ctx, 100, out)), (eng, lambda: eng.process_logits(2, 5, x, y))):
+        h.close()
+        with pytest.raises(g.GraftError) as e:
+            f()
+        assert e.value.code == gb.GRAFT_EINVAL
+
+
 # ------------------------------------------------------------------------------------------------------- refusals
 def test_refusals_of_live_handles():
     """Argument errors come back at once, name themselves and queue nothing."""
