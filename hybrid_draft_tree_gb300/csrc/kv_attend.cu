@@ -42,8 +42,8 @@ namespace {
 using namespace bulk;
 
 constexpr int kSoftmaxThreads = 256, kThreads = 384;
-// 384 threads start with 168 registers each; the softmax groups' 256 take 216, the rest keep 72: 64512 either way
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// 384 threads start with 168 registers each; the softmax groups' 256 take 224, the rest keep 56: 64512 either way
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
@@ -154,6 +154,7 @@ struct Bars {
   unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
   float2 ml[2][128];             // a shared tile's maxima and sums
   Line line;
+  int loads, queries;            // loads that were asked for, the last piece whose queries were
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -308,11 +309,18 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
     last_two = two;
   }
   if (bad) atomicOr(a.err, bad);
-  if (!ok && lane == 0) {  // the copies in flight land before the CTA ends
-    for (int x = max(0, loads - S::kStages); x < loads; ++x)
-      mbar_wait_drain(&sh.full[x % S::kStages], (x / S::kStages) & 1);
-    for (int x = max(0, q_last - 1); x <= q_last; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
+  if (lane == 0) {
+    sh.loads = loads;
+    sh.queries = q_last;
   }
+}
+
+// After a wait that ran out, whoever's: the copies in flight land before the CTA ends.
+template <int D>
+__device__ void drain_copies(Bars& sh) {
+  constexpr int kStages = Smem<D>::kStages;
+  for (int x = max(0, sh.loads - kStages); x < sh.loads; ++x) mbar_wait_drain(&sh.full[x % kStages], (x / kStages) & 1);
+  for (int x = max(0, sh.queries - 1); x <= sh.queries; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
 }
 
 // ---- warps 10, 11: values that no row may see --------------------------------------------------------------------
@@ -692,16 +700,21 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
                                        it.row0 / (it.nt * a.plan.tile) * a.c.kv_heads + it.head;
   // everybody has read what belonged to the piece two before; cleaning is at most the ring's 4 blocks ahead of this one
   if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
-  // a warp's last words on a piece: its reads of tensor memory are over; so are its writes to the queries' space
-  auto released = [&](unsigned long long* bar) {
+  // a warp's last words on a piece: its reads of tensor memory are over; so is its use of the queries' space
+  auto read = [&] {
     tc::fence_before();
-    tc::fence_async_smem();
     __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(bar);
+    if ((tid & 31) == 0) mbar_arrive(&sh.o_free);
   };
+  auto written = [&] {
+    if (D == 128) tc::fence_async_smem();
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(&sh.q_free[piece & 1]);
+  };
+  if (D == 64) written();                            // results do not pass through it
   if (!warp_live) {
-    released(&sh.o_free);
-    released(&sh.q_free[piece & 1]);
+    read();
+    if (D == 128) written();
     continue;
   }
   const uint64_t bad = sh.bad[piece & 7];
@@ -727,7 +740,6 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const bool part = it.dest != kFinal;
   const int slot = part_row(a, it.dest, it.b < 0, at, blockIdx.x, (it.nt == 2 ? t * 128 : 0) + lane_row);
   const int code = !live ? -1 : part ? slot : row.token << 10 | row.head;
-  // every product is done: the piece's queries are no longer needed
   uint8_t* stage = q + (D == 128 ? (it.nt == 1 ? (piece & 1) * S::kTile : 0) : S::kStage) + (tid >> 5) * 4096;
   // of a shared tile each group writes half of the columns
   const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
@@ -758,7 +770,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
         }
       }
     }
-    if (c + 32 == c_end) released(&sh.o_free);
+    if (c + 32 == c_end) read();
     store_rows<T, D>(a, stage, code, part, f, c);
   }
   if (live && (it.nt == 2 || t == 0)) {
@@ -766,7 +778,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
     if (part) a.part_lse[slot] = lse2;
     else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
   }
-  released(&sh.q_free[piece & 1]);
+  if (D == 128) written();
   }
 }
 
@@ -868,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  if (threadIdx.x == 0 && sh.abort) drain_copies<D>(sh);
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 
