@@ -534,6 +534,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   constexpr float kGrow = kGrowth<T>;
   const float scale = a.scale * kLog2e;
   uint32_t scores = 0, results = 0, piece = 0;
+  bool dead = false;                                 // a wait has run out: only the barriers of both groups are left
   Pieces pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); ++piece) {
@@ -566,7 +567,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const int units = it.nt == 2 ? it.blocks : (it.blocks + 1 - t) >> 1;
   float m = live ? -INFINITY : 0.f;                 // lanes without a row never wait
   float2 l2 = make_float2(0.f, 0.f);
-  bool ok = true;
+  bool ok = !dead;
   for (int n = 0; n < units && ok; ++n) {
     const Block k = block_of(a, it, it.nt == 2 ? n : 2 * n + t);
     ok = __all_sync(~0u, wait_bar(sh, a, &sh.s_full[t], scores++ & 1));
@@ -688,17 +689,21 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   float l = l2.x + l2.y;
   const bool two = it.nt == 1 && it.blocks > 1;      // two sums of one row to join
   if (it.nt == 1 && units > 0) sh.ml[t][lane_row] = make_float2(m, l);
-  // both groups' products are done, so the queries' space is free; and both take one decision when a wait has run out
-  int all_ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}"
-      : "=r"(all_ok) : "r"((int)ok) : "memory");
-  if (!all_ok) return;
+  // the groups of a shared tile join their results, and take one decision when a wait has run out
+  if (it.nt == 1) {
+    int all_ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}"
+        : "=r"(all_ok) : "r"((int)ok) : "memory");
+    ok = all_ok;
+  }
+  dead = !ok;
+  if (dead) continue;
   tc::fence_after();
   if (tid == 0 && it.dest == kCtaPart && it.first == 0 && it.b >= 0)
     a.line[a.batch + 1 + blockIdx.x] = (int64_t)it.b * a.plan.tiles_b * a.c.kv_heads +
                                        it.row0 / (it.nt * a.plan.tile) * a.c.kv_heads + it.head;
-  // everybody has read what belonged to the piece two before; cleaning is at most the ring's 4 blocks ahead of this one
+  // everybody has read O of the piece before, and what belonged to those before that; cleaning is at most the ring's 4 blocks ahead of this one
   if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
   // a warp's last words on a piece: its reads of tensor memory are over; so is its use of the queries' space
   auto read = [&] {
@@ -745,17 +750,15 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const int c_begin = it.nt == 1 ? t * (D / 2) : 0, c_end = it.nt == 1 ? c_begin + D / 2 : D;
   const uint32_t o_at = tmem + 256 + (it.nt == 1 ? 0 : t * D);
   for (int c = c_begin; c < c_end; c += 32) {
-    uint32_t o[32];
+    uint32_t o[64];
     float f[32];
     tc::ld32(o_at + c, o);
-    tc::wait_ld<32>(o);
+    tc::ld32(o_at + (two ? D : 0) + c, o + 32);
+    tc::wait_ld<64>(o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : __uint_as_float(o[i]) * f0;
-    if (two) {
-      tc::ld32(o_at + D + c, o);
-      tc::wait_ld<32>(o);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] += none ? 0.f : __uint_as_float(o[i]) * f1;
+    for (int i = 0; i < 32; ++i) {
+      const float x = __uint_as_float(o[i]) * f0;
+      f[i] = none ? 0.f : two ? x + __uint_as_float(o[32 + i]) * f1 : x;
     }
     if (bad & mask) {
       for (uint64_t w = bad & mask; w; w &= w - 1) {
