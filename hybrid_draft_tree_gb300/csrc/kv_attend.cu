@@ -275,7 +275,8 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
     auto page_of = [&](int j) -> int {
       const Block k = block_of(a, it, j);
       const int q = lane / S::kHalves;
-      if (q >= pages || (q << a.c.page_shift) >= k.valid) return -1;
+      if (q >= pages) return -1;
+      if ((q << a.c.page_shift) >= k.valid) return a.c.num_pages;  // past the last key: zeros
       const int at = (k.base >> a.c.page_shift) + q;
       int page = k.prefix ? a.prefix_pages[at] : a.page_table[(int64_t)it.b * a.table_stride + at];
       if (page < 0 || page >= a.c.num_pages) {                // reads as zeros
@@ -290,13 +291,12 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
       if (!ok) break;
       const int here = page;
       if (j + 1 < it.blocks) page = page_of(j + 1);
-      const int copies = __popc(__ballot_sync(~0u, here >= 0));
       for (int v = 0; v < 2 && ok; ++v) {
         const int stage = loads % S::kStages;
         ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh.full[stage], copies * page_bytes);
+        if (lane == 0) mbar_expect_tx(&sh.full[stage], S::kTile);
         __syncwarp();
         if (here >= 0)
           tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + (lane / S::kHalves) * page_bytes,
@@ -347,6 +347,7 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
       ok = ok && wait_bar(sh, a, &sh.full[stage], (x / S::kStages) & 1);
       if (!__all_sync(~0u, ok)) return;
       const int tree = k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid);  // first row that is a slot
+      const int end = (k.valid + a.c.page_size - 1) & -a.c.page_size;  // of the last page; zeros follow
       uint4* p = reinterpret_cast<uint4*>(ring + stage * S::kTile);
 #pragma unroll 1
       for (int half = 0; half < S::kHalves; ++half, p += 128 * 8) {
@@ -366,7 +367,7 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
           }
         }
 #pragma unroll 4
-        for (int i = k.valid * 8 + thread; i < BN * 8; i += 64) p[i] = make_uint4(0, 0, 0, 0);
+        for (int i = k.valid * 8 + thread; i < end * 8; i += 64) p[i] = make_uint4(0, 0, 0, 0);
       }
       tc::fence_async_smem();
       __syncwarp();
