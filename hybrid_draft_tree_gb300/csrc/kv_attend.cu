@@ -1061,7 +1061,7 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
   const bool wide = dim == 128;
-  const int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 440, fixed_one = wide ? 350 : 450;
+  const int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 400, fixed_one = wide ? 280 : 450;
   const int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
   AttendPlan best{};
   double best_t = 0;
