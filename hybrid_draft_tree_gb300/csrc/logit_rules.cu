@@ -5,17 +5,21 @@
 // the history, the bias entry, whether a slot's token falls there), so that the
 // history is read once a chunk and not once a row, and turns it into what an
 // element with a rule needs: what is taken off its logit, and whether it counts
-// as seen.  Then its warps take the rows in units of eight 16-byte pieces a lane.
-// Nearly every element has no rule: a unit is masked by its bits of the
-// grammar's row and stored; when some of its elements have rules, it passes
-// through shared memory, where they are done a lane each (in the pieces they
-// would cost the whole warp a pass for each of a lane's).  Bound by memory: a
-// row is read and written once; in place, units without a rule or a grammar are
-// not touched.
+// as seen.  Then its warps take the rows in units of four or eight 16-byte
+// pieces a lane.  Nearly every element has no rule: a unit is masked by its bits
+// of the grammar's row and stored; when some of its elements have rules, it
+// passes through shared memory, where they are done a lane each (in the pieces
+// they would cost the whole warp a pass for each of a lane's).  A row is read and
+// written once; in place, units without a rule or a grammar are not touched.
+// Bound by memory where a CTA has many rows (16 x 61 x 151936 bf16: 106 us, 5.5
+// TB/s, 82% of the copy rate), by the table's building where it has few (64 x 17
+// x 128256 behind 8192 tokens: 114 us, 4.7 TB/s), by latency for one row of 32000
+// (5.2 us).
 //
 // Rows need not start on 16-byte boundaries: the pieces are those of the row's
 // own alignment, so the bits are read at the row's offset, and the few elements
-// before its first and after its last piece go one by one.
+// before its first and after its last piece go one by one (so do rows whose input
+// and output are aligned differently: 515 us instead of 106).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -25,8 +29,14 @@
 namespace graft {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kLane = 8, kUnit = 32 * kLane; // pieces that a lane, a warp takes at a time
+// Threads of a CTA, 16-byte pieces that a lane takes at a time, CTAs an SM.
+template <int THREADS, int LANE, int CTAS>
+struct Shape {
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kLane = LANE, kUnit = 32 * LANE, kCtas = CTAS;
+  static size_t smem(int chunk) { return kWarps * kUnit * 16 + (size_t)chunk * 6 + 2 * (chunk / 32 + 1) * 4; }
+};
+using FewRows = Shape<384, 4, 3>;
+using ManyRows = Shape<512, 8, 2>;
 constexpr int kHeld = 8;                     // tokens of the history that a thread has in flight
 // a table entry while the rules are gathered
 constexpr uint32_t COUNT = (1u << 19) - 1;  // occurrences in the output (the history is shorter than 2^19)
@@ -109,11 +119,11 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int n
   return __funnelshift_r(lo, hi, s) & ((1u << n) - 1);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs a) {
   extern __shared__ uint4 space[];  // a unit a warp; the table [chunk]; bitmap, ranks [chunk / 32 + 1]; the list [chunk] of 16 bits
   __shared__ Shared sh;
-  constexpr int N = Elem<T>::N;
+  constexpr int N = Elem<T>::N, kThreads = S::kThreads, kWarps = S::kWarps, kLane = S::kLane, kUnit = S::kUnit;
   const int b = blockIdx.y, t = threadIdx.x;
   const int c0 = blockIdx.x * a.chunk, c1 = min(a.V, c0 + a.chunk), len = c1 - c0;
   const int i0 = blockIdx.z * a.rows_per_cta, i1 = min(a.slots, i0 + a.rows_per_cta);
@@ -241,30 +251,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
 
   const int n_rows = sh.n_rows, units = a.chunk / (kUnit * N);
   const bool in_place = a.in == a.out;
-  for (int u = t >> 5; u < n_rows * units; u += kWarps) {
-    const int r = u / units, part = u - r * units, i = sh.rows[r];
+  struct Row { const T* in; T* out; const uint32_t* gram; int slot; };
+  auto row_at = [&](int r) {
+    const int i = sh.rows[r];
     const int64_t row = (int64_t)b * a.slots + i;
-    const T* in = static_cast<const T*>(a.in) + row * a.in_stride + c0;
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + c0;
-    const uint32_t* gram = sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr;
-    auto forbidden = [&](int k) { return gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1); };
-    auto element = [&](int k) {
-      if (forbidden(k)) out[k] = Elem<T>::put(-INFINITY);
-      else if ((bitmap[k >> 5] >> (k & 31)) & 1) out[k] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(in[k])));
-      else out[k] = in[k];
-    };
-    const uint32_t from = (uint32_t)reinterpret_cast<uintptr_t>(in) & 15, to = (uint32_t)reinterpret_cast<uintptr_t>(out) & 15;
-    if (from != to) {
-      for (int k = part * kUnit * N + lane; k < min(len, (part + 1) * kUnit * N); k += 32) element(k);
+    return Row{static_cast<const T*>(a.in) + row * a.in_stride + c0, static_cast<T*>(a.out) + row * a.out_stride + c0,
+               sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr, i};
+  };
+  auto forbidden = [&](const uint32_t* gram, int k) { return gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1); };
+  auto element = [&](const Row& r, int k) {
+    if (forbidden(r.gram, k)) r.out[k] = Elem<T>::put(-INFINITY);
+    else if ((bitmap[k >> 5] >> (k & 31)) & 1) r.out[k] = Elem<T>::put(apply(sh, bias, table[k], r.slot, c0 + k, Elem<T>::get(r.in[k])));
+    else r.out[k] = r.in[k];
+  };
+  auto offset = [](const T* p) { return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) & 15); };
+  for (int u = t >> 5; u < n_rows * units; u += kWarps) {
+    const int r = u / units, part = u - r * units;
+    const Row row = row_at(r);
+    const T* const in = row.in;
+    T* const out = row.out;
+    const uint32_t* const gram = row.gram;
+    const int i = row.slot, from = offset(in);
+    if (from != offset(out)) {
+      for (int k = part * kUnit * N + lane; k < min(len, (part + 1) * kUnit * N); k += 32) element(row, k);
       continue;
     }
     const int off = min(len, (int)(((16 - from) & 15) / sizeof(T))), pieces = (len - off) / N;
-    if (part == 0)
-      for (int k = lane; k < len - pieces * N; k += 32) element(k < off ? k : k + pieces * N);
     const int k0 = off + min(pieces, part * kUnit) * N, k1 = off + min(pieces, (part + 1) * kUnit) * N;  // of the unit
     const int e0 = rank(k0), e1 = rank(k1);
     if (in_place && !gram) {
-      for (int e = e0 + lane; e < e1; e += 32) element(list[e]);
+      for (int e = e0 + lane; e < e1; e += 32) element(row, list[e]);
       continue;
     }
     const int n = (k1 - k0) / N;
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
       for (int e = e0 + lane; e < e1; e += 32) {
         const int k = list[e];
         // what the grammar forbids is -inf already, and stays so whatever its rule takes off
-        if (!forbidden(k)) values[k - k0] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(values[k - k0])));
+        if (!forbidden(gram, k)) values[k - k0] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(values[k - k0])));
       }
       __syncwarp();
 #pragma unroll
@@ -304,35 +320,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_logit_rules(LogitArgs a) {
     for (int j = 0; j < kLane; ++j)
       if (lane + 32 * j < n) __stcs(dst + lane + 32 * j, x[j]);
   }
+  // elements before a row's first piece and after its last, from the end on: the last warps have the fewest units
+  if ((len % N | offset(static_cast<const T*>(a.in) + c0) | (a.in_stride % N)) == 0) return;
+  for (int e = kThreads - 1 - t; e < n_rows * 2 * N; e += kThreads) {
+    const Row row = row_at(e / (2 * N));
+    const int x = e & (2 * N - 1), from = offset(row.in);
+    if (from != offset(row.out)) continue;
+    const int off = min(len, (int)(((16 - from) & 15) / sizeof(T))), pieces = (len - off) / N;
+    if (x < len - pieces * N) element(row, x < off ? x : x + pieces * N);
+  }
 }
 
 }  // namespace
 
-constexpr int kMaxChunk = 16384;
+constexpr int kMaxChunk = 6144;
 
-static size_t smem_bytes(int chunk) { return kWarps * kUnit * 16 + (size_t)chunk * 6 + 2 * (chunk / 32 + 1) * 4; }
+template <typename T, typename S>
+static cudaError_t prepare() {
+  return cudaFuncSetAttribute(k_logit_rules<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(kMaxChunk));
+}
 
 cudaError_t prepare_logit_rules() {
-  const int most = (int)smem_bytes(kMaxChunk);
-  cudaError_t e = cudaFuncSetAttribute(k_logit_rules<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_logit_rules<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  cudaError_t e = prepare<__nv_bfloat16, FewRows>();
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16, ManyRows>();
+  if (e == cudaSuccess) e = prepare<float, FewRows>();
+  if (e == cudaSuccess) e = prepare<float, ManyRows>();
   return e;
 }
 
-template <typename T>
+static int64_t ctas_of(const LogitArgs& a, int chunk) { return (int64_t)a.batch * ((a.V + chunk - 1) / chunk); }
+
+template <typename T, typename S>
 static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
-  // Every CTA reads the request's whole history: a chunk grows while that is more than an eighth of what its rows move
-  // and two CTAs an SM remain; rows are split, four at least, when the chunks alone give fewer than four.
-  const int pass = kThreads * Elem<T>::N;
+  // Every CTA reads the request's whole history: while that is more than an eighth of what its rows move, a chunk grows
+  // as long as two CTAs an SM remain and three fit (64 x 17 behind 8192: 122 us with 3072 elements, 114 with 6144, 161
+  // with 12288).  When the chunks alone are too few for the SMs, rows are split too, four at least, into one wave of CTAs
+  // (1 x 61 behind 32768: 22 us; into 4 CTAs an SM 33, into one 26).
+  const int pass = S::kThreads * Elem<T>::N;
   a.chunk = pass;
-  auto ctas = [&](int chunk) { return (int64_t)a.batch * ((a.V + chunk - 1) / chunk); };
-  while (a.chunk < kMaxChunk && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
-         ctas(2 * a.chunk) >= 2 * num_sms)
+  while (2 * a.chunk <= kMaxChunk && a.r.hist_stride * 32 > (int64_t)a.slots * a.chunk * (int)sizeof(T) * 2 &&
+         ctas_of(a, 2 * a.chunk) >= 2 * num_sms)
     a.chunk *= 2;
-  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>((a.slots + 3) / 4, 4 * num_sms / ctas(a.chunk)));
+  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>((a.slots + 3) / 4, 3 * num_sms / ctas_of(a, a.chunk)));
   a.rows_per_cta = (int)((a.slots + groups - 1) / groups);
   const dim3 grid((a.V + a.chunk - 1) / a.chunk, a.batch, (a.slots + a.rows_per_cta - 1) / a.rows_per_cta);
-  return launch_dependent(k_logit_rules<T>, grid, dim3(kThreads), smem_bytes(a.chunk), s, a);
+  return launch_dependent(k_logit_rules<T, S>, grid, dim3(S::kThreads), S::smem(a.chunk), s, a);
+}
+
+// With many rows a CTA the pieces in flight count (16 x 61 x 151936: 106 us with eight a lane, 109 with four), with few
+// how many CTAs build their tables at once (64 x 17 x 128256: 114 us with three an SM, 129 with two; one row of 32000:
+// 5.2 and 6.0).
+template <typename T>
+static cudaError_t launch(const LogitArgs& a, int num_sms, cudaStream_t s) {
+  const bool many = a.slots >= 32 && ctas_of(a, ManyRows::kThreads * Elem<T>::N) >= 2 * num_sms;
+  return many ? launch<T, ManyRows>(a, num_sms, s) : launch<T, FewRows>(a, num_sms, s);
 }
 
 cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s) {

@@ -580,6 +580,9 @@ LOGITS = [
     ("bf16", 1, 61, 128256, 0, 0, 4, 0, 0),
     ("bf16", 5, 1, 4097, 30000, 7, 5, 0, 0),       # a long history, one slot
     ("bf16", 1, 2, 31, 5, 3, 2, 0, 0),
+    ("bf16", 32, 33, 40009, 60, 9, 3, 0, 0),       # many rows and chunks enough for all SMs, odd rows
+    ("f32", 32, 32, 20012, 60, 9, 3, 0, 0),
+    ("bf16", 40, 1, 50001, 9000, 5, 3, 0, 0),      # long histories, chunks enough to grow
 ]
 
 
