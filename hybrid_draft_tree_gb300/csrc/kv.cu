@@ -223,6 +223,7 @@ int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   const bool rows16 = !misaligned(d_k, 16) && !misaligned(d_v, 16) && k_stride % 8 == 0 && v_stride % 8 == 0 &&
                       (!d_q || (!misaligned(d_q, 16) && !misaligned(d_q_out, 16) && q_stride % 8 == 0 &&
                                 q_out_stride % 8 == 0));
+  // 16-byte pieces where rows and rotating halves allow them, else elements (1 x 32768: 127 and 427 us; 16 x 61: 6.5 and 26)
   a.vec = rows16 && c.rot % (c.interleaved ? 8 : 16) == 0 && !misaligned(d_rope, 16);
   a.by_slots = graft::Divisor(slots);
   a.by_turn = graft::Divisor(c.dim / 8 - (c.interleaved ? 0 : c.rot / 16));
@@ -265,14 +266,14 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   a.prefix_pages = d_prefix_pages; a.prefix_len = prefix_len;
   a.page_table = d_page_table; a.table_stride = table_stride; a.ctx_len = d_ctx_len; a.max_ctx = max_ctx;
   a.tree_mask = d_tree_mask; a.scale = scale; a.out = d_out; a.lse = d_lse; a.err = h->err;
-  a.q_vec = !misaligned(d_q, 16) && q_stride % 8 == 0;
   a.out_vec = !misaligned(d_out, 16) && out_stride % 8 == 0;
   a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms);
   a.part_o = h->part_o; a.part_lse = h->part_lse; a.line = h->line; a.wait_polls = h->wait_polls;
   a.by_group = graft::Divisor(a.group);
-  a.by_rows = graft::Divisor(slots * a.group);
   a.by_heads = graft::Divisor(c.kv_heads);
-  a.q_map = a.q_vec && a.group <= 128 && q_stride < ((int64_t)1 << 38);
+  // A tensor map needs rows on 16-byte boundaries; other queries come by elements (16 x 61 behind 12001 + 2048: 167 us by
+  // map, 181 by elements; 64 x 1 behind 8192 + 1024: 60 and 72).
+  a.q_map = !misaligned(d_q, 16) && q_stride % 8 == 0 && a.group <= 128 && q_stride < ((int64_t)1 << 38);
   CUtensorMap qmap{}, kmap, vmap;
   if (a.q_map && !query_map(c, h->cfg.dtype, d_q, (int64_t)batch * slots, q_stride, a.group, &qmap))
     return fail(h, GRAFT_ECUDA, "the driver refused the queries' tensor map");

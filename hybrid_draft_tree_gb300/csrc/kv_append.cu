@@ -4,6 +4,14 @@
 // A token at position p turns each pair (a, b) of a rotating head's elements by
 // the pair's angle: (a c - b s, b c + a s), with c and s read from the row of p
 // in the caller's table, so any scaling of the angles is the caller's.
+//
+// A CTA a token, 128 threads, two 16-byte pieces (and their partners) a thread in
+// flight; the source rows are on their way before the page table has answered.
+// Bound by memory when there are many tokens (1 x 32768, 32/8 heads of 128: 127
+// us, 6.4 TB/s, 95% of the copy rate; every element is read and written once), by
+// the latency of launch, page table and row when there are few (16 x 61: 6.5 us,
+// 3.7 TB/s; one token: 3.0 us).  256 threads or three pieces a thread were no
+// faster.
 #include "kv_internal.cuh"
 
 namespace graft {

@@ -30,6 +30,17 @@
 // ragged the lengths are, the SMs end together, and the ring of keys and values
 // runs on from item to item.  What a cut item's pieces found (normalised O and
 // log-sum-exp, fp32) is joined by a second kernel, in the order of the keys.
+//
+// Measured (bf16, 32/8 heads of 128 unless said otherwise), and what bounds it:
+//   16 x 61 slots behind 12001 + 2048 keys   165 us, 1300 TFLOP/s: a block of 256
+//       rows takes 1.5 us, its operands' way through shared memory (256 KB);
+//   64 x 1 behind 8192 + 1024                 59 us, 3.9 TB/s: memory, then the
+//       start (4.5 us to the first scores) and the join (5 us);
+//   1 x 61 behind 32768, pages of 16          43 us, 3.1 TB/s: the copies' issue
+//       (one warp: 5.4 TB/s of 4 KB rows), start, ends and join;
+//   64 x 17 behind 2048 + 777, 40/8 heads of 64, f16, pages of 16   86 us:
+//       exponentials, the issuing thread, pieces' ends (4 us each);
+//   1 x 1 behind 117                           6.9 us: latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -1023,7 +1034,8 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
   const AttendPlan& p = a.plan;
   cudaError_t e = launch_dependent(k_kv_attend<T, D>, dim3(p.ctas), dim3(kThreads), kSmem<D>, s, a, qmap, kmap, vmap);
   if (e == cudaSuccess && p.cut) {
-    // many rows have few partials each
+    // many rows have few partials each: two rows a thread take 167 us where one takes 174 (16 x 61 behind 12001, with the
+    // main kernel), 86 and 91 (64 x 17, heads of 64), but 51 where one takes 43 (1 x 61 behind 32768)
     const bool many = p.rows > 8192;
     const int rows = std::min(a.slots * a.group, p.nt_b * p.tile), items = p.tiles_b * a.c.kv_heads;
     const int each = (many ? 2 : 1) * 1024 / D;
@@ -1056,6 +1068,9 @@ int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int6
 // units of 10 ns, measured on one SM: a key block of 128 against two tiles of 128 rows, against one, and the least a block
 // takes when its keys and values come from memory (the SM's share of the copy rate) or from L2, where other items' SMs
 // read them too; before its first block an item pays for its queries, and the pipeline's start and end.
+// Both sides, in us: packed 60 and joined 226 (64 x 1 behind 8192 + 1024), 86 and 100 (64 x 17 behind 2048 + 777, heads
+// of 64), 179 and 167 (16 x 61 behind 12001 + 2048); two tiles and one 167 and 195 in the last, 43 and 61 (1 x 61 behind
+// 32768); whole and cut 6.9 and 10.4 (1 x 1 behind 117).
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int num_sms) {
   const int64_t R = (int64_t)slots * group, all = batch * R;

@@ -69,8 +69,8 @@ struct AttendArgs {
   float scale;
   void* out;
   float* lse;
-  int32_t q_map, q_vec, out_vec;  // 1 = queries come by tensor map; rows start on 16-byte boundaries
-  Divisor by_group, by_rows, by_heads;  // group, slots * group, kv_heads
+  int32_t q_map, out_vec;  // 1 = queries come by tensor map; the output's rows start on 16-byte boundaries
+  Divisor by_group, by_heads;  // group, kv_heads
   AttendPlan plan;
   float *part_o, *part_lse;  // partial results (rows of dim) and their log-sum-exp in log2
   int64_t* line;             // [batch] starts of the requests' items; a CTA's share; [ctas] items that a CTA begins and does not end
