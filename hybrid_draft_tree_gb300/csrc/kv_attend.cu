@@ -5,9 +5,9 @@
 // of the head's query heads) against a range of key blocks of 128.  Its CTA:
 //   warps 0-3, 4-7   two softmax groups, a thread a row: scores out of tensor
 //                    memory, running maximum and sum, weights back into it;
-//   warp 8           keys and values by tensor map, a page a copy, into a ring;
+//   warp 8 (and 10)  keys and values by tensor map, a page a copy, into a ring;
 //   warp 9           S = Q K^T and O += P V, fp32 accumulators in tensor memory;
-//   warps 10, 11     values of places that no row may see, made harmless.
+//   warps (10), 11   values of places that no row may see, made harmless.
 // The groups alternate so that one's products run under the other's softmax.
 // With more than 128 rows each group has its own 128 (every block's keys and
 // values serve both); with fewer both share the rows and take the key blocks in
@@ -55,7 +55,7 @@ using namespace bulk;
 constexpr int kSoftmaxThreads = 256, kThreads = 384;
 // 384 threads start with 168 registers each; the softmax groups' 256 take 224, the rest keep 56: 64512 either way
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kSpareWarp = 10, kCleanWarp = 11;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 of how far a maximum may run ahead of the base: weights stay inside the type and their sums inside fp32
@@ -244,12 +244,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return reinterpret_cast<float2&>(d);
 }
 
-// ---- warp 8: keys and values into the ring ----------------------------------------------------------------------
-template <int D>
+// ---- warp 8, and 10 with small pages: keys and values into the ring ----------------------------------------------
+// L of them: a copy takes its warp some 75 cycles to issue.
+template <int D, int L>
 __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
                           const CUtensorMap* vmap) {
   using S = Smem<D>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, own = L == 1 ? 0 : (threadIdx.x >> 5) != kTmaWarp;  // the warp's number
   const int pages = BN >> a.c.page_shift;                   // of a block; a copy is a page's half
   const int page_bytes = a.c.page_size * 128;
   int loads = 0;
@@ -281,14 +282,14 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
       q_last = (int)piece;
       return true;
     };
-    const int q_at = two && piece > 0 ? min(2, it.blocks - 1) : 0;
-    // page of this lane's copy of block j: copy lane -> half lane % kHalves of page lane / kHalves
+    const int q_at = own ? -1 : two && piece > 0 ? min(2, it.blocks - 1) : 0;
+    // page of this lane's copy of block j: the warps take pages in turn, a page's halves side by side
+    const int place = lane / S::kHalves * L + own;
     auto page_of = [&](int j) -> int {
       const Block k = block_of(a, it, j);
-      const int q = lane / S::kHalves;
-      if (q >= pages) return -1;
-      if ((q << a.c.page_shift) >= k.valid) return a.c.num_pages;  // past the last key: zeros
-      const int at = (k.base >> a.c.page_shift) + q;
+      if (place >= pages) return -1;
+      if ((place << a.c.page_shift) >= k.valid) return a.c.num_pages;  // past the last key: zeros
+      const int at = (k.base >> a.c.page_shift) + place;
       int page = k.prefix ? a.prefix_pages[at] : a.page_table[(int64_t)it.b * a.table_stride + at];
       if (page < 0 || page >= a.c.num_pages) {                // reads as zeros
         bad = GRAFT_ERR_RANGE;
@@ -307,20 +308,20 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
         ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh.full[stage], S::kTile);
+        if (lane == 0 && own == 0) mbar_expect_tx(&sh.full[stage], S::kTile);  // all copies; the other's may land first
         __syncwarp();
         if (here >= 0)
-          tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + (lane / S::kHalves) * page_bytes,
+          tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + place * page_bytes,
                      v ? vmap : kmap, (lane % S::kHalves) * 64, 0, it.head, here, &sh.full[stage]);
         // values to clean: said once the stage's phase is this block's
-        if (v == 1 && lane == 0 && block_of(a, it, j).masked) mbar_arrive(&sh.dirty[stage]);
+        if (v == 1 && lane == 0 && own == 0 && block_of(a, it, j).masked) mbar_arrive(&sh.dirty[stage]);
         ++loads;
       }
     }
     last_two = two;
   }
   if (bad) atomicOr(a.err, bad);
-  if (lane == 0) {
+  if (lane == 0 && own == 0) {
     sh.loads = loads;
     sh.queries = q_last;
   }
@@ -334,15 +335,16 @@ __device__ void drain_copies(Bars& sh) {
   for (int x = max(0, sh.queries - 1); x <= sh.queries; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
 }
 
-// ---- warps 10, 11: values that no row may see --------------------------------------------------------------------
+// ---- warp 11, and 10 with large pages: values that no row may see --------------------------------------------------------------------
 // They must not reach a product as NaN or infinity (0 times them is NaN): rows past the last key are zeroed, and of the
 // tree's rows (a key that some rows see and others do not) the elements that are not finite; their slots are recorded,
 // and the rows that see them add those elements at the end.  It happens as soon as a block has landed, blocks ahead of
 // its products.
-template <typename T, int D>
+template <typename T, int D, int L>
 __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
   using S = Smem<D>;
-  const int lane = threadIdx.x & 31, thread = threadIdx.x - kCleanWarp * 32;
+  constexpr int kFirst = L == 2 ? kCleanWarp : kSpareWarp, kCleaners = (kCleanWarp + 1 - kFirst) * 32;
+  const int lane = threadIdx.x & 31, thread = threadIdx.x - kFirst * 32;
   constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
   uint32_t turn = 0;  // a bit a stage
   int before = 0, piece = 0;
@@ -363,7 +365,7 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
 #pragma unroll 1
       for (int half = 0; half < S::kHalves; ++half, p += 128 * 8) {
 #pragma unroll 4
-        for (int i = tree * 8 + thread; i < k.valid * 8; i += 64) {
+        for (int i = tree * 8 + thread; i < k.valid * 8; i += kCleaners) {
           const uint4 v = p[i];
           uint32_t e[4] = {v.x, v.y, v.z, v.w};
           bool any = false;
@@ -378,7 +380,7 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
           }
         }
 #pragma unroll 4
-        for (int i = k.valid * 8 + thread; i < end * 8; i += 64) p[i] = make_uint4(0, 0, 0, 0);
+        for (int i = k.valid * 8 + thread; i < end * 8; i += kCleaners) p[i] = make_uint4(0, 0, 0, 0);
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -850,7 +852,7 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int L>
 __global__ void __launch_bounds__(kThreads, 1)
     k_kv_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.dirty[i], 1);
-      mbar_init(&sh.clean[i], 2);
+      mbar_init(&sh.clean[i], 3 - L);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); }
@@ -886,11 +888,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<T, D>(a, sh, base);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kTmaWarp) load_role<D>(a, sh, base, base + S::kRing, &qmap, &kmap, &vmap);
+    if (warp == kTmaWarp || (L == 2 && warp == kSpareWarp)) load_role<D, L>(a, sh, base, base + S::kRing, &qmap, &kmap, &vmap);
     else if (warp == kMmaWarp) {
       if (tc::elect()) mma_role<T, D>(a, sh, base, base + S::kRing);
       __syncwarp();
-    } else if (warp >= kCleanWarp) clean_role<T, D>(a, sh, base + S::kRing);
+    } else clean_role<T, D, L>(a, sh, base + S::kRing);
   }
   tc::fence_before();
   __syncthreads();
@@ -1032,7 +1034,12 @@ template <typename T, int D>
 cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                    cudaStream_t s) {
   const AttendPlan& p = a.plan;
-  cudaError_t e = launch_dependent(k_kv_attend<T, D>, dim3(p.ctas), dim3(kThreads), kSmem<D>, s, a, qmap, kmap, vmap);
+  // Small pages' copies take two warps where items have one tile and blocks little else to do (8 x 1 behind 700, pages of
+  // 16: 12.6 us, 15.1 with one warp; 8 x 17 behind 300 + 600, heads of 64, pages of 32: 11.7 and 12.3); the ring's warps
+  // are in the way of more work (64 x 17 behind 2048 + 777, pages of 16: 88 us, 85.5 with one warp).
+  const bool two_loaders = a.c.page_size <= 32 && !p.packed && p.nt_b == 1;
+  cudaError_t e = launch_dependent(two_loaders ? k_kv_attend<T, D, 2> : k_kv_attend<T, D, 1>, dim3(p.ctas), dim3(kThreads),
+                                   kSmem<D>, s, a, qmap, kmap, vmap);
   if (e == cudaSuccess && p.cut) {
     // many rows have few partials each: two rows a thread take 167 us where one takes 174 (16 x 61 behind 12001, with the
     // main kernel), 86 and 91 (64 x 17, heads of 64), but 51 where one takes 43 (1 x 61 behind 32768)
@@ -1049,7 +1056,8 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
 
 template <typename T, int D>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(k_kv_attend<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
+  const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_kv_attend<T, D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D>);
 }
 
 }  // namespace
