@@ -1112,7 +1112,10 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     double t = work / num_sms + p.fixed_b + join;
     p.cut = 1;
     p.ctas = num_sms;
-    if (!packed && items_b <= num_sms && whole <= t) {
+    // With few items the costs of a busy machine are off by `off`: whole and cut are level at 500 keys for 1 x 61 slots (14.8
+    // us; at 1000 whole takes 20.5, cut 16.0), at 1000 for 1 x 1 (12.2; at 500 9.0 and 11.3), at 1900 for 8 x 1 (20).
+    const int off = p.nt_b == 2 ? (wide ? -400 : -200) : (wide ? -100 : 200);
+    if (!packed && items_b <= num_sms && whole <= t + off) {
       p.cut = 0;
       p.ctas = (int)items_b;
       t = whole;
