@@ -32,14 +32,15 @@
 // log-sum-exp, fp32) is joined by a second kernel, in the order of the keys.
 //
 // Measured (bf16, 32/8 heads of 128 unless said otherwise), and what bounds it:
-//   16 x 61 slots behind 12001 + 2048 keys   165 us, 1300 TFLOP/s: a block of 256
+//   16 x 61 slots behind 12001 + 2048 keys   166 us, 1290 TFLOP/s: a block of 256
 //       rows takes 1.5 us, its operands' way through shared memory (256 KB);
-//   64 x 1 behind 8192 + 1024                 59 us, 3.9 TB/s: memory, then the
+//   64 x 1 behind 8192 + 1024                 60 us, 3.9 TB/s: memory, then the
 //       start (4.5 us to the first scores) and the join (5 us);
 //   1 x 61 behind 32768, pages of 16          43 us, 3.1 TB/s: the copies' issue
 //       (one warp: 5.4 TB/s of 4 KB rows), start, ends and join;
 //   64 x 17 behind 2048 + 777, 40/8 heads of 64, f16, pages of 16   86 us:
-//       exponentials, the issuing thread, pieces' ends (4 us each);
+//       the latency from scores to weights to products (2700 cycles a unit of 128 x
+//       128, two units in flight), pieces' ends (4 us each);
 //   1 x 1 behind 117                           6.9 us: latency.
 #include <algorithm>
 #include <type_traits>
@@ -335,7 +336,7 @@ __device__ void drain_copies(Bars& sh) {
   for (int x = max(0, sh.queries - 1); x <= sh.queries; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
 }
 
-// ---- warp 11, and 10 with large pages: values that no row may see --------------------------------------------------------------------
+// ---- warp 11, and 10 with large pages: values that no row may see ------------------------------------------------
 // They must not reach a product as NaN or infinity (0 times them is NaN): rows past the last key are zeroed, and of the
 // tree's rows (a key that some rows see and others do not) the elements that are not finite; their slots are recorded,
 // and the rows that see them add those elements at the end.  It happens as soon as a block has landed, blocks ahead of
@@ -717,7 +718,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   if (tid == 0 && it.dest == kCtaPart && it.first == 0 && it.b >= 0)
     a.line[a.batch + 1 + blockIdx.x] = (int64_t)it.b * a.plan.tiles_b * a.c.kv_heads +
                                        it.row0 / (it.nt * a.plan.tile) * a.c.kv_heads + it.head;
-  // everybody has read O of the piece before, and what belonged to those before that; cleaning is at most the ring's 4 blocks ahead of this one
+  // everybody has read O of the piece before, and what belonged to those before that; cleaning is at most the ring's 4
+  // blocks ahead of this one
   if (tid == 0) sh.bad[(piece + 6) & 7] = 0;
   // a warp's last words on a piece: its reads of tensor memory are over; so is its use of the queries' space
   auto read = [&] {
