@@ -15,10 +15,9 @@
 //
 // The online softmax keeps, per row, a base m, l = sum 2^(s-m) and O = sum
 // 2^(s-m) v, s in units of log2.  m is the maximum of the row's first keys and
-// moves only when a later one exceeds it by 2^60 (2^12 with f16): until then
-// weights above 1 are as exact as below, O, which lives in tensor memory, is
-// not read and written back for every block, and the weights need not wait for
-// the block's maximum.
+// moves only when a later one exceeds it by 2^12: until then weights above 1 are
+// as exact as below, O, which lives in tensor memory, is not read and written
+// back for every block, and the weights need not wait for the block's maximum.
 //
 // Rows of all requests against the prefix are packed into the same tiles
 // ("packed"), so a prefix block is read once for up to 256 rows, when a
@@ -59,11 +58,8 @@ constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kSpareWarp = 10, kCleanWarp = 11;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
-// log2 of how far a maximum may run ahead of the base: weights stay inside the type and their sums inside fp32
-template <typename T>
-constexpr float kGrowth = 60.f;
-template <>
-constexpr float kGrowth<__half> = 12.f;
+// log2 of how far a maximum may run ahead of the base: weights stay inside f16, and sums of large values inside fp32
+constexpr float kGrow = 12.f;
 
 // Shared memory: two query tiles, the ring, where results pass on their way out, and the barriers.  A tile is stored in
 // column halves of 64 elements (128 bytes).  With D = 128 results pass through the query tile they belong to.
@@ -546,7 +542,6 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
   const uint32_t tmem = sh.tmem + lanes;
-  constexpr float kGrow = kGrowth<T>;
   const float scale = a.scale * kLog2e;
   uint32_t scores = 0, results = 0, piece = 0;
   bool dead = false;                                 // a wait has run out: only the barriers of both groups are left

@@ -297,6 +297,10 @@ ATTEND = [
     ("bf16", 2, 2, 0, [5, 140], 300, 2, 64, 32, "token"),
     ("f16", 500, 1, 140, [b % 37 for b in range(500)], 2, 1, 64, 16, "head"),   # more requests than a CTA has threads
     ("bf16", 3, 50, 260, [513, 40, 128], 21, 7, 128, 8, "token"),   # rows that fill no tile: 126 of 128
+    # more items than SMs, cut: of one tile with small pages, of two tiles
+    ("bf16", 60, 2, 0, [(37 * b) % 1900 for b in range(60)], 8, 4, 128, 32, "head"),
+    ("bf16", 30, 61, 0, [(53 * b) % 900 for b in range(30)], 32, 8, 64, 64, "head"),
+    ("f16", 24, 40, 0, [(71 * b) % 1300 for b in range(24)], 32, 8, 128, 16, "token"),
 ]
 
 
@@ -329,6 +333,20 @@ def test_attend_rising_scores():
             for at in range(int(ctx[b])):
                 k[table[b, at // page], at % page] *= 0.02 + at / 400.0
     run_attend("bf16", 2, 4, 0, [1500, 900], 4, 2, 128, 64, "head", tweak=tweak)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_large_values_behind_a_late_maximum(dim):
+    """Values of 1e25 whose keys outscore the first ones by 2^46: no intermediate sum leaves fp32."""
+    def tweak(rng, q, k, v, pre, table, ctx, mask, page):
+        q.zero_()
+        q.view(len(ctx), -1, 4, dim)[..., 0] = 8.0
+        k.zero_()
+        k[..., 0] = 4.0
+        for at in range(200):
+            k[table[0, at // page], at % page] = 0.0
+        v *= 1e25
+    run_attend("bf16", 1, 3, 0, [700], 4, 2, dim, 64, "head", scale=1.0, tweak=tweak)
 
 
 def test_attend_ctx_bound_above_every_length():
