@@ -33,7 +33,7 @@ namespace {
 template <int THREADS, int LANE, int CTAS>
 struct Shape {
   static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kLane = LANE, kUnit = 32 * LANE, kCtas = CTAS;
-  static size_t smem(int chunk) { return kWarps * kUnit * 16 + (size_t)chunk * 6 + 2 * (chunk / 32 + 1) * 4; }
+  static size_t smem(int chunk) { return kWarps * kUnit * 16 + (size_t)chunk * 6 + 3 * (chunk / 32 + 1) * 4; }
 };
 using FewRows = Shape<384, 4, 3>;
 using ManyRows = Shape<512, 8, 2>;
@@ -44,8 +44,9 @@ constexpr uint32_t PROMPT = 1u << 19;       // seen in the prompt
 constexpr int BIAS_SHIFT = 20;              // index of the bias entry + 1, 11 bits
 constexpr uint32_t BIAS = 0x7FFu << BIAS_SHIFT;
 constexpr uint32_t TREE = 1u << 31;         // the token of a slot
-// and then: the fp32 number taken off the logit, its lowest bit 1 for a token that was seen; or this NaN with the index
-// of a token that some slots' paths hold, whose count depends on the slot
+// and then: the fp32 number taken off the logit, all of its bits (a bias may be infinite, and f n beyond fp32; whether the
+// token was seen is in a bitmap of its own); or this NaN with the index of a token that some slots' paths hold, whose count
+// depends on the slot
 constexpr uint32_t PATH = 0xFFC00000u;
 
 // Elements and 16-byte pieces of them.
@@ -97,9 +98,8 @@ __device__ __forceinline__ float taken(const Shared& sh, const float* bias, uint
   return x;
 }
 
-// An element with a rule; i = the slot.
-__device__ __forceinline__ float apply(const Shared& sh, const float* bias, uint32_t entry, int i, int v, float x) {
-  bool seen = entry & 1;
+// An element with a rule; i = the slot, seen = the token occurs in the history (of a path's token the slot decides).
+__device__ __forceinline__ float apply(const Shared& sh, const float* bias, uint32_t entry, bool seen, int i, int v, float x) {
   float off = __uint_as_float(entry);
   if (entry >= PATH) {
     const uint32_t word = sh.path_word[entry - PATH];
@@ -121,7 +121,7 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int n
 
 template <typename T, typename S>
 __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs a) {
-  extern __shared__ uint4 space[];  // a unit a warp; the table [chunk]; bitmap, ranks [chunk / 32 + 1]; the list [chunk] of 16 bits
+  extern __shared__ uint4 space[];  // a unit a warp; the table [chunk]; two bitmaps, ranks [chunk / 32 + 1]; the list [chunk] of 16 bits
   __shared__ Shared sh;
   constexpr int N = Elem<T>::N, kThreads = S::kThreads, kWarps = S::kWarps, kLane = S::kLane, kUnit = S::kUnit;
   const int b = blockIdx.y, t = threadIdx.x;
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
   uint4* const stage = space + (t >> 5) * kUnit;
   uint32_t* const table = reinterpret_cast<uint32_t*>(space + kWarps * kUnit);
   uint32_t* const bitmap = table + a.chunk;            // elements with a rule
-  uint32_t* const ranks = bitmap + a.chunk / 32 + 1;   // how many lie before a word of the bitmap
+  uint32_t* const seen = bitmap + a.chunk / 32 + 1;    // elements whose token was seen
+  uint32_t* const ranks = seen + a.chunk / 32 + 1;     // how many lie before a word of the bitmap
   uint16_t* const list = reinterpret_cast<uint16_t*>(ranks + a.chunk / 32 + 1);  // they, in order
   uint32_t bad = 0;
   grid_dependents_launch();
@@ -212,7 +213,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
   const int lane = t & 31, words = a.chunk / 32;
   for (int k = t; k < a.chunk; k += kThreads) {
     const uint32_t word = table[k], ruled = __ballot_sync(~0u, word != 0);
-    if (lane == 0) bitmap[k >> 5] = ruled;
+    const uint32_t was_seen = __ballot_sync(~0u, (word & (COUNT | PROMPT)) != 0);
+    if (lane == 0) {
+      bitmap[k >> 5] = ruled;
+      seen[k >> 5] = was_seen;
+    }
     if (word == 0) continue;
     uint32_t entry;
     if (word & TREE) {
@@ -220,10 +225,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
       sh.path_word[path] = word;
       entry = PATH + path;
     } else {
-      const int n = word & COUNT;
-      const float off = taken(sh, bias, word, n);
-      entry = isnan(off) ? 0x7FC00000u : __float_as_uint(off) & ~1u;
-      if (n > 0 || (word & PROMPT)) entry |= 1;
+      const float off = taken(sh, bias, word, word & COUNT);
+      entry = isnan(off) ? 0x7FC00000u : __float_as_uint(off);
     }
     table[k] = entry;
   }
@@ -258,10 +261,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
     return Row{static_cast<const T*>(a.in) + row * a.in_stride + c0, static_cast<T*>(a.out) + row * a.out_stride + c0,
                sh.gram[i] >= 0 ? a.r.d_grammar + (int64_t)sh.gram[i] * a.r.grammar_stride : nullptr, i};
   };
+  auto ruled = [&](int k, int slot, T x) {
+    return Elem<T>::put(apply(sh, bias, table[k], (seen[k >> 5] >> (k & 31)) & 1, slot, c0 + k, Elem<T>::get(x)));
+  };
   auto forbidden = [&](const uint32_t* gram, int k) { return gram && !((gram[(c0 + k) >> 5] >> ((c0 + k) & 31)) & 1); };
   auto element = [&](const Row& r, int k) {
     if (forbidden(r.gram, k)) r.out[k] = Elem<T>::put(-INFINITY);
-    else if ((bitmap[k >> 5] >> (k & 31)) & 1) r.out[k] = Elem<T>::put(apply(sh, bias, table[k], r.slot, c0 + k, Elem<T>::get(r.in[k])));
+    else if ((bitmap[k >> 5] >> (k & 31)) & 1) r.out[k] = ruled(k, r.slot, r.in[k]);
     else r.out[k] = r.in[k];
   };
   auto offset = [](const T* p) { return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) & 15); };
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
       for (int e = e0 + lane; e < e1; e += 32) {
         const int k = list[e];
         // what the grammar forbids is -inf already, and stays so whatever its rule takes off
-        if (!forbidden(gram, k)) values[k - k0] = Elem<T>::put(apply(sh, bias, table[k], i, c0 + k, Elem<T>::get(values[k - k0])));
+        if (!forbidden(gram, k)) values[k - k0] = ruled(k, i, values[k - k0]);
       }
       __syncwarp();
 #pragma unroll

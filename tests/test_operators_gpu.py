@@ -727,6 +727,78 @@ def test_process_logits_infinities_and_nan(dtype):
         assert np.all(np.abs(low / ref - 1)[keep] <= 2 * U[dt])
 
 
+def _ruled(V, batch, slots, bias, r=1.2, f=0.5, p=0.1):
+    """Rules whose tokens are known: a chain of slots, prompt 20-22, output 30, 31, 31, 31, 5; `bias`: token -> value."""
+    s = dict(tok=np.tile(np.arange(5, 5 + slots, dtype=np.int32), (batch, 1)),
+             mask=np.array([[(1 << (i + 1)) - 1 for i in range(slots)]] * batch, np.uint64),
+             hist=np.tile(np.array([20, 21, 22, 30, 31, 31, 31, 5], np.int32), (batch, 1)),
+             hist_len=np.full(batch, 8, np.int32), prompt_len=np.full(batch, 3, np.int32),
+             penalty=np.tile(np.array([r, f, p], np.float32), (batch, 1)), bias_tok=None, bias_val=None, grammar=None,
+             gram_row=None)
+    if bias:
+        s["bias_tok"] = np.tile(np.array(list(bias), np.int32), (batch, 1))
+        s["bias_val"] = np.tile(np.array(list(bias.values()), np.float32), (batch, 1))
+    return s
+
+
+def _run_logits(dtype, V, batch, slots, s, x):
+    """The rules on x, out of place and then in place: both have to agree."""
+    eng = g.Graft(g.graft_default_config(V, batch, g.GRAFT_MODE_STATIC, g.GRAFT_F32 if dtype == "f32" else g.GRAFT_BF16))
+    out = torch.full_like(x, 9.0)
+    call_logits(eng, batch, slots, x, out, s)
+    y = x.clone()
+    call_logits(eng, batch, slots, y, y, s)
+    assert eng.sync() == 0
+    eng.close()
+    assert torch.equal(torch.where(torch.isnan(out), 0, out), torch.where(torch.isnan(y), 0, y))
+    assert torch.equal(torch.isnan(out), torch.isnan(y))
+    return out
+
+
+@pytest.mark.parametrize("rules", [(1.2, 0.5, 0.1), (1.3, 0.0, 0.0), (1.0, 0.0, 0.0)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_process_logits_infinite_biases(dtype, value, rules):
+    """A bias of -inf bans its token, one of +inf forces it, wherever the token has occurred: in the output (31), the
+    prompt (20), a slot's path (7, from slot 2 on), nowhere (400)."""
+    V, batch, slots = 1003, 2, 6
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x = torch.randn((batch * slots, V), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dt)
+    s = _ruled(V, batch, slots, {31: value, 20: value, 7: value, 400: value, 30: 1.5, 21: -1.5}, *rules)
+    out = _run_logits(dtype, V, batch, slots, s, x)
+    assert torch.all(out[:, [31, 20, 7, 400]] == value)
+    check_logits(out, x.double().cpu().numpy(), s, dt, V, slots)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_process_logits_frequency_beyond_the_types_range(dtype):
+    """f n that leaves fp32 is an infinity of its sign, not a NaN: 3 occurrences in the output, 2 on the path to slot 3."""
+    V, slots = 1003, 6
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x = torch.randn((slots, V), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(dt)
+    for sign in (1.0, -1.0):
+        s = _ruled(V, 1, slots, None, 1.2, sign * 3e38, 0.0)
+        s["tok"][0, 3] = s["tok"][0, 2]
+        out = _run_logits(dtype, V, 1, slots, s, x).float()
+        assert torch.all(out[:, 31] == -sign * math.inf)
+        assert torch.all(out[3:, 7] == -sign * math.inf) and torch.all(out[2, 7].abs() < math.inf)
+        assert torch.all((out[:, 30] + sign * 3e38).abs() < 2e36)
+
+
+def test_process_logits_keeps_every_bit_of_fp32():
+    """What a rule takes off is whole: a logit of 0 under a repetition penalty alone stays 0, and one of 0 under a bias
+    alone becomes the bias, for tokens of the output, the prompt, a path and none."""
+    V, slots = 1003, 6
+    x = torch.zeros((slots, V), device="cuda")
+    out = _run_logits("f32", V, 1, slots, _ruled(V, 1, slots, None, 1.3, 0.0, 0.0), x)
+    assert torch.all(out == 0)
+    odd = {t: float(np.float32(1 + k * 2.0 ** -23)) for k, t in zip((1, 3, 5, 7), (31, 20, 7, 400))}
+    for r in (1.3, 1.0):
+        out = _run_logits("f32", V, 1, slots, _ruled(V, 1, slots, odd, r, 0.0, 0.0), x)
+        for t, v in odd.items():
+            assert torch.all(out[:, t].double() == v), (r, t)
+
+
 def test_process_logits_bad_data_is_flagged():
     x, out, s, dt = logits_inputs("bf16", 2, 3, 500, 20, 4, 2, 0, 0)
     eng = g.Graft(g.graft_default_config(500, 2, g.GRAFT_MODE_STATIC, g.GRAFT_BF16))
