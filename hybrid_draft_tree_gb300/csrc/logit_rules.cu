@@ -85,11 +85,11 @@ struct Shared {
   uint32_t path_word[MAX_S]; // gathered entries of the tokens that some paths hold
   uint2 spread[16];
   int32_t n_rows, n_paths;
-  float rep, inv_rep, freq, pres;
+  float rep, freq, pres;
 };
 
-// What a gathered entry takes off a logit, for a token with n occurrences.  The quotient by the repetition penalty is a
-// product with its fp32 reciprocal and the differences are taken at once: a few fp32 roundings, far below the type's.
+// What a gathered entry takes off a logit, for a token with n occurrences.  The differences are taken at once: four fp32
+// roundings of their sizes' order, as many as one after the other would take.
 __device__ __forceinline__ float taken(const Shared& sh, const float* bias, uint32_t word, int n) {
   float x = sh.freq * (float)n;
   if (n > 0) x += sh.pres;
@@ -108,7 +108,7 @@ __device__ __forceinline__ float apply(const Shared& sh, const float* bias, uint
     seen = n > 0 || (word & PROMPT);
     off = taken(sh, bias, word, n);
   }
-  if (seen) x *= x > 0.f ? sh.inv_rep : sh.rep;
+  if (seen) x = x > 0.f ? x / sh.rep : x * sh.rep;
   return x - off;
 }
 
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) k_logit_rules(LogitArgs
       r = a.r.d_penalty[3 * b]; f = a.r.d_penalty[3 * b + 1]; p = a.r.d_penalty[3 * b + 2];
       if (!(r > 0.f) || !isfinite(r) || !isfinite(f) || !isfinite(p)) { bad |= GRAFT_ERR_RULE; r = 1.f; f = p = 0.f; }
     }
-    sh.rep = r; sh.inv_rep = 1.f / r; sh.freq = f; sh.pres = p;
+    sh.rep = r; sh.freq = f; sh.pres = p;
     sh.n_paths = 0;
   }
   if (t < 16) sh.spread[t] = make_uint2((t & 1 ? 0xFFFFu : 0u) | (t & 2 ? 0xFFFF0000u : 0u), (t & 4 ? 0xFFFFu : 0u) | (t & 8 ? 0xFFFF0000u : 0u));

@@ -799,6 +799,25 @@ def test_process_logits_keeps_every_bit_of_fp32():
             assert torch.all(out[:, t].double() == v), (r, t)
 
 
+@pytest.mark.parametrize("r", [1.3, 1.1, 0.7, 3.0, 1e-39, 3e38])
+def test_process_logits_quotient_is_rounded_once(r):
+    """x / r and x r in fp32, each the nearest number to the exact one, where no other rule is on; also for an r whose
+    reciprocal fp32 cannot hold."""
+    V, slots = 50021, 4
+    rng = np.random.default_rng(7)
+    x = (rng.standard_normal((slots, V)) * 10.0).astype(np.float32)
+    x[:, ::5] = 0.0
+    x[:, 1::5] *= np.float32(1e-30)
+    hist = rng.permutation(V).astype(np.int32)[None, :30000]
+    s = dict(tok=None, mask=None, hist=hist, hist_len=np.array([30000], np.int32), prompt_len=np.array([9000], np.int32),
+             penalty=np.array([[r, 0.0, 0.0]], np.float32), bias_tok=None, bias_val=None, grammar=None, gram_row=None)
+    out = _run_logits("f32", V, 1, slots, s, cuda(x)).cpu().numpy()
+    q = np.float32(r)
+    with np.errstate(over="ignore"):
+        want = np.where(np.isin(np.arange(V), hist[0]), np.where(x > 0, x / q, x * q), x)
+    assert want.dtype == np.float32 and np.array_equal(out, want)
+
+
 def test_process_logits_bad_data_is_flagged():
     x, out, s, dt = logits_inputs("bf16", 2, 3, 500, 20, 4, 2, 0, 0)
     eng = g.Graft(g.graft_default_config(500, 2, g.GRAFT_MODE_STATIC, g.GRAFT_BF16))
