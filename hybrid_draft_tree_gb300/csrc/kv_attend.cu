@@ -162,7 +162,7 @@ struct Bars {
   unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
   float2 ml[2][128];             // a shared tile's maxima and sums
   Line line;
-  int loads, queries;            // loads that were asked for, the last piece whose queries were
+  int loads[2], queries;         // loads that each copying warp asked for, the last piece whose queries were
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -242,7 +242,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // ---- warp 8, and 10 with small pages: keys and values into the ring ----------------------------------------------
-// L of them: a copy takes its warp some 75 cycles to issue.
+// L of them: a copy takes its warp some 75 cycles to issue.  Each says its own bytes of a tile to the tile's barrier, so a
+// phase ends when both have spoken and all has landed, and neither can pass the other by a phase.
 template <int D, int L>
 __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
                           const CUtensorMap* vmap) {
@@ -305,7 +306,7 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
         ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
-        if (lane == 0 && own == 0) mbar_expect_tx(&sh.full[stage], S::kTile);  // all copies; the other's may land first
+        if (lane == 0) mbar_expect_tx(&sh.full[stage], S::kTile / L);  // this warp's copies
         __syncwarp();
         if (here >= 0)
           tc::tma_4d(ring + stage * S::kTile + (lane % S::kHalves) * (128 * 128) + place * page_bytes,
@@ -318,17 +319,21 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
     last_two = two;
   }
   if (bad) atomicOr(a.err, bad);
-  if (lane == 0 && own == 0) {
-    sh.loads = loads;
-    sh.queries = q_last;
+  if (lane == 0) {
+    sh.loads[own] = loads;
+    if (own == 0) sh.queries = q_last;
   }
 }
 
-// After a wait that ran out, whoever's: the copies in flight land before the CTA ends.
-template <int D>
+// After a wait that ran out, whoever's: the copies in flight land before the CTA ends.  Two copying warps give up apart, so
+// one may have asked for loads that the other has not: the barriers of those get the missing word here.  They are fewer than
+// the ring's stages, since a stage is asked for again only after its last phase, which takes both.
+template <int D, int L>
 __device__ void drain_copies(Bars& sh) {
   constexpr int kStages = Smem<D>::kStages;
-  for (int x = max(0, sh.loads - kStages); x < sh.loads; ++x) mbar_wait_drain(&sh.full[x % kStages], (x / kStages) & 1);
+  const int loads = L == 2 ? max(sh.loads[0], sh.loads[1]) : sh.loads[0];
+  for (int x = L == 2 ? min(sh.loads[0], sh.loads[1]) : loads; x < loads; ++x) mbar_arrive(&sh.full[x % kStages]);
+  for (int x = max(0, loads - kStages); x < loads; ++x) mbar_wait_drain(&sh.full[x % kStages], (x / kStages) & 1);
   for (int x = max(0, sh.queries - 1); x <= sh.queries; ++x) mbar_wait_drain(&sh.q_full[x & 1], (x >> 1) & 1);
 }
 
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependents_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], L);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.dirty[i], 1);
       mbar_init(&sh.clean[i], 3 - L);
@@ -894,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (threadIdx.x == 0 && sh.abort) drain_copies<D>(sh);
+  if (threadIdx.x == 0 && sh.abort) drain_copies<D, L>(sh);
   if (warp == kMmaWarp) tc::tmem_free(sh.tmem, 512);
 }
 

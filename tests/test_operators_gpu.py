@@ -4,6 +4,7 @@ Tolerances follow from the number formats: u = 2^-8 (bf16) or 2^-11 (f16) is the
 to the type, e = 2^-24 that of an fp32 operation; each test adds up the roundings of its formula.
 """
 import math
+import time
 
 import numpy as np
 import pytest
@@ -515,6 +516,37 @@ def test_attend_waits_are_bounded():
         call(outs[1])
         assert kv.sync() == 0
         assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dim,page,ctx", [(128, 16, [600, 1, 300]), (64, 8, [600, 1, 300]), (128, 32, [9000]), (64, 16, [9000])])
+def test_attend_bounded_waits_with_two_copying_warps(dim, page, ctx):
+    """Small pages and one tile an item take two copying warps, which give up apart: the call ends at once all the same (a
+    drain that waits for what was never asked for takes a second), says so, and the handle works on."""
+    rng, gen = np.random.default_rng(6), torch.Generator(device="cuda").manual_seed(6)
+    batch = len(ctx)
+    _, table, pages = tables(rng, batch, max(ctx) + 1, 0, page)
+    k, v = (make_cache(gen, pages, 2, page, dim, torch.bfloat16, "head") for _ in range(2))
+    kv = g.GraftKV(g.graft_kv_default_config(8, 2, dim, page, pages, batch, 1))
+    table, at = cuda(table), cuda(np.array(ctx, np.int32))
+    q = torch.randn((batch, 8 * dim), generator=gen, device="cuda", dtype=torch.bfloat16)
+    want, out = torch.zeros_like(q), torch.zeros_like(q)
+    kv.attend(batch, 1, q, k, v, table, at, max(ctx), want)
+    assert kv.sync() == 0
+    expired = 0
+    for limit in [1, 2, 3] * 20:
+        kv.set_wait_limit(limit)
+        start = time.perf_counter()
+        kv.attend(batch, 1, q, k, v, table, at, max(ctx), out)
+        flags = kv.sync(raise_on_error=False)
+        assert time.perf_counter() - start < 0.5
+        assert flags in (0, gb.GRAFT_ERR_TIMEOUT)
+        assert flags or torch.equal(out, want)
+        expired += flags != 0
+    assert expired
+    kv.set_wait_limit(0)
+    out.zero_()
+    kv.attend(batch, 1, q, k, v, table, at, max(ctx), out)
+    assert kv.sync() == 0 and torch.equal(out, want)
 
 
 def test_offsets_beyond_32_bits():
