@@ -691,6 +691,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
           tc::st16(p_at + c / 2, p);
         }
         if (!known || !__any_sync(~0u, live && top > m + kGrow)) break;
+        tc::wait_st();  // two stores to one place keep no order of their own
         known = false;
       }
       l2 = add2(sum0, sum1);

@@ -336,6 +336,20 @@ def test_attend_rising_scores():
     run_attend("bf16", 2, 4, 0, [1500, 900], 4, 2, 128, 64, "head", tweak=tweak)
 
 
+@pytest.mark.parametrize("dtype,dim,slots,step", [("f16", 64, 4, 40), ("bf16", 64, 61, 130), ("f16", 128, 61, 130), ("bf16", 128, 1, 300)])
+def test_attend_scores_that_run_away_again_and_again(dtype, dim, slots, step):
+    """Scores that rise by about 2^20 every `step` keys: weights are computed, found too large and written again with the
+    new base, in block after block; the result is the definition's, and the same each time."""
+    def tweak(rng, q, k, v, pre, table, ctx, mask, page):
+        q.zero_()
+        q.view(slots, -1, dim)[..., :2] = 2.0
+        for at in range(int(ctx[0])):
+            k[table[0, at // page], at % page, :, 0] = 7.0 * (at // step)
+    first = run_attend(dtype, 1, slots, 0, [1500], 4, 2, dim, 16, "head", scale=1.0, tweak=tweak)[0]
+    for _ in range(3):
+        assert torch.equal(first, run_attend(dtype, 1, slots, 0, [1500], 4, 2, dim, 16, "head", scale=1.0, tweak=tweak)[0])
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_attend_large_values_behind_a_late_maximum(dim):
     """Values of 1e25 whose keys outscore the first ones by 2^46: no intermediate sum leaves fp32."""
