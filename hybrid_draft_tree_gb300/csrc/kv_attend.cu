@@ -58,7 +58,8 @@ constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kSpareWarp = 10, kCleanWarp = 11;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
-// log2 of how far a maximum may run ahead of the base: weights stay inside f16, and sums of large values inside fp32
+// log2 of how far a maximum may run ahead of the base: weights stay inside f16.  A sum of n values of at most |v| reaches
+// 2^12 n |v|, so it stays inside fp32 while n |v| < 2^115 (f16's values always do).
 constexpr float kGrow = 12.f;
 
 // Shared memory: two query tiles, the ring, where results pass on their way out, and the barriers.  A tile is stored in

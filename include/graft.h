@@ -530,7 +530,8 @@ int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
  *   d_lse         float [batch * slots][q_heads], or NULL
  * The cache buffers must start on 16-byte boundaries.  Products are exact in
  * fp32 and summed there, as are the softmax statistics; a key's weight is
- * rounded to the cache's type for its product with the value.  A ctx_len
+ * rounded to the cache's type for its product with the value.  Sums stay finite
+ * while the number of keys times the largest |v_j| is below 2^115.  A ctx_len
  * outside [0, max_ctx] is clamped to it, and a page outside the cache reads as
  * zeros; both set GRAFT_ERR_RANGE.  Asynchronous; one or two kernels. */
 int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride,

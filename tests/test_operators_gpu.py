@@ -364,6 +364,22 @@ def test_attend_large_values_behind_a_late_maximum(dim):
     run_attend("bf16", 1, 3, 0, [700], 4, 2, dim, 64, "head", scale=1.0, tweak=tweak)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_values_at_the_stated_bound(dim):
+    """704 keys of values up to 2^115 / 704, most of them 2^11.9 ahead of the first ones, which is as far as a base stays:
+    the sums are finite."""
+    def tweak(rng, q, k, v, pre, table, ctx, mask, page):
+        q.zero_()
+        q.view(len(ctx), -1, 4, dim)[..., 0] = 1.0
+        k.zero_()
+        k[..., 0] = 8.25
+        for at in range(200):
+            k[table[0, at // page], at % page] = 0.0
+        v.clamp_(0.5, 1.0)
+        v *= 2.0 ** 115 / 704
+    run_attend("bf16", 1, 4, 0, [700], 4, 2, dim, 64, "head", scale=1.0, tweak=tweak)
+
+
 def test_attend_ctx_bound_above_every_length():
     """max_ctx is a bound: lengths far below it, zero among them, leave whole splits of the key axis empty."""
     run_attend("bf16", 3, 3, 0, [0, 5, 300], 8, 2, 128, 16, "head", max_ctx=9000)
