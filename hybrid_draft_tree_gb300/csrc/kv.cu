@@ -27,6 +27,8 @@ namespace {
 
 using graft::misaligned;
 
+constexpr int32_t kMaxKeys = 0x7FFFFFFF - 256;  // of a row: key counts rounded up to blocks stay below 2^31
+
 int fail(graft_kv* h, int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -248,6 +250,8 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
   if (prefix_len < 0 || max_ctx < 0 || table_stride < 0 ||
       (int64_t)max_ctx + slots > (int64_t)table_stride * c.page_size)
     return fail(h, GRAFT_EINVAL, "prefix_len and max_ctx must be >= 0, max_ctx + slots <= table_stride * page_size");
+  if ((int64_t)prefix_len + max_ctx + slots > kMaxKeys)
+    return fail(h, GRAFT_EINVAL, "prefix_len + max_ctx + slots is more than %d", kMaxKeys);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(h, GRAFT_EINVAL, "scale must be finite and > 0");
   if (batch == 0) return GRAFT_OK;
   if (!d_q || !d_out || !d_page_table || !d_ctx_len || (prefix_len > 0 && !d_prefix_pages))

@@ -968,6 +968,25 @@ def test_calls_are_the_same_without_the_extension():
         assert e.value.code == gb.GRAFT_EINVAL
 
 
+def test_attend_refuses_more_keys_than_it_counts():
+    """Prefix, context and tree together stay below 2^31 keys; pages may repeat, so the tables alone would allow more."""
+    kv = g.GraftKV(g.graft_kv_default_config(4, 2, 64, 128, 4, 1, 4))
+    k = torch.zeros((4, 2, 128, 64), device="cuda", dtype=torch.bfloat16)
+    q = torch.zeros((4, 256), device="cuda", dtype=torch.bfloat16)
+    table = torch.zeros((1, 1 << 24), device="cuda", dtype=torch.int32)
+    ctx = torch.zeros(1, device="cuda", dtype=torch.int32)
+    most = 2 ** 31 - 257
+    for prefix, max_ctx in ((0, most - 3), (most - 3, 0), (most - 103, 100), (2 ** 31 - 1, 0), (0, 2 ** 31 - 5),
+                            (2 ** 31 - 1, 2 ** 31 - 5)):
+        with pytest.raises(g.GraftError, match="more than") as e:
+            kv.attend(1, 4, q, k, k, table, ctx, max_ctx, torch.empty_like(q), prefix_pages=table.view(-1), prefix_len=prefix)
+        assert e.value.code == gb.GRAFT_EINVAL
+    out, lse = torch.empty_like(q), torch.empty((4, 4), device="cuda")
+    kv.attend(1, 4, q, k, k, table, ctx, most - 4, out, lse=lse)      # the bound itself: the lengths are short
+    assert kv.sync() == 0
+    assert torch.allclose(lse, torch.arange(1, 5, device="cuda").log()[:, None].expand(4, 4), atol=1e-5)
+
+
 # ------------------------------------------------------------------------------------------------------- refusals
 def test_refusals_of_live_handles():
     """Argument errors come back at once, name themselves and queue nothing."""
