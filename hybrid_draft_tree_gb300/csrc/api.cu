@@ -780,13 +780,18 @@ int graft_process_logits(graft_handle* h, int32_t batch, int32_t slots, const in
       graft::misaligned(r.d_prompt_len, 4) || graft::misaligned(r.d_penalty, 4) || graft::misaligned(r.d_bias_tok, 4) ||
       graft::misaligned(r.d_bias_val, 4) || graft::misaligned(r.d_grammar, 4) || graft::misaligned(r.d_grammar_row, 4))
     return fail(h, GRAFT_EINVAL, "a buffer is not aligned to its element size");
-  // in place is element by element; rows that overlap otherwise would be read after they are written
+  // in place is element by element; rows that meet otherwise would be read after they are written (at one stride they do
+  // not when they are column ranges of one buffer)
   const uintptr_t in0 = reinterpret_cast<uintptr_t>(d_logits), out0 = reinterpret_cast<uintptr_t>(d_out);
   const uintptr_t last = (uintptr_t)((int64_t)batch * slots - 1);
   const uintptr_t in1 = in0 + (last * (uintptr_t)row_stride + c.vocab) * es;
   const uintptr_t out1 = out0 + (last * (uintptr_t)out_stride + c.vocab) * es;
-  if (in0 < out1 && out0 < in1 && !(in0 == out0 && row_stride == out_stride))
-    return fail(h, GRAFT_EINVAL, "d_out overlaps d_logits without being it at the same stride");
+  if (in0 < out1 && out0 < in1) {
+    const int64_t step = row_stride * (int64_t)es, width = c.vocab * (int64_t)es;
+    const int64_t apart = ((int64_t)(out0 - in0) % step + step) % step;  // from a row's start to the next start of d_out's
+    if (row_stride != out_stride || (in0 != out0 && (apart < width || apart > step - width)))
+      return fail(h, GRAFT_EINVAL, "rows of d_out overlap rows of d_logits without being them at the same stride");
+  }
   if (!h->rules_ready) return fail(h, GRAFT_ECUDA, "the logit rules' shared memory is not available on this device");
   graft::LogitArgs a{};
   a.r = r;

@@ -345,7 +345,8 @@ typedef struct {
  * without a tree (it need not be the handle's budget + 1).  d_tree_tok and
  * d_tree_mask [batch][slots] are those graft_assemble writes; both NULL: no
  * slot is a pad and no path counts.  d_out may be d_logits at the same stride
- * (in place); any other overlap is refused.  Rows whose starts lie equally off
+ * (in place), and rows of both may be column ranges of one buffer; rows that
+ * overlap are refused.  Rows whose starts lie equally off
  * a 16-byte boundary in d_logits and d_out move in 16-byte pieces, others by
  * elements.  Asynchronous; one kernel. */
 int graft_process_logits(graft_handle* h, int32_t batch, int32_t slots, const int32_t* d_tree_tok,

@@ -880,6 +880,27 @@ def test_process_logits_quotient_is_rounded_once(r):
     assert want.dtype == np.float32 and np.array_equal(out, want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_process_logits_between_columns_of_one_buffer(dtype):
+    """Input and output rows that are column ranges of one buffer do not meet, whichever comes first; ranges that do are
+    refused."""
+    V, batch, slots, gap = 1003, 2, 5, 13
+    x, out, s, dt = logits_inputs(dtype, batch, slots, V, 60, 9, 3, 0, 0)
+    eng = g.Graft(g.graft_default_config(V, batch, g.GRAFT_MODE_STATIC, g.GRAFT_F32 if dtype == "f32" else g.GRAFT_BF16))
+    for src, dst in ((0, V + gap), (V + gap, 0), (0, V), (V, 0)):
+        wide = torch.full((batch * slots, 2 * V + gap), 9.0, device="cuda", dtype=dt)
+        wide[:, src:src + V] = x
+        call_logits(eng, batch, slots, wide[:, src:src + V], wide[:, dst:dst + V], s)
+        assert eng.sync() == 0
+        check_logits(wide[:, dst:dst + V], x.double().cpu().numpy(), s, dt, V, slots)
+        assert torch.equal(wide[:, src:src + V], x)
+    for src, dst in ((0, V - 1), (V - 1, 0), (1, 2), (V + gap, gap + 1)):
+        with pytest.raises(g.GraftError) as e:
+            call_logits(eng, batch, slots, wide[:, src:src + V], wide[:, dst:dst + V], s)
+        assert e.value.code == gb.GRAFT_EINVAL
+    assert eng.sync() == 0
+
+
 def test_process_logits_bad_data_is_flagged():
     x, out, s, dt = logits_inputs("bf16", 2, 3, 500, 20, 4, 2, 0, 0)
     eng = g.Graft(g.graft_default_config(500, 2, g.GRAFT_MODE_STATIC, g.GRAFT_BF16))
