@@ -1,4 +1,5 @@
 // C ABI of the paged-cache calls (graft_kv_*): handle, argument checks and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -67,10 +68,16 @@ int check_cfg(const graft_kv_config* c, graft_kv* h) {
   const int64_t top = (int64_t)1 << 38;  // bytes of a stride stay below 2^40
   if (T < D || H < D || P < D || T % 8 != 0 || H % 8 != 0 || P % 8 != 0 || T >= top || H >= top || P >= top)
     return fail(h, GRAFT_EINVAL, "strides must be multiples of 8 elements, at least head_dim and below 2^38");
-  const int64_t tokens = (ps - 1) * T + D, heads = (int64_t)(c->kv_heads - 1) * H + D;
-  if (!(c->kv_heads == 1 || H >= tokens || T >= heads)) return fail(h, GRAFT_EINVAL, "a page's heads and tokens overlap");
-  if (c->num_pages > 1 && P < (ps - 1) * T + (int64_t)(c->kv_heads - 1) * H + D)
-    return fail(h, GRAFT_EINVAL, "page_stride is less than a page");
+  // tokens, heads and pages nest in the order of their strides, whichever that is: each steps over all that lies within
+  struct Axis { int64_t stride, count; };
+  Axis axes[3] = {{T, ps}, {H, c->kv_heads}, {P, c->num_pages}};
+  std::sort(axes, axes + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  int64_t extent = D;
+  for (const Axis& x : axes) {
+    if (x.count == 1) continue;
+    if (x.stride < extent) return fail(h, GRAFT_EINVAL, "the strides make tokens, heads or pages overlap");
+    extent = x.count - 1 > top / x.stride ? top : extent + (x.count - 1) * x.stride;  // top: no further stride reaches it
+  }
   return GRAFT_OK;
 }
 

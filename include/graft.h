@@ -472,7 +472,7 @@ typedef struct {
   int32_t max_batch;       /* largest batch passed to graft_kv_attend */
   int32_t max_slots;       /* largest slots passed to graft_kv_attend, in [1, 64] */
   int32_t dtype;           /* of queries, keys, values and outputs: GRAFT_BF16 or GRAFT_F16 */
-  int64_t page_stride;     /* elements; multiples of 8, no two tokens overlapping */
+  int64_t page_stride;     /* elements; multiples of 8; nested in any order, no two tokens overlapping */
   int64_t head_stride;
   int64_t token_stride;
 } graft_kv_config;

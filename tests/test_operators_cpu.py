@@ -107,6 +107,28 @@ def test_config_is_checked_before_any_device_call():
     assert L.graft_kv_last_launch_count(None) == 0 and L.graft_kv_last_error(None) == b"null handle"
 
 
+def test_strides_nest_in_any_order():
+    """Tokens, heads and pages may lie in any order (heads outermost, as one buffer per head, among them); what overlaps is
+    refused in each."""
+    if torch.cuda.is_available():
+        pytest.skip("has a GPU")
+    L = g.load()
+
+    def init(token, head, page, kv=2, ps=16, pages=10, dim=64):
+        cfg = g.graft_kv_default_config(4, kv, dim, ps, pages, 2, 4, token_stride=token, head_stride=head, page_stride=page)
+        return L.graft_kv_init(ctypes.byref(cfg), ctypes.byref(ctypes.c_void_p()))
+
+    for token, head, page in ((64, 1024, 2048), (128, 64, 2048), (64, 10240, 1024), (640, 10240, 64), (1280, 64, 128),
+                              (1280, 640, 64), (64, 10248, 1024), (72, 11520, 1152)):
+        assert init(token, head, page) == gb.GRAFT_ECUDA, (token, head, page)
+    for token, head, page in ((64, 10232, 1024), (64, 10240, 1016), (632, 10240, 64), (640, 10232, 64), (64, 64, 2048),
+                              (1272, 64, 128), (1280, 632, 64), (1280, 64, 120), (64, 1024, 1024)):
+        assert init(token, head, page) == gb.GRAFT_EINVAL, (token, head, page)
+    assert init(64, 64, 1024, kv=1) == gb.GRAFT_ECUDA and init(64, 1024, 64, pages=1) == gb.GRAFT_ECUDA
+    far = 1 << 37                                      # an extent beyond 64 bits
+    assert init(far + 8, 64, far, ps=8, pages=(1 << 28) - 1, kv=1) == gb.GRAFT_EINVAL
+
+
 def test_structs_match_the_c_header(tmp_path):
     if shutil.which("gcc") is None:
         pytest.skip("no C compiler")

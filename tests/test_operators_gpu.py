@@ -579,6 +579,41 @@ def test_attend_bounded_waits_with_two_copying_warps(dim, page, ctx):
     assert kv.sync() == 0 and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("order", [(1, 0, 2), (2, 0, 1), (2, 1, 0), (1, 2, 0)])
+def test_strides_in_any_order(order):
+    """Caches whose pages, heads and tokens nest in another order than pages first: `order` from the outermost in, of page
+    (0), head (1), token (2)."""
+    rng, gen = np.random.default_rng(3), torch.Generator(device="cuda").manual_seed(3)
+    batch, slots, hq, hk, dim, page = 2, 5, 4, 2, 64, 16
+    ctx = np.array([140, 33], np.int32)
+    _, table, pages = tables(rng, batch, int(ctx.max()) + slots, 0, page)
+    sizes = [pages, hk, page]
+    k_all, v_all = (torch.randn([*[sizes[a] for a in order], dim], generator=gen, device="cuda", dtype=torch.bfloat16)
+                    for _ in range(2))
+    back = [order.index(a) for a in range(3)] + [3]
+    k_cache, v_cache = k_all.permute(back), v_all.permute(back)                  # [page, head, token, dim]
+    stride = k_cache.stride()
+    kv = g.GraftKV(g.graft_kv_default_config(hq, hk, dim, page, pages, batch, slots, page_stride=stride[0],
+                                             head_stride=stride[1], token_stride=stride[2]))
+    q, k, v = (torch.randn((batch * slots, h * dim), generator=gen, device="cuda", dtype=torch.bfloat16) for h in (hq, hk, hk))
+    rope = torch.zeros((200, dim), device="cuda")
+    rope[:, :dim // 2] = 1.0
+    want_k, want_v = k_cache.clone(), v_cache.clone()
+    for b in range(batch):
+        for i in range(slots):
+            at = int(ctx[b]) + i
+            want_k[table[b, at // page], :, at % page] = k[b * slots + i].view(hk, dim)
+            want_v[table[b, at // page], :, at % page] = v[b * slots + i].view(hk, dim)
+    out, lse = torch.empty_like(q), torch.empty((batch * slots, hq), device="cuda")
+    kv.append(batch, slots, None, k, v, rope, cuda(table), cuda(ctx), k_all, v_all, None)
+    kv.attend(batch, slots, q, k_all, v_all, cuda(table), cuda(ctx), 140, out, lse=lse)
+    assert kv.sync() == 0
+    assert torch.equal(k_cache, want_k) and torch.equal(v_cache, want_v)
+    mask = np.array([[(1 << (i + 1)) - 1 for i in range(slots)]] * batch, np.uint64)
+    ref = attend_reference(q, want_k, want_v, "head", None, table, 0, ctx, mask, page, hq, hk, dim, dim ** -0.5)
+    check_attend(out, lse, ref, torch.bfloat16, 145)
+
+
 def test_offsets_beyond_32_bits():
     """Pages far apart in a cache of 2^31 elements and more: append writes and attend reads the right ones."""
     hk, dim, page, pages = 2, 128, 16, 5
