@@ -4,7 +4,9 @@
  * whose arguments do not pass returns NotImplemented, and the binding's own
  * checks then say what is wrong.  They also take the call when this extension
  * is not built.  What it saves is host time: on the GPU's host the Python form
- * of the checks takes about as long as the launch. */
+ * of the checks takes about as long as the launch.  The interpreter lock is
+ * free during the call, as it is under ctypes: a call may wait for room in the
+ * launch queue. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -117,9 +119,13 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     GIVE_UP;
   if (rope && (width != rot || !small(positions))) GIVE_UP;
   if (!small(pages)) GIVE_UP;
-  return PyLong_FromLong(((append_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, k, ks, w,
-                                                      ws, pos, src, rope, (int32_t)positions, (int32_t)prefix, pt,
-                                                      (int32_t)pages, ctx, qo, qos, kc, vc, (void*)(uintptr_t)v[2]));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((append_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, k, ks, w, ws, pos,
+                                    src, rope, (int32_t)positions, (int32_t)prefix, pt, (int32_t)pages, ctx, qo, qos,
+                                    kc, vc, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
 }
 
 /* attend(entry, handle, stream, dtype, float32, int32, int64, q_width, q_heads, page_size, span,
@@ -143,9 +149,13 @@ static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       !buffer(a[22], i32, (prefix + page - 1) / page, &pre) || !buffer(a[23], i64, rows, &mask) ||
       !buffer(a[24], f32, rows * heads, &lse) || !small(pages))
     GIVE_UP;
-  return PyLong_FromLong(((attend_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, kc, vc, pre,
-                                                      (int32_t)prefix, pt, (int32_t)pages, ctx, (int32_t)max_ctx, mask,
-                                                      (float)scale, out, os, lse, (void*)(uintptr_t)v[2]));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((attend_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, kc, vc, pre,
+                                    (int32_t)prefix, pt, (int32_t)pages, ctx, (int32_t)max_ctx, mask, (float)scale,
+                                    out, os, lse, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
 }
 
 /* logits(entry, handle, stream, dtype, float32, int32, int64, vocab, batch, slots, logits, out, tree_tok, tree_mask,
@@ -174,8 +184,12 @@ static PyObject* logits(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   r.d_hist = hist; r.hist_stride = hs; r.d_hist_len = hist_len; r.d_prompt_len = prompt; r.d_penalty = pen;
   r.d_bias_tok = btok; r.d_bias_val = bval; r.n_bias = (int32_t)bs;
   r.n_grammar = (int32_t)gr; r.d_grammar = gram; r.grammar_stride = gs; r.d_grammar_row = grow;
-  return PyLong_FromLong(((logits_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, tok, mask, x, xs,
-                                                      &r, out, os, (void*)(uintptr_t)v[2]));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((logits_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, tok, mask, x, xs, &r,
+                                    out, os, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
 }
 
 static PyMethodDef methods[] = {{"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},

@@ -5,12 +5,15 @@ import ctypes
 import os
 import shutil
 import subprocess
+import threading
+import time
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import hybrid_draft_tree_gb300 as g  # noqa: E402
+from hybrid_draft_tree_gb300 import _build  # noqa: E402
 from hybrid_draft_tree_gb300 import graft as gb  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -223,3 +226,64 @@ def test_cache_reach_follows_the_strides(as_device):
     assert gb._cache(one, "k", torch.bfloat16, kv.span) == one.data_ptr()
     with pytest.raises(g.GraftError, match="elements"):
         gb._cache(layers[:7, 1], "k", torch.bfloat16, kv.span)
+
+
+class DeviceRows:
+    """What the extension reads of a tensor, on a machine without a GPU."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype, self.is_cuda = tuple(shape), dtype, True
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+    def stride(self):
+        return tuple(DeviceRows(self.shape[i + 1:], self.dtype).numel() for i in range(len(self.shape)))
+
+
+def test_the_extension_frees_the_interpreter_lock_during_a_call():
+    """Other threads run while a call waits (for room in the launch queue, say).  usleep stands in for the library's entry
+    points: the handle, its first argument, is how long it takes."""
+    if _build.build_fastcall() is None:
+        pytest.skip("no C compiler or Python headers")
+    ext = gb._load_fastcall()
+    at = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    q, kv, cache = DeviceRows((8, 256), bf), DeviceRows((8, 128), bf), DeviceRows((8, 2, 16, 64), bf)
+    table, ctx, rope = DeviceRows((2, 2), i32), DeviceRows((2,), i32), DeviceRows((32, 64), f32)
+    x = DeviceRows((8, 100), bf)
+    delay = 400000
+    span = 8 * 2 * 16 * 64
+    calls_ = {
+        "append": (at, delay, 0, bf, f32, i32, 256, 128, 64, span, 2, 4, 0, q, kv, kv, rope, table, ctx, cache, cache, q, None, None),
+        "attend": (at, delay, 0, bf, f32, i32, i64, 256, 4, 16, span, 2, 4, 0, 20, 0.125, q, cache, cache, table, ctx, q, None,
+                   None, None),
+        "logits": (at, delay, 0, bf, f32, i32, i64, 100, 2, 4, x, x, *[None] * 10),
+    }
+    for name, args in calls_.items():
+        ticks, stop = [], threading.Event()
+
+        def tick():
+            while not stop.is_set():
+                ticks.append(time.perf_counter())
+                time.sleep(0.001)
+        other = threading.Thread(target=tick)
+        other.start()
+        while not ticks:
+            time.sleep(0.001)
+        start = time.perf_counter()
+        assert getattr(ext, name)(*args) == 0
+        end = time.perf_counter()
+        stop.set()
+        other.join()
+        assert end - start >= 0.3, name
+        assert sum(start + 0.05 < t < end - 0.05 for t in ticks) >= 5, name
