@@ -13,7 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgraft.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")   # the binding's per-layer calls, a CPython extension
+# the binding's per-layer calls, a CPython extension: its name holds the interpreter's ABI, so that one over the same tree
+# with another ABI builds its own and loads no other's
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ("api.cu", "assemble.cu", "scan.cu", "umax.cu", "select.cu", "coverage.cu", "sample.cu", "scan_tma.cu", "noalloc.cu",
            "cluster_select.cu", "logit_rules.cu", "kv.cu", "kv_append.cu", "kv_attend.cu")

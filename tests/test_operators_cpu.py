@@ -5,6 +5,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 import time
 
@@ -287,3 +288,10 @@ def test_the_extension_frees_the_interpreter_lock_during_a_call():
         other.join()
         assert end - start >= 0.3, name
         assert sum(start + 0.05 < t < end - 0.05 for t in ticks) >= 5, name
+
+
+def test_the_extension_is_named_for_its_interpreter():
+    """An interpreter of another ABI looks for another file: it neither loads nor reuses this one's."""
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert sysconfig.get_config_var("SOABI") in suffix
+    assert os.path.basename(_build.FASTCALL) == "_fastcall" + suffix
