@@ -66,19 +66,6 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void ld2(uint32_t addr, float& x, float& y) {
-  uint32_t r[2];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
-  wait_ld<2>(r);
-  x = __uint_as_float(r[0]);
-  y = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ void st2(uint32_t addr, float x, float y) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(__float_as_uint(x)),
-               "r"(__float_as_uint(y)) : "memory");
-  wait_st();
-}
-
 // --- matrix products ----------------------------------------------------------------------------------------------
 // Shared-memory operand in 128-byte rows with the 128-byte swizzle; groups of 8 rows follow each other (1024 bytes).
 // `lead`: bytes between groups of 64 elements of an operand whose row index is the contraction's (transposed operand).
