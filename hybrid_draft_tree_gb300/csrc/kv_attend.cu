@@ -31,8 +31,9 @@
 // log-sum-exp, fp32) is joined by a second kernel, in the order of the keys.
 //
 // Measured (bf16, 32/8 heads of 128 unless said otherwise), and what bounds it:
-//   16 x 61 slots behind 12001 + 2048 keys   166 us, 1290 TFLOP/s: a block of 256
-//       rows takes 1.5 us, its operands' way through shared memory (256 KB);
+//   16 x 61 slots behind 12001 + 2048 keys   166 us, 1290 TFLOP/s (176 us in seconds
+//       of it, at the power limit): a block of 256 rows takes 1.5 us, its operands'
+//       way through shared memory (256 KB);
 //   64 x 1 behind 8192 + 1024                 60 us, 3.9 TB/s: memory, then the
 //       start (4.5 us to the first scores) and the join (5 us);
 //   1 x 61 behind 32768, pages of 16          43 us, 3.1 TB/s: the copies' issue
@@ -63,7 +64,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 12.f;
 
 // Shared memory: two query tiles, the ring, where results pass on their way out, and the barriers.  A tile is stored in
-// column halves of 64 elements (128 bytes).  With D = 128 results pass through the query tile they belong to.
+// column halves of 64 elements (128 bytes).  With D = 128 results pass through a query tile, 4 KB a warp: a shared tile's
+// through its own, those of two tiles both through the first.  No product reads the queries there any more: a group comes
+// here after its last commit, which covers every product before it, and those of the second tile are issued after the
+// first's.
 template <int D>
 struct Smem {
   static constexpr int kHalves = D / 64;
@@ -672,6 +676,9 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
+        // The sums take the weights in fp32, the product with the values takes them rounded to the cache's type: the tensor
+        // cores multiply 16-bit operands, and the lower halves would take a second product of the size of the first.  The
+        // result's distance from the definition is then about 1.4 times that of fp32 weights, whose result is rounded too.
         const float2 sc = make_float2(scale, scale), mb = make_float2(-base, -base);
         const uint32_t p_at = tmem + (D == 128 ? t * 128 : 384 + t * 64);
         sum0 = l2;
