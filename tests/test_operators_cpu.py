@@ -295,3 +295,18 @@ def test_the_extension_is_named_for_its_interpreter():
     suffix = sysconfig.get_config_var("EXT_SUFFIX")
     assert sysconfig.get_config_var("SOABI") in suffix
     assert os.path.basename(_build.FASTCALL) == "_fastcall" + suffix
+
+
+def test_accepted_rows_where_siblings_repeat_a_token():
+    """The path is the verified one: the deepest, of equals the one that ends in the lowest slot, also when a lower slot
+    with the same token has no child on it."""
+    from workloads.target_model import accepted_rows
+    tok = torch.tensor([[9, 4, 4, 5, 6, 6, -1], [9, 4, 5, 4, 5, 7, -1], [9, 1, 2, 3, -1, -1, -1], [9, 4, 4, 4, 5, 5, 8]],
+                       dtype=torch.int32)
+    parent = torch.tensor([[-1, 0, 0, 2, 3, 3, -1], [-1, 0, 1, 0, 3, 4, -1], [-1, 0, 0, 1, -1, -1, -1], [-1, 0, 0, 0, 3, 2, 1]],
+                          dtype=torch.int8)
+    emitted = torch.tensor([[4, 5, 6, 2, -1, -1, -1], [4, 5, 7, 1, -1, -1, -1], [5, -1, -1, -1, -1, -1, -1],
+                            [4, 5, 0, -1, -1, -1, -1]], dtype=torch.int32)
+    rows = accepted_rows(tok, parent, torch.tensor([3, 3, 0, 2], dtype=torch.int32), emitted)
+    assert rows.tolist() == [[0, 2, 3, 4, -1, -1, -1], [0, 3, 4, 5, -1, -1, -1], [0, -1, -1, -1, -1, -1, -1],
+                             [0, 3, 4, -1, -1, -1, -1]]

@@ -45,16 +45,21 @@ class ToyTarget:
 
 def accepted_rows(tok, parent, accept_len, out_tokens):
     """The slots of each request's accepted path, the root first, then -1: int32 [batch, S].  The path is the one whose
-    tokens were emitted (the lowest slot where siblings repeat a token)."""
+    tokens were emitted; where siblings repeat a token several are, and it is the one that ends in the lowest slot."""
     batch, S = tok.shape
     rows = torch.full((batch, S), -1, dtype=torch.int32, device=tok.device)
     rows[:, 0] = 0
-    cur = torch.zeros(batch, dtype=torch.int64, device=tok.device)
-    slot = torch.arange(S, device=tok.device)
-    for d in range(int(accept_len.max())):
-        fits = (parent.long() == cur[:, None]) & (tok == out_tokens[:, d:d + 1]) & (slot > 0)
-        cur = torch.where(d < accept_len, torch.where(fits, slot, S).amin(1), cur)
-        rows[:, d + 1] = torch.where(d < accept_len, cur.int(), -1)
+    slot, above = torch.arange(S, device=tok.device), parent.long().clamp(min=0)
+    most = int(accept_len.max())
+    level = (slot == 0).expand(batch, S)              # the slots that paths of the emitted tokens have reached
+    for d in range(most):
+        below = level.gather(1, above) & (tok == out_tokens[:, d:d + 1]) & (slot > 0)
+        level = torch.where((d < accept_len)[:, None], below, level)
+    end = torch.where(level, slot, S).amin(1)
+    for d in range(most, 0, -1):
+        on = d <= accept_len
+        rows[:, d] = torch.where(on, end, -1)
+        end = torch.where(on, above.gather(1, end.clamp(max=S - 1)[:, None])[:, 0], end)
     return rows
 
 
