@@ -468,6 +468,60 @@ def test_attend_non_finite_slots_reach_only_those_that_see_them(value):
                 assert not torch.isfinite(out[b, i, :4]).any()
 
 
+CLEANED = [
+    # dtype, batch, slots, prefix, ctx, hq, hk, dim, page, layout
+    ("f16", 2, 9, 37, [130, 61], 8, 2, 64, 8, "token"),
+    ("f16", 2, 61, 300, [64, 70], 8, 2, 128, 128, "head"),
+    ("bf16", 3, 1, 200, [20, 0, 100], 8, 2, 64, 128, "head"),
+    ("f16", 1, 61, 0, [3001], 8, 2, 64, 16, "head"),                # cut and joined, two copying warps
+    ("bf16", 1, 61, 0, [3001], 32, 2, 128, 8, "token"),             # of two tiles
+    ("f16", 20, 3, 700, list(range(0, 600, 30)), 8, 2, 128, 32, "head"),   # packed
+    ("bf16", 30, 61, 0, [(53 * b) % 900 for b in range(30)], 32, 8, 64, 8, "head"),   # more items than SMs
+]
+
+
+@pytest.mark.parametrize("value", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("case", CLEANED, ids=lambda c: f"{c[0]}-b{c[1]}-s{c[2]}-p{c[3]}-d{c[7]}-g{c[8]}{c[9]}")
+def test_attend_cleans_values_in_every_form(case, value):
+    """Each type, head and page size, item whole, cut, packed: what nobody sees is not finite, and so are a few elements of
+    some slots' values, which reach the rows that see them and no others."""
+    batch, slots, prefix, ctx = case[1:5]
+    spoiled = []
+
+    def tweak(rng, q, k, v, pre, table, ctx, mask, page):
+        keep = torch.zeros(k.shape[:2], dtype=torch.bool)
+        for p in range(prefix):
+            keep[pre[p // page], p % page] = True
+        for b in range(batch):
+            for at in range(int(ctx[b]) + slots):
+                seen = at < ctx[b] or any(int(m) >> (at - int(ctx[b])) & 1 for m in mask[b])
+                keep[table[b, at // page], at % page] = bool(seen)
+        keep = keep.cuda()
+        k[~keep] = value
+        v[~keep] = value
+        for b in range(0, batch, 2):
+            for j in {slots // 3, slots - 1}:
+                if mask[b, j]:
+                    at = int(ctx[b]) + j
+                    v[table[b, at // page], at % page, 0, 5] = value
+                    v[table[b, at // page], at % page, -1, -1] = value
+                    spoiled.append((b, j))
+    out, _, _ = run_attend(*case, tweak=tweak)
+    assert spoiled and not torch.isfinite(out).all()
+
+
+def test_attend_finite_slots_are_untouched_by_cleaning():
+    """The largest numbers of each type, subnormal ones and both zeros in slots' values are no infinities."""
+    for dtype, dim in (("f16", 64), ("f16", 128), ("bf16", 64)):
+        top = torch.finfo(DT[dtype]).max if dtype == "f16" else 1e30
+
+        def tweak(rng, q, k, v, pre, table, ctx, mask, page):
+            for j, x in enumerate((top, -top, torch.finfo(DT[dtype]).tiny / 4, -0.0)):
+                at = int(ctx[0]) + j
+                v[table[0, at // page], at % page, :, j::7] = x
+        run_attend(dtype, 1, 9, 0, [125], 4, 2, dim, 16, "head", tweak=tweak)
+
+
 def test_attend_bad_data_is_flagged_and_stays_in_bounds():
     rng, gen = np.random.default_rng(1), torch.Generator(device="cuda").manual_seed(1)
     k, v = (make_cache(gen, 8, 2, 16, 64, torch.bfloat16, "head") for _ in range(2))
