@@ -11,15 +11,15 @@
 // passes through shared memory, where they are done a lane each (in the pieces
 // they would cost the whole warp a pass for each of a lane's).  A row is read and
 // written once; in place, units without a rule or a grammar are not touched.
-// Bound by memory where a CTA has many rows (16 x 61 x 151936 bf16: 106 us, 5.5
-// TB/s, 82% of the copy rate), by the table's building where it has few (64 x 17
-// x 128256 behind 8192 tokens: 114 us, 4.7 TB/s), by latency for one row of 32000
-// (5.2 us).
+// Bound by memory where a CTA has many rows (16 x 61 x 151936 bf16: 110 us, 5.3
+// TB/s, 79% of the copy rate), by the table's building where it has few (64 x 17
+// x 128256 behind 8192 tokens: 115 us, 4.7 TB/s), by latency for one row of 32000
+// (5.3 us).
 //
 // Rows need not start on 16-byte boundaries: the pieces are those of the row's
 // own alignment, so the bits are read at the row's offset, and the few elements
 // before its first and after its last piece go one by one (so do rows whose input
-// and output are aligned differently: 515 us instead of 106).
+// and output are aligned differently: 461 us instead of 110).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -348,7 +348,6 @@ static cudaError_t prepare() {
 
 cudaError_t prepare_logit_rules() {
   cudaError_t e = prepare<__nv_bfloat16, FewRows>();
-  if (e == cudaSuccess) e = prepare<__nv_bfloat16, ManyRows>();
   if (e == cudaSuccess) e = prepare<float, FewRows>();
   if (e == cudaSuccess) e = prepare<float, ManyRows>();
   return e;
@@ -359,8 +358,7 @@ static int64_t ctas_of(const LogitArgs& a, int chunk) { return (int64_t)a.batch 
 template <typename T, typename S>
 static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
   // Every CTA reads the request's whole history: while that is more than an eighth of what its rows move, a chunk grows
-  // as long as two CTAs an SM remain and three fit (64 x 17 behind 8192: 122 us with 3072 elements, 114 with 6144, 161
-  // with 12288).  When the chunks alone are too few for the SMs, rows are split too, four at least, into one wave of CTAs
+  // as long as two CTAs an SM remain and three fit (64 x 17 behind 8192: 123 us with 3072 elements, 115 with 6144).  When the chunks alone are too few for the SMs, rows are split too, four at least, into one wave of CTAs
   // (1 x 61 behind 32768: 22 us; into 4 CTAs an SM 33, into one 26).
   const int pass = S::kThreads * Elem<T>::N;
   a.chunk = pass;
@@ -373,17 +371,15 @@ static cudaError_t launch(LogitArgs a, int num_sms, cudaStream_t s) {
   return launch_dependent(k_logit_rules<T, S>, grid, dim3(S::kThreads), S::smem(a.chunk), s, a);
 }
 
-// With many rows a CTA the pieces in flight count (16 x 61 x 151936: 106 us with eight a lane, 109 with four), with few
-// how many CTAs build their tables at once (64 x 17 x 128256: 114 us with three an SM, 129 with two; one row of 32000:
-// 5.2 and 6.0).
-template <typename T>
-static cudaError_t launch(const LogitArgs& a, int num_sms, cudaStream_t s) {
-  const bool many = a.slots >= 32 && ctas_of(a, ManyRows::kThreads * Elem<T>::N) >= 2 * num_sms;
-  return many ? launch<T, ManyRows>(a, num_sms, s) : launch<T, FewRows>(a, num_sms, s);
-}
-
+// How many CTAs build their tables at once counts most (bf16, 64 x 17 x 128256: 115 us with three an SM, 140 with two; one
+// fp32 row of 32000: 5.3 and 6.0), for bf16 at every number of rows (16 x 61 x 151936: 110 and 111).  With many fp32 rows
+// a CTA it is the pieces in flight: 16 x 32 x 151936 take 106 us with eight a lane and two CTAs, 109 with four and three;
+// 16 x 28 96 either way, 16 x 17 65.4 and 64.9; where the chunks are less than two CTAs an SM, four (1 x 61 behind 32768:
+// 27 us, 35 with eight).
 cudaError_t launch_logit_rules(const LogitArgs& a, int dtype, int num_sms, cudaStream_t s) {
-  return dtype == GRAFT_BF16 ? launch<__nv_bfloat16>(a, num_sms, s) : launch<float>(a, num_sms, s);
+  if (dtype == GRAFT_BF16) return launch<__nv_bfloat16, FewRows>(a, num_sms, s);
+  const bool many = a.slots >= 32 && ctas_of(a, ManyRows::kThreads * Elem<float>::N) >= 2 * num_sms;
+  return many ? launch<float, ManyRows>(a, num_sms, s) : launch<float, FewRows>(a, num_sms, s);
 }
 
 }  // namespace graft
