@@ -1054,7 +1054,8 @@ cudaError_t launch(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorM
                                    kSmem<D>, s, a, qmap, kmap, vmap);
   if (e == cudaSuccess && p.cut) {
     // many rows have few partials each: two rows a thread take 167 us where one takes 174 (16 x 61 behind 12001, with the
-    // main kernel), 86 and 91 (64 x 17, heads of 64), but 51 where one takes 43 (1 x 61 behind 32768)
+    // main kernel), 86 and 91 (64 x 17, heads of 64), but 51 where one takes 43 (1 x 61 behind 32768).  Between, behind
+    // 4000 keys: 29.9 and 28.1 at 5856 rows, 30.9 and 31.1 at 7808, 33.9 and 33.5 at 9760, 42.9 and 44.9 at 15616.
     const bool many = p.rows > 8192;
     const int rows = std::min(a.slots * a.group, p.nt_b * p.tile), items = p.tiles_b * a.c.kv_heads;
     const int each = (many ? 2 : 1) * 1024 / D;
@@ -1084,7 +1085,9 @@ cudaError_t prepare_kv_attend() {
 
 int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int64_t)num_sms * 256; }
 
-// Chooses between packed and joined items, and between cut and whole ones, from the sizes alone.  Costs are in
+// Chooses between packed and joined items, and between cut and whole ones, from the sizes alone: of the contexts it knows
+// the bound, and a loose one costs what the wrong form does (1 x 1 behind 100: 6.8 us, 10.0 with a bound of 4096; 16 x 61
+// behind 500: 19.6, 19.9 with 4096, 33.7 with 32768; 64 x 17 behind 2048 + 100: 81 with any).  Costs are in
 // units of 10 ns, measured on one SM: a key block of 128 against two tiles of 128 rows, against one, and the least a block
 // takes when its keys and values come from memory (the SM's share of the copy rate) or from L2, where other items' SMs
 // read them too; before its first block an item pays for its queries, and the pipeline's start and end.
@@ -1125,7 +1128,9 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     p.cut = 1;
     p.ctas = num_sms;
     // With few items the costs of a busy machine are off by `off`: whole and cut are level at 500 keys for 1 x 61 slots (14.8
-    // us; at 1000 whole takes 20.5, cut 16.0), at 1000 for 1 x 1 (12.2; at 500 9.0 and 11.3), at 1900 for 8 x 1 (20).
+    // us; at 1000 whole takes 20.5, cut 16.0), at 1000 for 1 x 1 (12.2; at 500 9.0 and 11.3), at 1900 for 8 x 1 (21).
+    // On both sides of these points (1 x 1 and 61, 2 x 61, 4 x 4, 8 x 1 and 17, 32/8 heads of 64 and 128, 52 sizes) the rule
+    // takes the faster form but for 1 x 61 at 600 (16.3, cut 14.8), 4 x 4 at 1500 (15.8 and 14.6) and two level ones.
     const int off = p.nt_b == 2 ? (wide ? -400 : -200) : (wide ? -100 : 200);
     if (!packed && items_b <= num_sms && whole <= t + off) {
       p.cut = 0;

@@ -526,7 +526,8 @@ int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
  *   d_prefix_pages int32 [ceil(prefix_len / page_size)], NULL when prefix_len is 0
  *   max_ctx       a bound on every ctx_len[b], known to the host (it sizes the
  *                 work; max_ctx + slots <= table_stride * page_size, and
- *                 prefix_len + max_ctx + slots <= 2^31 - 257)
+ *                 prefix_len + max_ctx + slots <= 2^31 - 257).  A bound near
+ *                 the longest length is faster than a loose one
  *   d_tree_mask   uint64 [batch][slots], NULL: slot i sees slots 0 .. i
  *   scale         finite and > 0
  *   d_lse         float [batch * slots][q_heads], or NULL

@@ -67,3 +67,15 @@ def test_tree_decoding_emits_the_targets_own_tokens(prefix_len, lengths):
                 x[1::2] = -float("inf")
                 assert t % 2 == 0
             assert x[t] >= x.max() - 0.4, (b, i, t)
+
+
+def test_the_longest_request_is_refused_before_its_pages_end():
+    """The bound that the loop passes follows its requests; one that has outgrown its pages is refused, and nothing ran."""
+    from workloads.target_model import TargetLoop, ToyTarget
+    loop = TargetLoop(ToyTarget(seed=3), [], [list(range(20)), [5]], longest=24)
+    steps = 0
+    with pytest.raises(ValueError, match="24 tokens"):
+        for steps in range(30):
+            loop.step()
+            assert loop.ctx.tolist() == loop.held
+    assert steps > 0 and loop.kv.sync() == 0 and max(loop.held) <= 24 + loop.S

@@ -105,6 +105,7 @@ class TargetLoop:
         self.prompt_len = self.hist_len.clone()
         self.ctx = self.hist_len - 1
         self.emitted = [[] for _ in prompts]
+        self.held = [len(p) - 1 for p in prompts]      # the host's copy of ctx: its largest bounds the attention's work
         assert most <= longest
 
     def _prefill(self, tokens, table, prefix_len, ctx):
@@ -131,12 +132,14 @@ class TargetLoop:
 
     def step(self):
         """One decode step of every request; returns the accepted lengths."""
+        if max(self.held) > self.longest:
+            raise ValueError(f"a request has passed the {self.longest} tokens that the pages were laid out for")
         B, S, eng, dev = self.B, self.S, self.eng, self.hist.device
         t = g.TreeBuffers(B, S, dev)
         root = self.hist.gather(1, (self.hist_len - 1).long()[:, None]).view(-1)
         none = torch.zeros((B, 0), device=dev)
         eng.assemble(B, root, none.int(), none.short(), none.float(), t.tok, t.parent, t.pos, t.mask, t.info)
-        logits, kept = self._forward(t.tok, t.pos, t.mask, self.table, self.prefix_len, self.ctx, self.longest)
+        logits, kept = self._forward(t.tok, t.pos, t.mask, self.table, self.prefix_len, self.ctx, max(self.held))
         rules = {}
         if self.grammar is not None:
             rules = dict(grammar=self.grammar, grammar_row=self.grammar_of[t.tok.clamp(min=0).long()].contiguous())
@@ -154,6 +157,7 @@ class TargetLoop:
             at = int(self.hist_len[b])
             self.hist[b, at:at + n + 1] = new
             self.emitted[b] += new.tolist()
+            self.held[b] += n + 1
         self.hist_len += t.accept_len + 1
         self.ctx += t.accept_len + 1
         assert eng.sync() == 0 and self.kv.sync() == 0
