@@ -192,9 +192,121 @@ static PyObject* logits(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
+typedef int (*append_ext_fn)(void*, int32_t, int32_t, const void*, int64_t, const void*, int64_t, const void*, int64_t,
+                             const int32_t*, const int32_t*, const int32_t*, const float*, int32_t, int32_t, const int32_t*,
+                             int32_t, const int32_t*, void*, int64_t, void*, void*, const graft_kv_scales*, void*);
+typedef int (*attend_ext_fn)(void*, int32_t, int32_t, const void*, int64_t, const void*, const void*, const int32_t*, int32_t,
+                             const int32_t*, int32_t, const int32_t*, int32_t, const uint64_t*, float, void*, int64_t,
+                             float*, const graft_kv_scales*, const graft_kv_scores*, void*);
+typedef int (*read_fn)(void*, int32_t, int32_t, const void*, const void*, const int32_t*, int32_t, const int32_t*,
+                       const int32_t*, const graft_kv_scales*, void*, int64_t, void*, int64_t, void*);
+
+/* append_ext(entry, handle, stream, dtype, float32, int32, cache_dtype, q_width, kv_width, rot_dim, span, kv_heads, axes,
+ *            batch, slots, prefix_len, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, pos, rows, positions,
+ *            k_scale, v_scale) */
+static PyObject* append_ext(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long v[16];
+  if (n != 30) GIVE_UP;
+  for (int i = 0; i < 16; ++i)
+    if (!(i >= 3 && i <= 6) && !whole(a[i], &v[i])) GIVE_UP;
+  PyObject *dt = a[3], *f32 = a[4], *i32 = a[5], *dc = a[6];
+  const long long qw = v[7], kw = v[8], rot = v[9], span = v[10], heads = v[11], axes = v[12], batch = v[13], slots = v[14], prefix = v[15];
+  if (!small(batch) || !small(slots) || !small(prefix) || batch < 0 || slots < 1) GIVE_UP;
+  const long long rows = batch * slots;
+  void *q, *k, *w, *rope, *pt, *ctx, *kc, *vc, *qo, *pos, *src, *at, *sk, *sv;
+  int64_t qs, ks, ws, qos;
+  long long width, pages, positions, unused;
+  if (!rows_of(a[16], dt, rows, qw, &q, &qs) || !rows_of(a[17], dt, rows, kw, &k, &ks) ||
+      !rows_of(a[18], dt, rows, kw, &w, &ws) || !table(a[19], f32, 0, &rope, &positions, &width) ||
+      !table(a[20], i32, batch, &pt, &unused, &pages) || !buffer(a[21], i32, batch, &ctx) || !buffer(a[22], dc, span, &kc) ||
+      !buffer(a[23], dc, span, &vc) || !rows_of(a[24], dt, rows, qw, &qo, &qos) || !buffer(a[25], i32, rows, &pos) ||
+      !buffer(a[26], i32, rows, &src) || !buffer(a[27], i32, axes * rows, &at) || !buffer(a[28], f32, heads, &sk) ||
+      !buffer(a[29], f32, heads, &sv))
+    GIVE_UP;
+  if (rope && (width != rot || !small(positions))) GIVE_UP;
+  if (at && number(a[27], s_numel) != axes * rows) GIVE_UP;
+  if (!small(pages)) GIVE_UP;
+  const graft_kv_scales scales = {sk, sv};
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((append_ext_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, k, ks, w, ws, pos, src,
+                                        at, rope, (int32_t)positions, (int32_t)prefix, pt, (int32_t)pages, ctx, qo, qos, kc,
+                                        vc, &scales, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
+}
+
+/* attend_ext(entry, handle, stream, dtype, float32, int32, int64, cache_dtype, q_width, q_heads, page_size, span, kv_heads,
+ *            batch, slots, prefix_len, max_ctx, window, scale, softcap, q, k_cache, v_cache, page_table, ctx_len, out,
+ *            prefix_pages, tree_mask, lse, slopes, k_scale, v_scale) */
+static PyObject* attend_ext(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long v[18];
+  if (n != 32) GIVE_UP;
+  for (int i = 0; i < 18; ++i)
+    if (!(i >= 3 && i <= 7) && !whole(a[i], &v[i])) GIVE_UP;
+  PyObject *dt = a[3], *f32 = a[4], *i32 = a[5], *i64 = a[6], *dc = a[7];
+  const long long qw = v[8], heads = v[9], page = v[10], span = v[11], kv_heads = v[12], batch = v[13], slots = v[14];
+  const long long prefix = v[15], max_ctx = v[16], window = v[17];
+  const double scale = PyFloat_AsDouble(a[18]);
+  if (PyErr_Occurred()) { PyErr_Clear(); GIVE_UP; }
+  const double softcap = PyFloat_AsDouble(a[19]);
+  if (PyErr_Occurred()) { PyErr_Clear(); GIVE_UP; }
+  if (!small(batch) || !small(slots) || !small(prefix) || !small(max_ctx) || !small(window) || batch < 0 || slots < 1 || prefix < 0)
+    GIVE_UP;
+  const long long rows = batch * slots;
+  void *q, *kc, *vc, *pt, *ctx, *out, *pre, *mask, *lse, *slope, *sk, *sv;
+  int64_t qs, os;
+  long long pages, unused;
+  if (!rows_of(a[20], dt, rows, qw, &q, &qs) || !buffer(a[21], dc, span, &kc) || !buffer(a[22], dc, span, &vc) ||
+      !table(a[23], i32, batch, &pt, &unused, &pages) || !buffer(a[24], i32, batch, &ctx) || !rows_of(a[25], dt, rows, qw, &out, &os) ||
+      !buffer(a[26], i32, (prefix + page - 1) / page, &pre) || !buffer(a[27], i64, rows, &mask) ||
+      !buffer(a[28], f32, rows * heads, &lse) || !buffer(a[29], f32, heads, &slope) || !buffer(a[30], f32, kv_heads, &sk) ||
+      !buffer(a[31], f32, kv_heads, &sv) || !small(pages))
+    GIVE_UP;
+  const graft_kv_scales scales = {sk, sv};
+  const graft_kv_scores scores = {(float)softcap, (int32_t)window, slope};
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((attend_ext_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, q, qs, kc, vc, pre,
+                                        (int32_t)prefix, pt, (int32_t)pages, ctx, (int32_t)max_ctx, mask, (float)scale, out,
+                                        os, lse, &scales, &scores, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
+}
+
+/* read(entry, handle, stream, dtype, float32, int32, cache_dtype, kv_width, span, kv_heads, batch, slots, k_cache, v_cache,
+ *      page_table, first, count, k_out, v_out, k_scale, v_scale) */
+static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long v[12];
+  if (n != 21) GIVE_UP;
+  for (int i = 0; i < 12; ++i)
+    if (!(i >= 3 && i <= 6) && !whole(a[i], &v[i])) GIVE_UP;
+  PyObject *dt = a[3], *f32 = a[4], *i32 = a[5], *dc = a[6];
+  const long long kw = v[7], span = v[8], heads = v[9], batch = v[10], slots = v[11];
+  if (!small(batch) || !small(slots) || batch < 0 || slots < 1) GIVE_UP;
+  void *kc, *vc, *pt, *first, *count, *k, *w, *sk, *sv;
+  int64_t ks, ws;
+  long long pages, unused;
+  if (!buffer(a[12], dc, span, &kc) || !buffer(a[13], dc, span, &vc) || !table(a[14], i32, batch, &pt, &unused, &pages) ||
+      !buffer(a[15], i32, batch, &first) || !buffer(a[16], i32, batch, &count) || !rows_of(a[17], dt, batch * slots, kw, &k, &ks) ||
+      !rows_of(a[18], dt, batch * slots, kw, &w, &ws) || !buffer(a[19], f32, heads, &sk) || !buffer(a[20], f32, heads, &sv) ||
+      !small(pages))
+    GIVE_UP;
+  const graft_kv_scales scales = {sk, sv};
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = ((read_fn)(uintptr_t)v[0])((void*)(uintptr_t)v[1], (int32_t)batch, (int32_t)slots, kc, vc, pt, (int32_t)pages, first,
+                                  count, &scales, k, ks, w, ws, (void*)(uintptr_t)v[2]);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(rc);
+}
+
 static PyMethodDef methods[] = {{"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
                                 {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, NULL},
                                 {"logits", (PyCFunction)(void (*)(void))logits, METH_FASTCALL, NULL},
+                                {"append_ext", (PyCFunction)(void (*)(void))append_ext, METH_FASTCALL, NULL},
+                                {"attend_ext", (PyCFunction)(void (*)(void))attend_ext, METH_FASTCALL, NULL},
+                                {"read", (PyCFunction)(void (*)(void))read_back, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -11,6 +11,7 @@ namespace graft {
 struct KvLayout {
   int32_t q_heads, kv_heads, dim, rot, interleaved, page_size, page_shift, num_pages;
   int64_t page_stride, head_stride, token_stride;  // elements
+  int32_t eight;                                   // 1 = the caches hold e4m3 numbers
 };
 
 // Quotients of numbers below 2^31 by a divisor that the host knows: with s = ceil(log2 d) and
@@ -39,6 +40,24 @@ struct AppendArgs {
   const int32_t* ctx_len;
   void *q_out, *k_cache, *v_cache;
   Divisor by_slots, by_turn, by_value;  // slots; 16-byte pieces of a rotating head (each with its partner), of a head
+  const int32_t* position;  // [axes][tokens], or NULL
+  int64_t tokens;           // batch * slots
+  int32_t axes;
+  uint8_t pair_axis[64];    // axis whose position turns a pair
+  const float *k_scale, *v_scale;  // of 8-bit caches
+  uint32_t* err;
+};
+
+struct ReadArgs {
+  KvLayout c;
+  int32_t batch, slots, vec;  // vec: 16-byte stores of the rows
+  const void *k_cache, *v_cache;
+  const int32_t *page_table, *first, *count;
+  int32_t table_stride;
+  const float *k_scale, *v_scale;
+  void *k_out, *v_out;
+  int64_t k_stride, v_stride;
+  Divisor by_slots, by_head;  // slots; 16-byte pieces of a head
   uint32_t* err;
 };
 
@@ -75,6 +94,10 @@ struct AttendArgs {
   float *part_o, *part_lse;  // partial results (rows of dim) and their log-sum-exp in log2
   int64_t* line;             // [batch] starts of the requests' items; a CTA's share; [ctas] items that a CTA begins and does not end
   uint32_t wait_polls;       // 0 = the default
+  const float *k_scale, *v_scale;  // of 8-bit caches
+  float softcap;             // 0 = none
+  int32_t window;            // 0 = none
+  const float* slope;        // [q_heads], or NULL
   uint32_t* err;
 };
 
@@ -106,12 +129,23 @@ struct Pair<__half> {
   static __device__ __forceinline__ __half round(float x) { return __float2half_rn(x); }
 };
 
+// A head's scale of an 8-bit cache; one that is no number above zero counts as 1.
+__device__ __forceinline__ float kv_scale(const float* scale, int head, uint32_t* err) {
+  if (!scale) return 1.f;
+  const float s = scale[head];
+  if (s > 0.f && s < INFINITY) return s;
+  atomicOr(err, GRAFT_ERR_RULE);
+  return 1.f;
+}
+
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t s);
 cudaError_t prepare_kv_attend();
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int num_sms);
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s);
+cudaError_t launch_kv_attend_ext(const AttendArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace graft

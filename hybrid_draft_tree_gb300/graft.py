@@ -24,6 +24,7 @@ GRAFT_ERR_TOKEN, GRAFT_ERR_NAN, GRAFT_ERR_TREE, GRAFT_ERR_TIMEOUT = 1, 2, 4, 8
 GRAFT_ERR_RANGE, GRAFT_ERR_RULE = 16, 32
 GRAFT_MODE_CHECKPOINT, GRAFT_MODE_STATIC, GRAFT_MODE_TAIL = 0, 1, 2
 GRAFT_F32, GRAFT_BF16, GRAFT_F16 = 0, 1, 2
+GRAFT_CACHE_E4M3 = 256
 K = 8
 
 # Entry points declared in include/graft.h (checked by the CPU tests).
@@ -34,7 +35,7 @@ EXPORTS = ("graft_default_config", "graft_init", "graft_destroy", "graft_warmup"
            "graft_confidence", "graft_calibrate_thresholds", "graft_set_thresholds", "graft_coverage",
            "graft_verify_update_sample", "graft_template", "graft_set_wait_limit", "graft_process_logits",
            "graft_kv_default_config", "graft_kv_init", "graft_kv_destroy", "graft_kv_append", "graft_kv_attend",
-           "graft_kv_sync", "graft_kv_last_error", "graft_kv_last_launch_count", "graft_kv_set_wait_limit")
+           "graft_kv_append_ext", "graft_kv_attend_ext", "graft_kv_read", "graft_kv_set_axes", "graft_kv_sync", "graft_kv_last_error", "graft_kv_last_launch_count", "graft_kv_set_wait_limit")
 
 
 def calibrate_thresholds(best: np.ndarray, quantile: float) -> np.ndarray:
@@ -82,6 +83,14 @@ class graft_kv_config(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("max_batch", ctypes.c_int32), ("max_slots", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64)]
+
+
+class graft_kv_scales(ctypes.Structure):
+    _fields_ = [("d_k_scale", ctypes.c_void_p), ("d_v_scale", ctypes.c_void_p)]
+
+
+class graft_kv_scores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("d_slope", ctypes.c_void_p)]
 
 
 class graft_logit_rules(ctypes.Structure):
@@ -152,6 +161,12 @@ def load(build_if_missing: bool = True):
                                   vp, vp, vp]
     L.graft_kv_attend.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, i64,
                                   vp, vp]
+    L.graft_kv_append_ext.argtypes = [vp, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp,
+                                      i64, vp, vp, ctypes.POINTER(graft_kv_scales), vp]
+    L.graft_kv_attend_ext.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, i64,
+                                      vp, ctypes.POINTER(graft_kv_scales), ctypes.POINTER(graft_kv_scores), vp]
+    L.graft_kv_read.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, ctypes.POINTER(graft_kv_scales), vp, i64, vp, i64, vp]
+    L.graft_kv_set_axes.argtypes = [vp, i32, ctypes.POINTER(i32)]
     L.graft_kv_sync.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     L.graft_kv_last_error.argtypes = [vp]
     L.graft_kv_last_error.restype = ctypes.c_char_p
@@ -593,10 +608,14 @@ class Graft:
 
 
 def graft_kv_default_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_slots, dtype=GRAFT_BF16,
-                            layout="head", **overrides):
+                            layout="head", cache=None, **overrides):
     """layout: "head" for pages of [kv_heads, page_size, head_dim], "token" for
-    [page_size, kv_heads, head_dim]; other strides through the overrides."""
+    [page_size, kv_heads, head_dim]; other strides through the overrides.
+    cache: "e4m3" for keys and values held in 8 bits, None for the type itself."""
     cfg = graft_kv_config()
+    if cache not in (None, "e4m3"):
+        raise GraftError(GRAFT_EINVAL, f"cache {cache!r}, expected None or 'e4m3'")
+    dtype |= GRAFT_CACHE_E4M3 if cache else 0
     load().graft_kv_default_config(ctypes.byref(cfg), q_heads, kv_heads, head_dim, page_size, num_pages, max_batch,
                                    max_slots, dtype)
     if layout not in ("head", "token"):
@@ -613,13 +632,16 @@ class GraftKV:
     target's keys, values and attention around a draft tree.  The caches are
     the caller's tensors."""
 
-    _append = _attend = None
+    _append = _attend = _append_ext = _attend_ext = _read = None
+    eight = False  # an 8-bit cache
+    axes = 1       # of positions given to append
 
     def __init__(self, cfg: graft_kv_config):
         import torch
         self.L = load()
         self.cfg = cfg
-        self.dtype = torch.float16 if cfg.dtype == GRAFT_F16 else torch.bfloat16
+        self.dtype = torch.float16 if cfg.dtype & ~GRAFT_CACHE_E4M3 == GRAFT_F16 else torch.bfloat16
+        self.eight = bool(cfg.dtype & GRAFT_CACHE_E4M3)
         self.q_heads, self.page_size, self.rot_dim = cfg.q_heads, cfg.page_size, cfg.rot_dim
         self.q_width, self.kv_width = cfg.q_heads * cfg.head_dim, cfg.kv_heads * cfg.head_dim
         self.span = _cache_span(cfg)
@@ -629,14 +651,15 @@ class GraftKV:
         if rc != GRAFT_OK:
             raise GraftError(rc, "graft_kv_init failed (bad config, no CUDA device, or out of memory)")
         self.h = h
-        self._append, self._attend = _Entry(self.L, "graft_kv_append", h), _Entry(self.L, "graft_kv_attend", h)
+        self._append, self._attend, self._append_ext, self._attend_ext, self._read = (
+            _Entry(self.L, "graft_kv_" + name, h) for name in ("append", "attend", "append_ext", "attend_ext", "read"))
 
     def _check(self, rc):
         if rc != GRAFT_OK:
             raise GraftError(rc, self.L.graft_kv_last_error(self.h).decode())
 
     def close(self):
-        self._append = self._attend = None
+        self._append = self._attend = self._append_ext = self._attend_ext = self._read = None
         if self.h:
             self.L.graft_kv_destroy(self.h)
             self.h = None
@@ -647,13 +670,43 @@ class GraftKV:
         except Exception:
             pass
 
+    def _cache_dtype(self, cache):
+        """Element type that a cache has to have: 8-bit ones may be held as bytes."""
+        if not self.eight:
+            return self.dtype
+        return _T.uint8 if getattr(cache, "dtype", None) is _T.uint8 else _T.float8_e4m3fn
+
+    def _scales(self, k_scale, v_scale):
+        heads = self.cfg.kv_heads
+        if k_scale is None and v_scale is None:
+            return None
+        if not self.eight:
+            raise GraftError(GRAFT_EINVAL, "k_scale, v_scale: only 8-bit caches have scales")
+        return ctypes.byref(graft_kv_scales(_addr(k_scale, "k_scale", _T.float32, heads),
+                                            _addr(v_scale, "v_scale", _T.float32, heads)))
+
+    def set_axes(self, pair_axis):
+        """Positions of several axes: pair_axis[i] is the axis, 0 and up, whose
+        position turns pair i of a rotating head (rot_dim / 2 of them)."""
+        pair_axis = [int(x) for x in pair_axis]
+        if len(pair_axis) != self.rot_dim // 2:
+            raise GraftError(GRAFT_EINVAL, f"pair_axis: {len(pair_axis)} entries, a head has {self.rot_dim // 2} pairs")
+        axes = max(pair_axis, default=0) + 1
+        self._check(self.L.graft_kv_set_axes(self.h, axes, (i32 * max(1, len(pair_axis)))(*pair_axis)))
+        self.axes = axes
+
     def append(self, batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len=0, pos=None,
-               rows=None, stream=None):
+               rows=None, stream=None, positions=None, k_scale=None, v_scale=None):
         """Rotate and write the slots' keys and values into the cache, and rotate
         the queries into q_out (both None: keys and values only).  q, k, v: rows
         [batch * slots, heads * head_dim], any row stride; rope: float32
         [positions, rot_dim]; page_table: int32 [batch, pages]; pos: the slots'
-        depths (tree_pos); rows: int32 [batch, slots], the slot each place takes."""
+        depths (tree_pos); rows: int32 [batch, slots], the slot each place takes;
+        positions: int32 [axes, batch, slots], rotated by in place of prefix_len +
+        ctx_len + pos; k_scale, v_scale: float32 [kv_heads], of an 8-bit cache."""
+        if self.eight or positions is not None or k_scale is not None or v_scale is not None:
+            return self._append_more(batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len,
+                                     pos, rows, stream, positions, k_scale, v_scale)
         f = self._append
         if f is not None and f.module is not None:
             rc = f.module.append(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, self.q_width,
@@ -677,11 +730,72 @@ class GraftKV:
                                            _cache(k_cache, "k_cache", dt, self.span),
                                            _cache(v_cache, "v_cache", dt, self.span), _stream_addr(stream)))
 
+    def _append_more(self, batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len, pos, rows,
+                     stream, positions, k_scale, v_scale):
+        f, dc = self._append_ext, self._cache_dtype(k_cache)
+        if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
+            rc = f.module.append_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, dc, self.q_width,
+                                     self.kv_width, self.rot_dim, self.span, self.cfg.kv_heads, self.axes, batch, slots,
+                                     prefix_len, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, pos, rows,
+                                     positions, k_scale, v_scale)
+            if rc is not NotImplemented:
+                return self._check(rc)
+        b, dt, i32 = max(batch, 0), self.dtype, _T.int32
+        n = b * slots
+        scales = self._scales(k_scale, v_scale)
+        pq, qs = _row_addr(q, "q", dt, n, self.q_width)
+        pk, ks = _row_addr(k, "k", dt, n, self.kv_width)
+        pv, vs = _row_addr(v, "v", dt, n, self.kv_width)
+        po, qos = _row_addr(q_out, "q_out", dt, n, self.q_width)
+        pr, width = _table(rope, "rope", _T.float32, 0)
+        if rope is not None and width != self.rot_dim:
+            raise GraftError(GRAFT_EINVAL, f"rope: rows of {width}, the handle rotates {self.rot_dim}")
+        pt, ts = _table(page_table, "page_table", i32, b)
+        pp = _addr(positions, "positions", i32, self.axes * n)
+        if positions is not None and positions.numel() != self.axes * n:
+            raise GraftError(GRAFT_EINVAL, f"positions: {positions.numel()} elements, expected [{self.axes}, {b}, {slots}]")
+        self._check(self.L.graft_kv_append_ext(self.h, batch, slots, pq, qs, pk, ks, pv, vs, _addr(pos, "pos", i32, n),
+                                               _addr(rows, "rows", i32, n), pp, pr, 0 if rope is None else rope.shape[0],
+                                               prefix_len, pt, ts, _addr(ctx_len, "ctx_len", i32, b), po, qos,
+                                               _cache(k_cache, "k_cache", dc, self.span),
+                                               _cache(v_cache, "v_cache", dc, self.span), scales, _stream_addr(stream)))
+
+    def read(self, batch, slots, k_cache, v_cache, page_table, first, count, k_out, v_out, k_scale=None, v_scale=None,
+             stream=None):
+        """Read back keys and values: place first[b] + i of request b, for i <
+        count[b] (<= slots), into row b * slots + i of k_out and v_out (rows
+        [batch * slots, kv_heads * head_dim] of the 16-bit type, any row stride);
+        of an 8-bit cache, what the codes stand for."""
+        f, dc = self._read, self._cache_dtype(k_cache)
+        if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
+            rc = f.module.read(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, dc, self.kv_width,
+                               self.span, self.cfg.kv_heads, batch, slots, k_cache, v_cache, page_table, first, count, k_out,
+                               v_out, k_scale, v_scale)
+            if rc is not NotImplemented:
+                return self._check(rc)
+        b, dt, i32 = max(batch, 0), self.dtype, _T.int32
+        n = b * slots
+        scales = self._scales(k_scale, v_scale)
+        pk, ks = _row_addr(k_out, "k_out", dt, n, self.kv_width)
+        pv, vs = _row_addr(v_out, "v_out", dt, n, self.kv_width)
+        pt, ts = _table(page_table, "page_table", i32, b)
+        self._check(self.L.graft_kv_read(self.h, batch, slots, _cache(k_cache, "k_cache", dc, self.span),
+                                         _cache(v_cache, "v_cache", dc, self.span), pt, ts, _addr(first, "first", i32, b),
+                                         _addr(count, "count", i32, b), scales, pk, ks, pv, vs, _stream_addr(stream)))
+
     def attend(self, batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages=None,
-               prefix_len=0, tree_mask=None, scale=None, lse=None, stream=None):
+               prefix_len=0, tree_mask=None, scale=None, lse=None, stream=None, softcap=0.0, window=0, slopes=None,
+               k_scale=None, v_scale=None):
         """Attention of the slots' rotated queries over the prefix, each
         request's ctx_len (<= max_ctx) tokens and the tree under tree_mask
-        (None: causal), into out and lse.  scale defaults to head_dim ** -0.5."""
+        (None: causal), into out and lse.  scale defaults to head_dim ** -0.5.
+        softcap: scores pass softcap * tanh(score / softcap); slopes: float32
+        [q_heads], times the distance off a score; window: the last positions that
+        a row sees, its own among them (0: all); k_scale, v_scale: float32
+        [kv_heads], of an 8-bit cache."""
+        if self.eight or softcap or window or slopes is not None or k_scale is not None or v_scale is not None:
+            return self._attend_more(batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages,
+                                     prefix_len, tree_mask, scale, lse, stream, softcap, window, slopes, k_scale, v_scale)
         f = self._attend
         if f is not None and f.module is not None:
             rc = f.module.attend(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, _T.int64,
@@ -703,6 +817,34 @@ class GraftKV:
                                            _mask_addr(tree_mask, "tree_mask", n),
                                            self.scale if scale is None else scale, po, os_,
                                            _addr(lse, "lse", _T.float32, n * self.q_heads), _stream_addr(stream)))
+
+    def _attend_more(self, batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages, prefix_len,
+                     tree_mask, scale, lse, stream, softcap, window, slopes, k_scale, v_scale):
+        f, dc = self._attend_ext, self._cache_dtype(k_cache)
+        scale = self.scale if scale is None else scale
+        if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
+            rc = f.module.attend_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, _T.int64, dc,
+                                     self.q_width, self.q_heads, self.page_size, self.span, self.cfg.kv_heads, batch, slots,
+                                     prefix_len, max_ctx, window, scale, softcap, q, k_cache, v_cache, page_table, ctx_len,
+                                     out, prefix_pages, tree_mask, lse, slopes, k_scale, v_scale)
+            if rc is not NotImplemented:
+                return self._check(rc)
+        b, dt, i32 = max(batch, 0), self.dtype, _T.int32
+        n = b * slots
+        scales = self._scales(k_scale, v_scale)
+        pq, qs = _row_addr(q, "q", dt, n, self.q_width)
+        po, os_ = _row_addr(out, "out", dt, n, self.q_width)
+        pt, ts = _table(page_table, "page_table", i32, b)
+        pages = -(-max(prefix_len, 0) // self.page_size)
+        if not -2 ** 31 <= window < 2 ** 31:
+            raise GraftError(GRAFT_EINVAL, f"window {window}: beyond 32 bits")
+        scores = graft_kv_scores(softcap, window, _addr(slopes, "slopes", _T.float32, self.q_heads))
+        self._check(self.L.graft_kv_attend_ext(self.h, batch, slots, pq, qs, _cache(k_cache, "k_cache", dc, self.span),
+                                               _cache(v_cache, "v_cache", dc, self.span),
+                                               _addr(prefix_pages, "prefix_pages", i32, pages), prefix_len, pt, ts,
+                                               _addr(ctx_len, "ctx_len", i32, b), max_ctx, _mask_addr(tree_mask, "tree_mask", n),
+                                               scale, po, os_, _addr(lse, "lse", _T.float32, n * self.q_heads), scales,
+                                               ctypes.byref(scores), _stream_addr(stream)))
 
     def sync(self, stream=None, raise_on_error=True) -> int:
         flags = ctypes.c_uint32(0)

@@ -68,7 +68,7 @@ typedef enum {
 #define GRAFT_ERR_TREE 4u    /* parent index not before its child, bad position */
 #define GRAFT_ERR_TIMEOUT 8u /* a bounded wait inside a kernel expired; that call's results are invalid */
 #define GRAFT_ERR_RANGE 16u /* a cache page, a length, a row or a position outside its range (graft_kv_*) */
-#define GRAFT_ERR_RULE 32u  /* a penalty that is not a number it can be, or a grammar row outside the table */
+#define GRAFT_ERR_RULE 32u  /* a penalty, scale or slope that is not a number it can be, or a grammar row outside the table */
 
 typedef enum {
   GRAFT_MODE_CHECKPOINT = 0, /* article §二: checkpoints at depths 0/1/5 */
@@ -461,6 +461,13 @@ int graft_set_wait_limit(graft_handle* h, uint32_t polls);
  * time.  One handle serves every layer of a model. */
 typedef struct graft_kv graft_kv;
 
+/* Beside the type in graft_kv_config's dtype: the cache holds its keys and
+ * values in 8 bits, as e4m3 numbers (sign, 4 bits of exponent, 3 of fraction;
+ * largest 448, no infinities) that stand for themselves times their head's
+ * scale (graft_kv_scales).  Queries, the rows given to an append and results
+ * stay in the 16-bit type. */
+#define GRAFT_CACHE_E4M3 256
+
 typedef struct {
   int32_t q_heads;         /* query heads, a multiple of kv_heads */
   int32_t kv_heads;        /* key and value heads */
@@ -471,8 +478,8 @@ typedef struct {
   int32_t num_pages;       /* pages of each cache buffer */
   int32_t max_batch;       /* largest batch passed to graft_kv_attend */
   int32_t max_slots;       /* largest slots passed to graft_kv_attend, in [1, 64] */
-  int32_t dtype;           /* of queries, keys, values and outputs: GRAFT_BF16 or GRAFT_F16 */
-  int64_t page_stride;     /* elements; multiples of 8; nested in any order, no two tokens overlapping */
+  int32_t dtype;           /* of queries, keys, values and outputs: GRAFT_BF16 or GRAFT_F16; + GRAFT_CACHE_E4M3 */
+  int64_t page_stride;     /* elements; multiples of 8 (16 of an 8-bit cache); nested in any order, no two tokens overlapping */
   int64_t head_stride;
   int64_t token_stride;
 } graft_kv_config;
@@ -542,6 +549,80 @@ int graft_kv_attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
                     const int32_t* d_page_table, int32_t table_stride, const int32_t* d_ctx_len, int32_t max_ctx,
                     const uint64_t* d_tree_mask, float scale, void* d_out, int64_t out_stride, float* d_lse,
                     void* stream);
+
+/* The scales of an 8-bit cache (only of one): DEVICE float [kv_heads] each, all
+ * finite and > 0; NULL: 1.  A scale is the caller's, from a calibration: e4m3
+ * numbers carry their own exponent, so all it has to do is to bring a head's
+ * largest magnitudes below 448 and what matters above 2^-6.  One that is not
+ * finite and > 0 counts as 1 and sets GRAFT_ERR_RULE. */
+typedef struct {
+  const float* d_k_scale;
+  const float* d_v_scale;
+} graft_kv_scales;
+
+/* Positions of several axes (time, height and width of images and video): pair
+ * i of a rotating head (element i and its partner) turns by the angle of the
+ * position on axis pair_axis[i], HOST int32 [rot_dim / 2], each in [0, axes);
+ * axes in [1, 8].  Of later appends that pass d_position; before any call there
+ * is one axis for all pairs. */
+int graft_kv_set_axes(graft_kv* h, int32_t axes, const int32_t* pair_axis);
+
+/* graft_kv_append on either kind of cache, with what graft_kv_append has no
+ * arguments for (all NULL: the same call):
+ *   d_position   int32 [axes][batch][slots]: the positions by which the query
+ *                and the key of a slot (of source row r with d_rows) are
+ *                rotated, in place of prefix_len + ctx_len[b] + depth.  Places
+ *                and pads stay as they are there.  One outside d_rope on any
+ *                axis skips that write and sets GRAFT_ERR_RANGE
+ *   scales       of an 8-bit cache, or NULL.  The stored number is the nearest
+ *                e4m3 number to x / scale (ties to even), x the rotated key or
+ *                the value in fp32, and 448 in magnitude beyond that, for an
+ *                infinite x too; a NaN is kept */
+int graft_kv_append_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride, const void* d_k,
+                        int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_depth,
+                        const int32_t* d_rows, const int32_t* d_position, const float* d_rope, int32_t rope_len,
+                        int32_t prefix_len, const int32_t* d_page_table, int32_t table_stride,
+                        const int32_t* d_ctx_len, void* d_q_out, int64_t q_out_stride, void* d_k_cache,
+                        void* d_v_cache, const graft_kv_scales* scales, void* stream);
+
+/* Read back: the key and value of place d_first[b] + i of request b, for i <
+ * d_count[b], into row b * slots + i of d_k_out and d_v_out (kv_heads * head_dim
+ * elements of the 16-bit type; row strides in elements); of an 8-bit cache, code
+ * times scale, rounded once.  Rows from d_count[b] on are not written.
+ *   d_first, d_count   int32 [batch], first >= 0, count in [0, slots] (outside:
+ *                      clamped, with GRAFT_ERR_RANGE; a negative first reads
+ *                      nothing)
+ * A place outside the table or a page outside the cache skips that row and sets
+ * GRAFT_ERR_RANGE.  Asynchronous; one kernel. */
+int graft_kv_read(graft_kv* h, int32_t batch, int32_t slots, const void* d_k_cache, const void* d_v_cache,
+                  const int32_t* d_page_table, int32_t table_stride, const int32_t* d_first, const int32_t* d_count,
+                  const graft_kv_scales* scales, void* d_k_out, int64_t k_stride, void* d_v_out, int64_t v_stride,
+                  void* stream);
+
+/* What becomes of a score before the softmax (all zero: nothing).  With pos the
+ * position in the sequence that a row sees (the prefix and the context in order,
+ * then the slots of its mask in order, as if its path had been emitted token by
+ * token; the row's own is the last of these), in this order:
+ *   softcap  > 0: s = softcap * tanh(s / softcap); finite
+ *   d_slope  DEVICE float [q_heads] or NULL: s -= d_slope[h] * (pos_i - pos_j);
+ *            one that is not finite counts as 0 and sets GRAFT_ERR_RULE
+ *   window   > 0: keys with pos_i - pos_j >= window are not seen */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* d_slope;
+} graft_kv_scores;
+
+/* graft_kv_attend on either kind of cache, with scales (of an 8-bit one) and
+ * shaped scores; either may be NULL.  On an 8-bit cache
+ *   s_j = scale * k_scale[h] * (q . code of k_j),  out = v_scale[h] * sum exp(s_j - lse) (code of v_j).
+ * scale * k_scale[h] has to stay within fp32; otherwise as there. */
+int graft_kv_attend_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride,
+                        const void* d_k_cache, const void* d_v_cache, const int32_t* d_prefix_pages,
+                        int32_t prefix_len, const int32_t* d_page_table, int32_t table_stride,
+                        const int32_t* d_ctx_len, int32_t max_ctx, const uint64_t* d_tree_mask, float scale,
+                        void* d_out, int64_t out_stride, float* d_lse, const graft_kv_scales* scales,
+                        const graft_kv_scores* scores, void* stream);
 
 /* As graft_sync, graft_last_error, graft_last_launch_count and
  * graft_set_wait_limit, for a graft_kv handle. */
