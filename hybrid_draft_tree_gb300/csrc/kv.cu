@@ -263,16 +263,11 @@ int attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q
     a.window = scores->window < prefix_len + max_ctx + slots ? scores->window : 0;
   }
   a.out_vec = !misaligned(d_out, 16) && out_stride % 8 == 0;
-  a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, h->num_sms);
+  a.plan = graft::plan_kv_attend(batch, slots, a.group, c.kv_heads, c.dim, prefix_len, max_ctx, a.window, c.eight != 0, a.softcap > 0.f,
+                                 h->num_sms);
   a.part_o = h->part_o; a.part_lse = h->part_lse; a.line = h->line; a.wait_polls = h->wait_polls;
   a.by_group = graft::Divisor(a.group);
   a.by_heads = graft::Divisor(c.kv_heads);
-  if (c.eight || a.softcap > 0.f || a.window > 0 || a.slope) {
-    const cudaError_t e = graft::launch_kv_attend_ext(a, h->cfg.dtype, (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_attend launch");
-    h->last_launches = 1;
-    return GRAFT_OK;
-  }
   // A tensor map needs rows on 16-byte boundaries; other queries come by elements (16 x 61 behind 12001 + 2048: 167 us by
   // map, 181 by elements; 64 x 1 behind 8192 + 1024: 60 and 72).
   a.q_map = !misaligned(d_q, 16) && q_stride % 8 == 0 && a.group <= 128 && q_stride < ((int64_t)1 << 38);

@@ -143,9 +143,15 @@ cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t s);
 cudaError_t prepare_kv_attend();
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
-                          int num_sms);
+                          int window, bool eight, bool capped, int num_sms);
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s);
-cudaError_t launch_kv_attend_ext(const AttendArgs& a, int dtype, cudaStream_t s);
+// its forms, a translation unit each
+cudaError_t prepare_kv_attend_shaped();
+cudaError_t launch_kv_attend_shaped(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                    const CUtensorMap& vmap, int dtype, cudaStream_t s);
+cudaError_t prepare_kv_attend_eight();
+cudaError_t launch_kv_attend_eight(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, int dtype, bool shaped, cudaStream_t s);
 
 }  // namespace graft
