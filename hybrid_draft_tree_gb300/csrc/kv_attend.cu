@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
   const int tile_a = p.packed ? (b * per + first) / rows_a : 0;
   if (threadIdx.x < 6) {
     const int np = (a.prefix_len + BN - 1) / BN, which = threadIdx.x >> 1;
-    const int64_t chunk = a.line[a.batch];
+    const int64_t chunk = which && p.split ? p.chunk_a : a.line[a.batch];
     int64_t at;
     if (which == 0) {
       const int blocks = blocks_of<true>(a, ctx_of(a, b));
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(256, R == 2 ? 4 : 3) k_kv_join(const __grid_co
     int c = (int)((float)at * (1.f / (float)chunk));
     if ((int64_t)c * chunk > at) --c;
     if ((int64_t)(c + 1) * chunk <= at) ++c;
-    held[threadIdx.x] = c;
+    held[threadIdx.x] = which ? c : c + p.split;
   }
   __syncthreads();
   const int b_first = held[0], b_last = held[1];
@@ -171,8 +171,20 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   const int64_t R = (int64_t)slots * group, all = batch * R;
   const int np = (prefix_len + BN - 1) / BN, no = (int)(((int64_t)max_ctx + slots + BN - 1) / BN);
   const bool wide = dim == 128;
-  const int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 400, fixed_one = wide ? 280 : 450;
-  const int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
+  int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 400, fixed_one = wide ? 280 : 450;
+  int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
+  const bool few = eight && R <= 16;
+  const int step_few = wide ? 40 : 25, fixed_few = 150;
+  if (eight) {
+    two = wide ? 220 : 195;
+    one = wide ? 150 : 140;
+    memory = wide ? 75 : 40;
+    l2 = wide ? 40 : 20;
+  }
+  if (capped) {
+    two += wide ? 150 : 170;
+    one += wide ? 80 : 90;
+  }
   AttendPlan best{};
   double best_t = 0;
   for (int packed = 0; packed < 2; ++packed) {
@@ -192,7 +204,9 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     int blocks = packed ? no : np + no;
     if (window) blocks = std::min(blocks, (int)(((int64_t)window + slots + BN - 1) / BN) + 1);
     const double alone = packed || batch == 1 ? 1.0 : (double)no / blocks;
-    p.step_b = std::max(p.nt_b == 2 ? two : one, (int)(p.tiles_b > 1 ? l2 : l2 + alone * (memory - l2)));
+    p.few = few ? (R > 8 ? 2 : 1) : 0;
+    if (few) p.fixed_b = fixed_few;
+    p.step_b = std::max(few ? step_few : p.nt_b == 2 ? two : one, (int)(p.tiles_b > 1 ? l2 : l2 + alone * (memory - l2)));
     const int64_t items_b = (int64_t)batch * p.tiles_b * kv_heads;
     const double whole = p.fixed_b + (double)blocks * p.step_b;
     const double work = p.items_a * (p.fixed_a + (double)np * p.step_a) + items_b * whole;
@@ -209,6 +223,13 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
       p.cut = 0;
       p.ctas = (int)items_b;
       t = whole;
+    }
+    if (few && packed) {
+      // the packed items' CTAs, as many as their share of the work
+      const double work_a = p.items_a * (p.fixed_a + (double)np * p.step_a);
+      p.split = std::min(num_sms - 1, std::max(1, (int)(num_sms * (work_a / work) + 0.5)));
+      const int64_t line = (int64_t)p.items_a * (p.fixed_a + (int64_t)np * p.step_a);
+      p.chunk_a = std::max((line + p.split - 1) / p.split, (int64_t)p.step_a);
     }
     if (best_t == 0 || t < best_t) {
       best_t = t;

@@ -201,6 +201,7 @@ struct Bars {
   unsigned long long bad_edge[8];  // such keys where the slots' windows begin, from the root's first on
   float2 ml[2][128];             // a shared tile's maxima and sums
   Line line;
+  int few_loads[4];              // blocks up to and with the last that each copying warp of few rows asked for
   int loads[2], queries;         // loads that each copying warp asked for, the last piece whose queries were
   uint32_t tmem;
   volatile uint32_t abort;
@@ -501,72 +502,81 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {  // 8 numbers
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// kTeams teams of warps take the tiles in turn: a tile's way through a warp is latency (a wait, loads, stores, the word to
+// the products), of which there are then as many under way.
+constexpr int kTeams = 2, kTeamWarps = 2;
+
 template <typename T, int D, bool SHAPED>
 __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring, uint8_t* products) {
   using S = Smem<D, true>;
-  constexpr int kChunks = D / 16;  // of a row
-  const int lane = threadIdx.x & 31, row = threadIdx.x - kConvertWarp * 32;
-  int tiles = 0, piece = 0, to = 0;
-  uint32_t to_phase = 1;  // a fresh barrier passes for the phase before its first
+  constexpr int kChunks = D / 16, kRows = kTeamWarps * 32;  // 16-byte places of a row; rows that a team takes at a time
+  const int lane = threadIdx.x & 31, team = (threadIdx.x / 32 - kConvertWarp) / kTeamWarps;
+  const int first = threadIdx.x - (kConvertWarp + team * kTeamWarps) * 32;
+  int before = 0, piece = 0;
   Pieces<SHAPED> pieces(a, sh.line);
   Item it;
-  for (; pieces.next(it); ++piece) {
-    for (int x = 0; x < 2 * it.blocks; ++x, ++tiles) {
-      const int tile = tile_of<true>(x, it.blocks), v = tile & 1, from = tiles % S::kStages;
-      bool zero = false, check = false;
+  for (; pieces.next(it); before += 2 * it.blocks, ++piece) {
+    for (int x = (team + kTeams - before % kTeams) % kTeams; x < 2 * it.blocks; x += kTeams) {
+      const int tile = tile_of<true>(x, it.blocks), v = tile & 1, number = before + x;
+      const int from = number % S::kStages, to = number % S::kReady;
       Block k{};
       Unseen u{};
+      bool masked = false;
       if (v) {
         k = block_of<SHAPED>(a, it, tile >> 1);
-        if (k.masked) {
-          u = unseen_of<SHAPED>(a, it, k);
-          zero = row >= k.valid || row < u.unseen;
-          check = row >= u.tree || row < u.edge;
-        }
+        masked = k.masked;
+        if (masked) u = unseen_of<SHAPED>(a, it, k);
       }
-      bool ok = wait_bar(sh, a, &sh.full[from], (tiles / S::kStages) & 1);
-      ok = ok && wait_bar(sh, a, &sh.dirty[to], to_phase);
+      // Teams take the places of an odd ring in turn, so the last tile here was the other's: its word is waited for first,
+      // else this wait could be over by the phase before.  A fresh barrier passes for the phase before its first.
+      const uint32_t phase = (number / S::kReady) & 1;
+      bool ok = number < S::kReady || wait_bar(sh, a, &sh.clean[to], phase ^ 1);
+      ok = ok && wait_bar(sh, a, &sh.dirty[to], phase ^ 1);
+      ok = ok && wait_bar(sh, a, &sh.full[from], (number / S::kStages) & 1);
       if (!__all_sync(~0u, ok)) return;
-      const uint8_t* src = ring + from * S::kCopied + row * D;
-      uint8_t* dst = products + to * S::kTile + row * 128;
-      // 16-byte places are exchanged as the copies' swizzle has it: of 128-byte rows by the row's last 3 bits, of 64-byte
-      // rows by bits 1 and 2
-      const int turn = D == 128 ? row & 7 : (row >> 1) & 3;
-      bool any = false;
+#pragma unroll 1
+      for (int row = first; row < 128; row += kRows) {
+        const bool zero = masked && (row >= k.valid || row < u.unseen), check = masked && (row >= u.tree || row < u.edge);
+        const uint8_t* src = ring + from * S::kCopied + row * D;
+        uint8_t* dst = products + to * S::kTile + row * 128;
+        // 16-byte places are exchanged as the copies' swizzle has it: of 128-byte rows by the row's last 3 bits, of 64-byte
+        // rows by bits 1 and 2
+        const int turn = D == 128 ? row & 7 : (row >> 1) & 3;
+        bool any = false;
 #pragma unroll
-      for (int c0 = 0; c0 < kChunks; c0 += 4) {
-        uint4 w[4];
+        for (int c0 = 0; c0 < kChunks; c0 += 4) {
+          uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + (((c0 + c) ^ turn) << 4));
-        if (zero || check) {
+          for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + (((c0 + c) ^ turn) << 4));
+          if (zero || check) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t e[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t nan = ((e[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a bit a NaN
+                any |= nan != 0;
+                e[i] = zero ? 0 : e[i] & ~((nan >> 7) * 0xFF);
+              }
+              w[c] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+          }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t e[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t nan = ((e[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a bit a NaN
-              any |= nan != 0;
-              e[i] = zero ? 0 : e[i] & ~((nan >> 7) * 0xFF);
-            }
-            w[c] = make_uint4(e[0], e[1], e[2], e[3]);
+            const int at = 2 * (c0 + c);  // 16-byte place in the 16-bit row, 8 of them a half
+            uint8_t* half = dst + (at >> 3) * (128 * 128);
+            *reinterpret_cast<uint4*>(half + (((at & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].x, w[c].y);
+            *reinterpret_cast<uint4*>(half + ((((at + 1) & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].z, w[c].w);
           }
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = 2 * (c0 + c);  // 16-byte place in the 16-bit row, 8 of them a half
-          uint8_t* half = dst + (at >> 3) * (128 * 128);
-          *reinterpret_cast<uint4*>(half + (((at & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].x, w[c].y);
-          *reinterpret_cast<uint4*>(half + ((((at + 1) & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].z, w[c].w);
-        }
+        if (any && check && !zero) record_bad<SHAPED>(a, it, k, u, sh, piece, row);
       }
-      if (any && check && !zero) record_bad<SHAPED>(a, it, k, u, sh, piece, row);
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sh.empty[from]);
         mbar_arrive(&sh.clean[to]);
       }
-      if (++to == S::kReady) { to = 0; to_phase ^= 1; }
     }
   }
 }
@@ -778,14 +788,22 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Scores of a block, from products to units of log2, capped and with their bias.  tanh x = 1 - 2 / (1 + e^2x): off by some
-// 2^-21 of the cap wherever x lies (tanh.approx is off by 2^-11).  The bias takes the distance as a whole number, so that
-// it is exact next to the row's own key whatever the slope.
+// cap tanh(s / cap), s and cap in units of log2; of_cap = 2 / softcap, so that e^2x is 2^(s of_cap).  tanh x = 1 - 2 / (1 +
+// e^2x) is off by some 2^-22 of the cap wherever x lies (tanh.approx by 2^-11), too much of a small x: below 1/4 the series
+// to x^9, off by 2^-26 of tanh x.
+__device__ __forceinline__ float capped(float s, float cap, float of_cap) {
+  const float y = s * of_cap, x = y * 0.34657359028f, z = x * x;  // y = 2 x log2 e
+  const float far = fmaf(rcp(1.f + ex2(y)), -2.f * cap, cap);
+  const float near = cap * fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 0.021869489f, -0.053968254f), 0.13333333f), -0.33333333f), x);
+  return fabsf(x) < 0.25f ? near : far;
+}
+// Scores of a block, from products to units of log2, capped and with their bias, which takes the distance as a whole
+// number, so that it is exact next to the row's own key whatever the slope.
 __device__ __forceinline__ void shape_scores(const AttendArgs& a, const Item& it, const Block& k, int place, uint64_t mask,
                                              float slope, float cap, float to_cap, float to_log2, float* s) {
   if (a.softcap > 0.f) {
 #pragma unroll
-    for (int c = 0; c < BN; ++c) s[c] = fmaf(rcp(1.f + ex2(s[c] * to_cap)), -2.f * cap, cap);
+    for (int c = 0; c < BN; ++c) s[c] = capped(s[c] * to_log2, cap, to_cap);
   } else {
 #pragma unroll
     for (int c = 0; c < BN; ++c) s[c] *= to_log2;
@@ -860,7 +878,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       }
     }
     cap = a.softcap * kLog2e;
-    to_cap = a.softcap > 0.f ? 2.f * to_log2 / a.softcap : 0.f;
+    to_cap = a.softcap > 0.f ? 2.f / a.softcap : 0.f;
     if (a.softcap > 0.f || a.slope) scale = 1.f;
   }
   const bool warp_live = __any_sync(~0u, live);
@@ -1105,9 +1123,22 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
 // Where this CTA's part of the line begins; block 0 leaves the requests' places to the join.
 template <int THREADS, bool SHAPED>
 __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
-  const int t = threadIdx.x, items = a.plan.tiles_b * a.c.kv_heads;
-  if (!a.plan.cut) {  // an item, whole
+  const AttendPlan& p = a.plan;
+  const int t = threadIdx.x, items = p.tiles_b * a.c.kv_heads;
+  if (!p.cut) {  // an item, whole
     if (t == 0) sh.line = Line{0, INT64_MAX, 0, (int)(blockIdx.x / items), (int)(blockIdx.x % items)};
+    return;
+  }
+  const uint32_t ca = cost_a(a);
+  // packed items on a line of their own, before the CTAs of few rows
+  const int cta = (int)blockIdx.x - p.split, ctas = (int)gridDim.x - p.split;
+  if (cta < 0) {
+    const int64_t lo = blockIdx.x * p.chunk_a, end = (int64_t)p.items_a * ca;
+    const int k = (int)(lo / ca);
+    if (t == 0) {
+      a.line[a.batch + 1 + blockIdx.x] = -1;
+      sh.line = lo < end ? Line{lo, min(lo + p.chunk_a, end), (int64_t)k * ca, -1, k} : Line{lo, lo, end, a.batch, 0};
+    }
     return;
   }
   const int lane = t & 31, warp = t >> 5;
@@ -1122,8 +1153,7 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  const uint32_t ca = cost_a(a);
-  const int64_t ta = (int64_t)a.plan.items_a * ca;
+  const int64_t ta = p.split ? 0 : (int64_t)p.items_a * ca;
   int64_t start = ta + upto - sum, total = ta;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
@@ -1131,17 +1161,17 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
     total += sums[w];
   }
   // at least a block's length, so that every CTA between the first and the last of an item holds a piece of it
-  const int64_t chunk = max((total + gridDim.x - 1) / gridDim.x, (int64_t)max(a.plan.step_a, a.plan.step_b));
-  const int64_t lo = blockIdx.x * chunk;
+  const int64_t chunk = max((total + ctas - 1) / ctas, (int64_t)(p.split ? p.step_b : max(p.step_a, p.step_b)));
+  const int64_t lo = cta * chunk;
   if (t == 0) {
-    if (blockIdx.x == 0) a.line[a.batch] = chunk;
+    if (cta == 0) a.line[a.batch] = chunk;
     a.line[a.batch + 1 + blockIdx.x] = -1;
     const int k = lo < ta ? (int)(lo / ca) : 0;
     if (lo < ta) sh.line = Line{lo, lo + chunk, (int64_t)k * ca, -1, k};
     if (lo >= total) sh.line = Line{lo, lo, total, a.batch, 0};
   }
   const bool here = lo >= ta && lo >= start && lo < start + sum;
-  if (here || blockIdx.x == 0) {
+  if (here || cta == 0) {
     int64_t at = start;
     for (int b = b0; b < b1; ++b) {
       const uint32_t cb = cost_b(a, blocks_of<SHAPED>(a, ctx_of(a, b)));
@@ -1150,11 +1180,19 @@ __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
         const int k = (int)((lo - at) / cb);
         sh.line = Line{lo, lo + chunk, at + (int64_t)k * cb, b, k};
       }
-      if (blockIdx.x == 0) a.line[b] = at;
+      if (cta == 0) a.line[b] = at;
       at += c;
     }
   }
 }
+
+}  // namespace
+}  // namespace graft
+
+#include "kv_few.cuh"
+
+namespace graft {
+namespace {
 
 // EIGHT: an 8-bit cache; SHAPED: capped, windowed or biased scores.
 template <typename T, int D, int L, bool EIGHT, bool SHAPED>
@@ -1166,14 +1204,18 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
   Bars& sh = *reinterpret_cast<Bars*>(base + S::kBars);
   const int warp = threadIdx.x >> 5;
   grid_dependents_launch();
+  if (EIGHT && a.plan.few && (int)blockIdx.x >= a.plan.split) {
+    few_cta<T, D, SHAPED>(a, sh, base, &kmap, &vmap);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], L);
-      mbar_init(&sh.empty[i], EIGHT ? 4 : 1);
+      mbar_init(&sh.empty[i], EIGHT ? kTeamWarps : 1);
     }
     for (int i = 0; i < S::kReady; ++i) {
       mbar_init(&sh.dirty[i], 1);
-      mbar_init(&sh.clean[i], EIGHT ? 4 : 3 - L);
+      mbar_init(&sh.clean[i], EIGHT ? kTeamWarps : 3 - L);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); }

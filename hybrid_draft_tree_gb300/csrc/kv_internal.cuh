@@ -71,6 +71,10 @@ struct AttendPlan {
   int32_t tile;              // rows of a tile: the most whole groups in 128
   int32_t fixed_a, fixed_b, step_a, step_b;  // cost of an item before its first block, and of a block
   int64_t rows;              // query rows times query heads
+  // An 8-bit cache and at most 16 rows a request and head: tiles of 8 rows (1 or 2; else 0) on the CTAs from `split` on;
+  // those before take the packed items, `chunk_a` of their line each.
+  int32_t few, split;
+  int64_t chunk_a;
 };
 
 struct AttendArgs {
