@@ -329,7 +329,7 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->line), ((size_t)cfg->max_batch + 1 + h->num_sms) * 8);
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ENOMEM; }
   e = cudaMemset(h->err, 0, 16);
-  if (e == cudaSuccess) e = graft::prepare_kv_attend();
+  if (e == cudaSuccess) e = graft::prepare_kv_attend(c.eight != 0);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ECUDA; }
   *out = h;

@@ -148,11 +148,17 @@ cudaError_t join(const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t prepare_kv_attend() {
-  cudaError_t e = prepare_form<false, false>();
-  if (e == cudaSuccess) e = prepare_kv_attend_shaped();
-  if (e == cudaSuccess) e = prepare_kv_attend_eight();
-  return e;
+const AttendForm kAttendPlain = {prepare_form<false, kPlain>, launch_form<false, kPlain>};
+
+namespace {
+const AttendForm* const kForms[2][4] = {{&kAttendPlain, &kAttendWindowed, &kAttendCapped, &kAttendBiased},
+                                        {&kAttendEightPlain, &kAttendEightWindowed, &kAttendEightCapped, &kAttendEightBiased}};
+}  // namespace
+
+cudaError_t prepare_kv_attend(bool eight) {
+  for (const AttendForm* f : kForms[eight])
+    if (const cudaError_t e = f->prepare()) return e;
+  return cudaSuccess;
 }
 
 int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int64_t)num_sms * 256; }
@@ -241,10 +247,8 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
 
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s) {
-  const bool shaped = a.softcap > 0.f || a.window > 0 || a.slope;
-  cudaError_t e = a.c.eight ? launch_kv_attend_eight(a, qmap, kmap, vmap, dtype, shaped, s)
-                  : shaped  ? launch_kv_attend_shaped(a, qmap, kmap, vmap, dtype, s)
-                            : launch_form<false, false>(a, qmap, kmap, vmap, dtype, s);
+  const int form = a.slope ? kBiased : a.softcap > 0.f ? kCapped : a.window > 0 ? kWindowed : kPlain;
+  const cudaError_t e = kForms[a.c.eight != 0][form]->launch(a, qmap, kmap, vmap, dtype, s);
   if (e != cudaSuccess || !a.plan.cut) return e;
   if (a.c.dim == 128) return dtype == GRAFT_BF16 ? join<__nv_bfloat16, 128>(a, s) : join<__half, 128>(a, s);
   return dtype == GRAFT_BF16 ? join<__nv_bfloat16, 64>(a, s) : join<__half, 64>(a, s);

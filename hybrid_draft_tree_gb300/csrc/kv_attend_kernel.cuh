@@ -111,6 +111,11 @@ struct Item {
 };
 constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 
+// What becomes of scores, a kernel each (what the loop over the blocks does not use costs it registers and instruction
+// fetches: 19 x 61 behind 2048 under a window takes 41 us in a kernel of its own, 45 in one that can do all of it).  Each can
+// do what those before it can; windows are in all but the first.
+constexpr int kPlain = 0, kWindowed = 1, kCapped = 2, kBiased = 3;
+
 // The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
 // `fixed` units before its first block's.  An item is shorter than 2^32 units: prefix, context and tree together are below
 // 2^31 keys (graft_kv_attend), so its key blocks below 2^24 + 2, of at most 152 units.
@@ -122,13 +127,13 @@ struct Line {
 
 // With a window (items are not packed then): the whole blocks before the first key that the root sees.  Slots sit one after
 // the other behind the context, so no slot sees an earlier one.
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ int skip_of(const AttendArgs& a, int ctx) {
   const int low = SHAPED && a.window ? a.prefix_len + ctx - a.window + 1 : 0;
   if (low <= 0) return 0;
   return low < a.prefix_len ? low / BN : (a.prefix_len + BN - 1) / BN + (low - a.prefix_len) / BN;
 }
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ int blocks_of(const AttendArgs& a, int ctx) {
   return (a.plan.packed ? 0 : (a.prefix_len + BN - 1) / BN) + (ctx + a.slots + BN - 1) / BN - skip_of<SHAPED>(a, ctx);
 }
@@ -141,7 +146,7 @@ __device__ __forceinline__ uint32_t cost_b(const AttendArgs& a, int blocks) {
 }
 
 // Walks the pieces of a CTA.
-template <bool SHAPED>
+template <int SHAPED>
 class Pieces {
  public:
   __device__ Pieces(const AttendArgs& a, const Line& line) : a_(a), line_(line), at_(line.at), b_(line.b), k_(line.k) {}
@@ -217,9 +222,10 @@ struct Block {
   int base, valid;
   int place;            // position of the first
 };
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ Block block_of(const AttendArgs& a, const Item& it, int j) {
-  const int x = (SHAPED ? it.skip : 0) + it.first + j;
+  // with slopes the nearest keys first: their scores are the largest, so that bases are set once
+  const int x = (SHAPED ? it.skip : 0) + it.first + (SHAPED == kBiased ? it.blocks - 1 - j : j);
   Block k;
   k.prefix = x < it.np;
   k.base = (k.prefix ? x : x - it.np) * BN;
@@ -291,19 +297,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // ---- warp 8, and 10 with small pages: keys and values into the ring ----------------------------------------------
 // L of them: a copy takes its warp some 75 cycles to issue.  Each says its own bytes of a tile to the tile's barrier, so a
 // phase ends when both have spoken and all has landed, and neither can pass the other by a phase.
-// Tile t of a piece of n blocks of an 8-bit cache, in the order that products take them, so that three of them are enough:
-// K0 K1 V0 K2 V1 ... V(n-1).  Its block, times 2, plus 1 for values.  16-bit tiles come as K0 V0 K1 V1 ...
-template <bool EIGHT>
-__device__ __forceinline__ int tile_of(int t, int n) {
-  if (!EIGHT) return t;
-  if (t == 0) return 0;
-  if (t == 2 * n - 1) return t;
+// Tiles of a piece come as K0 V0 K1 V1 ..., but of an 8-bit cache with one row tile an item in the order in which products
+// take them, K0 K1 V0 K2 V1 ... V(n-1) of n blocks: few of them are held as 16-bit numbers at a time.  The block of tile t,
+// times 2, plus 1 for values; and the places of a block's keys and values.
+__device__ __forceinline__ int tile_of(bool ahead, int t, int n) {
+  if (!ahead || t == 0 || t == 2 * n - 1) return t;
   return t & 1 ? t + 1 : t - 1;
 }
-__device__ __forceinline__ int keys_at(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int values_at(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
+__device__ __forceinline__ int keys_at(bool ahead, int j) { return ahead && j > 0 ? 2 * j - 1 : 2 * j; }
+__device__ __forceinline__ int values_at(bool ahead, int j, int n) { return ahead && j + 1 < n ? 2 * j + 2 : 2 * j + 1; }
 
-template <int D, int L, bool EIGHT, bool SHAPED>
+template <int D, int L, bool EIGHT, int SHAPED>
 __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
                           const CUtensorMap* vmap) {
   using S = Smem<D, EIGHT>;
@@ -357,7 +361,7 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
     };
     int next = page_of(0), last = -1, before = -1;  // pages of the keys to come, of the last ones, of those before
     for (int x = 0; x < 2 * it.blocks && ok; ++x) {
-      const int tile = tile_of<EIGHT>(x, it.blocks), j = tile >> 1, v = tile & 1;
+      const int tile = tile_of(EIGHT && !two, x, it.blocks), j = tile >> 1, v = tile & 1;
       if (x == 2 * q_at) ok = queries();
       if (!ok) break;
       if (!v) {
@@ -365,7 +369,7 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
         last = next;
         if (j + 1 < it.blocks) next = page_of(j + 1);
       }
-      const int from = EIGHT && v && j + 1 < it.blocks ? before : last;
+      const int from = EIGHT && !two && v && j + 1 < it.blocks ? before : last;
       const int stage = loads % S::kStages;
       ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
       ok = __all_sync(~0u, ok);
@@ -408,7 +412,7 @@ __device__ void drain_copies(Bars& sh) {
 // Rows of the block with key 0 at k.place: those before `unseen` no row of the item sees, neither those from k.valid on;
 // those before `edge`, and from `tree` on, some rows see and others do not.
 struct Unseen { int unseen, edge, tree; };
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ Unseen unseen_of(const AttendArgs& a, const Item& it, const Block& k) {
   Unseen u{0, 0, k.prefix ? k.valid : min(max(it.ctx - k.base, 0), k.valid)};
   if (SHAPED && a.window) {
@@ -418,13 +422,13 @@ __device__ __forceinline__ Unseen unseen_of(const AttendArgs& a, const Item& it,
   return u;
 }
 // A row whose value is not finite everywhere: a slot of the tree, or a key that some windows hold.
-template <bool SHAPED>
+template <int SHAPED>
 __device__ __forceinline__ void record_bad(const AttendArgs& a, const Item& it, const Block& k, const Unseen& u, Bars& sh, int piece, int row) {
   if (!SHAPED || row >= u.tree) atomicOr(&sh.bad[piece & 7], 1ull << (k.base + row - it.ctx));
   else atomicOr(&sh.bad_edge[piece & 7], 1ull << (k.place + row - edge_begin(a, it)));
 }
 
-template <typename T, int D, int L, bool SHAPED>
+template <typename T, int D, int L, int SHAPED>
 __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
   using S = Smem<D, false>;
   constexpr int kFirst = L == 2 ? kCleanWarp : kSpareWarp, kCleaners = (kCleanWarp + 1 - kFirst) * 32;
@@ -506,7 +510,7 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {  // 8 numbers
 // the products), of which there are then as many under way.
 constexpr int kTeams = 2, kTeamWarps = 2;
 
-template <typename T, int D, bool SHAPED>
+template <typename T, int D, int SHAPED>
 __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring, uint8_t* products) {
   using S = Smem<D, true>;
   constexpr int kChunks = D / 16, kRows = kTeamWarps * 32;  // 16-byte places of a row; rows that a team takes at a time
@@ -517,7 +521,7 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
   Item it;
   for (; pieces.next(it); before += 2 * it.blocks, ++piece) {
     for (int x = (team + kTeams - before % kTeams) % kTeams; x < 2 * it.blocks; x += kTeams) {
-      const int tile = tile_of<true>(x, it.blocks), v = tile & 1, number = before + x;
+      const int tile = tile_of(it.nt == 1, x, it.blocks), v = tile & 1, number = before + x;
       const int from = number % S::kStages, to = number % S::kReady;
       Block k{};
       Unseen u{};
@@ -586,7 +590,7 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
 // the scores of a group's next block may follow its O += P V at once, although they overwrite P.
 // What it does between products is on every unit's path, so it keeps the ring's places instead of computing them, and
 // waits once for what both groups use.
-template <typename T, int D, bool EIGHT, bool SHAPED>
+template <typename T, int D, bool EIGHT, int SHAPED>
 __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring) {
   using S = Smem<D, EIGHT>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -618,10 +622,16 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
     // masked blocks: the prefix's last when part full, and the request's own from where the tree begins
     const int part_full = !(a.prefix_len & (BN - 1)) ? -1 : it.np - 1 - it.first - (SHAPED ? it.skip : 0);
     const int tree = it.b < 0 ? INT32_MAX : it.np + it.ctx / BN - it.first - (SHAPED ? it.skip : 0);
+    // ... and, up to this one, where windows begin
+    int edge = 0;
+    if (SHAPED && a.window) {
+      const int end = edge_end(a, it);
+      if (end > 0) edge = (end <= a.prefix_len ? (end + BN - 1) / BN : it.np + (end - a.prefix_len + BN - 1) / BN) - it.first - it.skip;
+    }
     if (EIGHT) {
       kj = vj = 0;
       place(before, ks, kp);
-      place(before + values_at(0, it.blocks), vs, vp);
+      place(before + values_at(!two, 0, it.blocks), vs, vp);
     }
     // unit u is group u & 1 on key block u >> 1 (two tiles) or u (one)
     auto qk = [&](int t) -> bool {
@@ -637,7 +647,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       if (!two || t) {
         tc::commit(&free[ks]);
         if (EIGHT) {
-          place(before + keys_at(++kj), ks, kp);
+          place(before + keys_at(!two, ++kj), ks, kp);
         } else {
           ks += 2;
           if (ks >= S::kStages) { ks -= S::kStages; kp ^= 1; }
@@ -658,8 +668,9 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       if (!ok) break;
       if (!two || t == 0) {
         ok = wait_bar(sh, a, &ready[vs], vp);
-        const int j = two ? u >> 1 : u;
-        if (!EIGHT && ok && (SHAPED ? block_of<SHAPED>(a, it, j).masked : j >= tree || j == part_full)) {
+        int j = two ? u >> 1 : u;
+        if (SHAPED == kBiased) j = it.blocks - 1 - j;
+        if (!EIGHT && ok && (j >= tree || j == part_full || (SHAPED && j < edge))) {
           ok = wait_bar(sh, a, &sh.clean[vs], (cleaned >> vs) & 1);
           cleaned ^= 1u << vs;
         }
@@ -676,7 +687,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       if (!two || t) {
         tc::commit(&free[vs]);
         if (EIGHT) {
-          place(before + values_at(++vj, it.blocks), vs, vp);
+          place(before + values_at(!two, ++vj, it.blocks), vs, vp);
         } else {
           vs += 2;
           if (vs >= S::kStages) { vs -= S::kStages; vp ^= 1; }
@@ -788,32 +799,71 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap tanh(s / cap), s and cap in units of log2; of_cap = 2 / softcap, so that e^2x is 2^(s of_cap).  tanh x = 1 - 2 / (1 +
-// e^2x) is off by some 2^-22 of the cap wherever x lies (tanh.approx by 2^-11), too much of a small x: below 1/4 the series
-// to x^9, off by 2^-26 of tanh x.
-__device__ __forceinline__ float capped(float s, float cap, float of_cap) {
-  const float y = s * of_cap, x = y * 0.34657359028f, z = x * x;  // y = 2 x log2 e
-  const float far = fmaf(rcp(1.f + ex2(y)), -2.f * cap, cap);
-  const float near = cap * fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 0.021869489f, -0.053968254f), 0.13333333f), -0.33333333f), x);
-  return fabsf(x) < 0.25f ? near : far;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return reinterpret_cast<float2&>(d);
 }
-// Scores of a block, from products to units of log2, capped and with their bias, which takes the distance as a whole
-// number, so that it is exact next to the row's own key whatever the slope.
-__device__ __forceinline__ void shape_scores(const AttendArgs& a, const Item& it, const Block& k, int place, uint64_t mask,
-                                             float slope, float cap, float to_cap, float to_log2, float* s) {
-  if (a.softcap > 0.f) {
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// cap tanh(x), x = s / softcap and cap in units of log2, as factors of a product: x = s f, cap tanh(x) = s g tanh(x) / x.
+// Small x: tanh(x) / x by a polynomial in x^2 (fitted to |x| <= 1/2, off by 2^-25 of it).  Others: 1 - 2 / (1 + e^2x), off by
+// some 2^-22 of the cap wherever x lies, which at a half of it and above is no more than such a score's own rounding steps
+// (tanh.approx is off by 2^-11).
+constexpr float kSmall = 0.5f, kTanh0 = 0.017135f, kTanh1 = -0.05298607f, kTanh2 = 0.13324779f, kTanh3 = -0.33333069f;
+__device__ __forceinline__ float capped(float s, float f, float g, float cap) {
+  const float x = s * f, z = x * x;
+  const float far = fmaf(rcp(1.f + ex2(x * (2.f * kLog2e))), -2.f * cap, cap);
+  const float near = s * g * fmaf(fmaf(fmaf(fmaf(kTanh0, z, kTanh1), z, kTanh2), z, kTanh3), z, 1.f);
+  return fabsf(x) <= kSmall ? near : far;
+}
+// A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
+// score; f^8 has to stay inside fp32), any other the exponential and one reciprocal for two scores, 1 / a = b / (a b): three
+// of the special-function unit's results for two of a plain block's.
+__device__ __forceinline__ void cap_scores(const AttendArgs& a, float g, float* s) {
+  const float cap = a.softcap * kLog2e, f = g / cap;
+  float top = 0.f;
 #pragma unroll
-    for (int c = 0; c < BN; ++c) s[c] = capped(s[c] * to_log2, cap, to_cap);
-  } else {
+  for (int c = 0; c < BN; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
+  if (__all_sync(~0u, top * f <= kSmall) && f > 0x1p-15f && f < 0x1p15f) {
+    const float f2 = f * f, f4 = f2 * f2;
+    const float2 c3 = both(g * (kTanh3 * f2)), c2 = both(g * (kTanh2 * f4)), c1 = both(g * (kTanh1 * f4 * f2)), c0 = both(g * (kTanh0 * f4 * f4));
 #pragma unroll
-    for (int c = 0; c < BN; ++c) s[c] *= to_log2;
+    for (int c = 0; c < BN; c += 2) {
+      const float2 v = make_float2(s[c], s[c + 1]), z = mul2(v, v);
+      const float2 p = mul2(fma2(fma2(fma2(fma2(c0, z, c1), z, c2), z, c3), z, both(g)), v);
+      s[c] = p.x;
+      s[c + 1] = p.y;
+    }
+    return;
   }
-  if (!a.slope) return;
+  const float2 to_e = both(f * (2.f * kLog2e));
+#pragma unroll
+  for (int c = 0; c < BN; c += 2) {
+    const float2 y = mul2(make_float2(s[c], s[c + 1]), to_e);
+    // beyond 2^60 the quotient is 0 in all of the cap's bits; the product of two stays inside fp32
+    const float2 e = add2(make_float2(ex2(min_nan(y.x, 60.f)), ex2(min_nan(y.y, 60.f))), both(1.f));
+    const float r = rcp(e.x * e.y) * (-2.f * cap);
+    s[c] = fmaf(r, e.y, cap);
+    s[c + 1] = fmaf(r, e.x, cap);
+  }
+}
+// The bias takes distances as whole numbers, from the block's last key on: it is exact next to the row's own key whatever
+// the slope, and no further off than the bias of the block's nearest key is rounded.
+__device__ __forceinline__ void bias_scores(const Item& it, const Block& k, int place, uint64_t mask, float slope, float factor, float* s) {
   const int d = k.prefix ? BN : it.ctx - k.base;  // keys before the tree
   if (d >= BN) {
-    const float at = (float)(k.place - place);
+    const float near = slope * (float)(k.place + (BN - 1) - place);
 #pragma unroll
-    for (int c = 0; c < BN; ++c) s[c] = fmaf(slope, at + (float)c, s[c]);
+    for (int c = 0; c < BN; c += 2) {
+      const float2 v = fma2(make_float2(s[c], s[c + 1]), both(factor), both(near));
+      s[c] = fmaf(slope, (float)(c - (BN - 1)), v.x);
+      s[c + 1] = fmaf(slope, (float)(c + 1 - (BN - 1)), v.y);
+    }
     return;
   }
   // slots lie as far apart as the row's mask has them
@@ -823,12 +873,12 @@ __device__ __forceinline__ void shape_scores(const AttendArgs& a, const Item& it
   float at = (float)(k.place + (d < 0 ? d + __popcll(d > -64 ? mask & ((1ull << -d) - 1) : mask) : 0) - place);
 #pragma unroll
   for (int c = 0; c < BN; ++c) {
-    s[c] = fmaf(slope, at, s[c]);
+    s[c] = fmaf(slope, at, s[c] * factor);
     at += (w[c >> 5] >> (c & 31)) & 1 ? 1.f : 0.f;
   }
 }
 
-template <typename T, int D, bool EIGHT, bool SHAPED>
+template <typename T, int D, bool EIGHT, int SHAPED>
 __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   using S = Smem<D, EIGHT>;
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
@@ -866,20 +916,14 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const uint64_t mask = live ? mask_of(a, row.token) : 0;
   // scores in units of log2; shaped ones get there before the softmax, whose own factor is 1 then
   const float to_log2 = a.scale * kLog2e * (EIGHT ? kv_scale(a.k_scale, it.head, a.err) : 1.f);
-  View view{0, 0, mask};
-  float slope = 0.f, cap = 0.f, to_cap = 0.f, scale = to_log2;
-  if (SHAPED) {
-    if (live) view = view_of(a, it, row.token, mask);
-    if (a.slope && live) {
-      slope = a.slope[row.head] * kLog2e;
-      if (!(fabsf(slope) < INFINITY)) {
-        slope = 0.f;
-        atomicOr(a.err, GRAFT_ERR_RULE);
-      }
+  const float scale = SHAPED >= kCapped ? 1.f : to_log2;
+  float slope = 0.f;
+  if (SHAPED == kBiased && live) {
+    slope = a.slope[row.head] * kLog2e;
+    if (!(fabsf(slope) < INFINITY)) {
+      slope = 0.f;
+      atomicOr(a.err, GRAFT_ERR_RULE);
     }
-    cap = a.softcap * kLog2e;
-    to_cap = a.softcap > 0.f ? 2.f / a.softcap : 0.f;
-    if (a.softcap > 0.f || a.slope) scale = 1.f;
   }
   const bool warp_live = __any_sync(~0u, live);
   const int units = it.nt == 2 ? it.blocks : (it.blocks + 1 - t) >> 1;
@@ -909,15 +953,20 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
       tc::wait_ld<BN>(s);
       if (D == 64) read_done();
-      if (SHAPED && (a.softcap > 0.f || a.slope)) shape_scores(a, it, k, view.place, mask, slope, cap, to_cap, to_log2, reinterpret_cast<float*>(s));
+      if (SHAPED == kCapped) cap_scores(a, to_log2, reinterpret_cast<float*>(s));
+      if (SHAPED == kBiased) {
+        if (a.softcap > 0.f) cap_scores(a, to_log2, reinterpret_cast<float*>(s));
+        bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
+      }
       if (k.masked) {
         // bit c: the row sees key c of the block
         uint64_t lo, hi;
+        const View view = SHAPED ? view_of(a, it, row.token, mask) : View{0, 0, mask};
         if (k.prefix) {
           lo = k.valid >= 64 ? ~0ull : (1ull << k.valid) - 1;
           hi = k.valid >= 128 ? ~0ull : k.valid > 64 ? (1ull << (k.valid - 64)) - 1 : 0;
         } else {
-          seen_keys(it.ctx - k.base, SHAPED ? view.mask : mask, lo, hi);
+          seen_keys(it.ctx - k.base, view.mask, lo, hi);
         }
         if (SHAPED && a.window && view.low > k.place) {  // a slot never precedes its place in the row's order
           const int cut = view.low - k.place;
@@ -1044,7 +1093,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
     if (D == 128) written();
     continue;
   }
-  const uint64_t bad = sh.bad[piece & 7] & (SHAPED ? view.mask : mask);
+  const View view = SHAPED ? view_of(a, it, row.token, mask) : View{0, 0, mask};
+  const uint64_t bad = sh.bad[piece & 7] & view.mask;
   // of the keys where the windows begin, those that the row sees
   uint64_t bad_edge = 0;
   if (SHAPED && a.window && mask) bad_edge = sh.bad_edge[piece & 7] & ~0ull << (view.low - edge_begin(a, it));
@@ -1121,7 +1171,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
 }
 
 // Where this CTA's part of the line begins; block 0 leaves the requests' places to the join.
-template <int THREADS, bool SHAPED>
+template <int THREADS, int SHAPED>
 __device__ void find_line(const AttendArgs& a, Bars& sh, int64_t* sums) {
   const AttendPlan& p = a.plan;
   const int t = threadIdx.x, items = p.tiles_b * a.c.kv_heads;
@@ -1195,7 +1245,7 @@ namespace graft {
 namespace {
 
 // EIGHT: an 8-bit cache; SHAPED: capped, windowed or biased scores.
-template <typename T, int D, int L, bool EIGHT, bool SHAPED>
+template <typename T, int D, int L, bool EIGHT, int SHAPED>
 __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
     k_kv_attend(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -1260,13 +1310,13 @@ static_assert(kSmem<64, false> <= 227 * 1024 && kSmem<128, false> <= 227 * 1024 
 // Small pages' copies take two warps where items have one tile and blocks little else to do (8 x 1 behind 700, pages of
 // 16: 12.6 us, 15.1 with one warp; 8 x 17 behind 300 + 600, heads of 64, pages of 32: 11.7 and 12.3); the ring's warps
 // are in the way of more work (64 x 17 behind 2048 + 777, pages of 16: 88 us, 85.5 with one warp).
-template <typename T, int D, bool EIGHT, bool SHAPED>
+template <typename T, int D, bool EIGHT, int SHAPED>
 cudaError_t launch_one(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   const bool two_loaders = a.c.page_size <= 32 && !a.plan.packed && a.plan.nt_b == 1;
   return launch_dependent(two_loaders ? k_kv_attend<T, D, 2, EIGHT, SHAPED> : k_kv_attend<T, D, 1, EIGHT, SHAPED>, dim3(a.plan.ctas),
                           dim3(kThreads<EIGHT>), kSmem<D, EIGHT>, s, a, qmap, kmap, vmap);
 }
-template <bool EIGHT, bool SHAPED>
+template <bool EIGHT, int SHAPED>
 cudaError_t launch_form(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, cudaStream_t s) {
   if (a.c.dim == 128)
     return dtype == GRAFT_BF16 ? launch_one<__nv_bfloat16, 128, EIGHT, SHAPED>(a, qmap, kmap, vmap, s)
@@ -1275,12 +1325,12 @@ cudaError_t launch_form(const AttendArgs& a, const CUtensorMap& qmap, const CUte
                              : launch_one<__half, 64, EIGHT, SHAPED>(a, qmap, kmap, vmap, s);
 }
 
-template <typename T, int D, bool EIGHT, bool SHAPED>
+template <typename T, int D, bool EIGHT, int SHAPED>
 cudaError_t prepare_one() {
   const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, 1, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
   return e != cudaSuccess ? e : cudaFuncSetAttribute(k_kv_attend<T, D, 2, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
 }
-template <bool EIGHT, bool SHAPED>
+template <bool EIGHT, int SHAPED>
 cudaError_t prepare_form() {
   cudaError_t e = prepare_one<__nv_bfloat16, 128, EIGHT, SHAPED>();
   if (e == cudaSuccess) e = prepare_one<__nv_bfloat16, 64, EIGHT, SHAPED>();

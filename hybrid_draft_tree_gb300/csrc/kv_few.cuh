@@ -56,7 +56,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 }
 
 // Blocks into the ring.
-template <int D, bool SHAPED>
+template <int D, int SHAPED>
 __device__ void few_load(const AttendArgs& a, Bars& sh, uint8_t* ring, const CUtensorMap* kmap, const CUtensorMap* vmap, int loader) {
   using S = FewSmem<D>;
   const int lane = threadIdx.x & 31, place = lane & 15, pages = BN >> a.c.page_shift;
@@ -105,7 +105,7 @@ __device__ void few_drain(Bars& sh) {
       mbar_wait_drain(&sh.full[n % S::kStages], (n / S::kStages) & 1);
 }
 
-template <typename T, int D, int NT, bool SHAPED>
+template <typename T, int D, int NT, int SHAPED>
 __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, float2* merge) {
   using S = FewSmem<D>;
   constexpr int kSteps = D / 16, kHalf = D / 64, kWords = D / 32;  // products over d; 64-byte parts of a key; words of a lane's values
@@ -180,7 +180,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
         slope[nt][i] = 0.f;
         if (SHAPED && on) {
           view[nt][i] = view_of(a, it, own.token, mask[nt][i]);
-          if (a.slope) {
+          if (SHAPED == kBiased) {
             slope[nt][i] = a.slope[own.head] * kLog2e;
             if (!(fabsf(slope[nt][i]) < INFINITY)) {
               slope[nt][i] = 0.f;
@@ -194,7 +194,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nt][s][i] = 0.f;
     }
-    const float cap = SHAPED ? a.softcap * kLog2e : 0.f, of_cap = SHAPED && a.softcap > 0.f ? 2.f / a.softcap : 0.f;
+    const float cap = SHAPED ? a.softcap * kLog2e : 0.f, of_cap = SHAPED && a.softcap > 0.f ? 1.f / cap : 0.f;
     bool ok = true;
     for (int j = 0; j < it.blocks && ok; ++j, ++number) {
       const int stage = number % S::kStages;
@@ -225,10 +225,10 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[nt][i] *= f[nt][i & 1];
-          if (SHAPED && a.softcap > 0.f) s[nt][i] = capped(s[nt][i], cap, of_cap);
+          if (SHAPED >= kCapped && a.softcap > 0.f) s[nt][i] = capped(s[nt][i], f[nt][i & 1] * of_cap, f[nt][i & 1], cap);
+          else s[nt][i] *= f[nt][i & 1];
         }
-      if (SHAPED && a.slope) {
+      if (SHAPED == kBiased) {
         const int d = k.prefix ? BN : it.ctx - k.base;  // keys before the tree
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -406,7 +406,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
   }
 }
 
-template <typename T, int D, bool SHAPED>
+template <typename T, int D, int SHAPED>
 __device__ void few_cta(const AttendArgs& a, Bars& sh, uint8_t* base, const CUtensorMap* kmap, const CUtensorMap* vmap) {
   using S = FewSmem<D>;
   const int warp = threadIdx.x >> 5;

@@ -144,18 +144,20 @@ __device__ __forceinline__ float kv_scale(const float* scale, int head, uint32_t
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t s);
-cudaError_t prepare_kv_attend();
+cudaError_t prepare_kv_attend(bool eight);
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int window, bool eight, bool capped, int num_sms);
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s);
-// its forms, a translation unit each
-cudaError_t prepare_kv_attend_shaped();
-cudaError_t launch_kv_attend_shaped(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                                    const CUtensorMap& vmap, int dtype, cudaStream_t s);
-cudaError_t prepare_kv_attend_eight();
-cudaError_t launch_kv_attend_eight(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                                   const CUtensorMap& vmap, int dtype, bool shaped, cudaStream_t s);
+// Its forms, a translation unit each: what becomes of scores (kPlain to kBiased) over a cache in the model's type and over an
+// 8-bit one.
+struct AttendForm {
+  cudaError_t (*prepare)();
+  cudaError_t (*launch)(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        int dtype, cudaStream_t s);
+};
+extern const AttendForm kAttendPlain, kAttendWindowed, kAttendCapped, kAttendBiased;
+extern const AttendForm kAttendEightPlain, kAttendEightWindowed, kAttendEightCapped, kAttendEightBiased;
 
 }  // namespace graft
