@@ -205,6 +205,12 @@ int append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q
   a.err = h->err;
   a.position = d_position; a.tokens = (int64_t)batch * slots; a.axes = h->axes;
   std::memcpy(a.pair_axis, h->pair_axis, sizeof a.pair_axis);
+  const int per = c.interleaved ? 4 : 8;
+  for (int i = 0; i < c.rot / 2; i += per) {
+    uint64_t axis = a.pair_axis[i];
+    for (int j = 1; j < per && i + j < c.rot / 2; ++j) axis = a.pair_axis[i + j] == axis ? axis : graft::kMixed;
+    a.piece_axis |= axis << 4 * (i / per);
+  }
   if (scales) { a.k_scale = scales->d_k_scale; a.v_scale = scales->d_v_scale; }
   const bool rows16 = !misaligned(d_k, 16) && !misaligned(d_v, 16) && k_stride % 8 == 0 && v_stride % 8 == 0 &&
                       (!d_q || (!misaligned(d_q, 16) && !misaligned(d_q_out, 16) && q_stride % 8 == 0 &&

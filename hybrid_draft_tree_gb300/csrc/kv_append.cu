@@ -26,34 +26,43 @@ struct Token {
   int32_t k_pos, q_pos;  // positions, -1: no key and value to write, no query
 };
 
-template <bool EXT>
-__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r) {
+// Positions of the caller's, of the query's token and of the key's: read once by the CTA, which takes one verdict on them.
+struct Given { int32_t q[8], k[8]; };
+__device__ __forceinline__ uint32_t read_given(const AppendArgs& a, int64_t q_row, int64_t k_row, bool has_k, Given& s) {
+  const int x = threadIdx.x;
+  bool q_in = true, k_in = true;
+  if (x < a.axes) {
+    s.q[x] = a.position[x * a.tokens + q_row];
+    q_in = (uint32_t)s.q[x] < (uint32_t)a.rope_len;
+  } else if (x >= 8 && x < 8 + a.axes && has_k) {
+    s.k[x - 8] = a.position[(x - 8) * a.tokens + k_row];
+    k_in = (uint32_t)s.k[x - 8] < (uint32_t)a.rope_len;
+  }
+  const bool all_q = __syncthreads_and(q_in), all_k = __syncthreads_and(k_in);
+  return (uint32_t)all_q | (uint32_t)all_k << 1;
+}
+
+// given: 4, or the verdict on positions of the caller's, which take the place of base + depth.
+__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r, uint32_t given = 4) {
   Token t{0, -1, -1};
   const int64_t first = (int64_t)b * a.slots;
   const int64_t ctx = a.ctx_len[b];
   const int64_t base = a.prefix_len + ctx;
   const int64_t limit = a.c.rot > 0 ? a.rope_len : INT32_MAX;
-  // positions of the caller's take the place of base + depth, all axes inside the table of angles
-  const bool given = EXT && a.position && a.c.rot > 0;
-  auto inside = [&](int64_t row, int64_t pos) {
-    if (!given) return pos < limit;
-    bool in = true;
-    for (int x = 0; x < a.axes; ++x) in = in && (uint32_t)a.position[x * a.tokens + row] < (uint32_t)a.rope_len;
-    return in;
-  };
   uint32_t bad = ctx < 0 || r >= a.slots ? GRAFT_ERR_RANGE : 0;
   if (ctx >= 0 && a.q) {
     const int32_t d = a.depth ? a.depth[first + i] : i;
-    if (d >= 0 && !inside(first + i, base + d)) bad = GRAFT_ERR_RANGE;
-    else if (d >= 0) t.q_pos = given ? 0 : (int32_t)(base + d);
+    const bool in = given == 4 ? base + d < limit : given & 1;
+    if (d >= 0 && !in) bad = GRAFT_ERR_RANGE;
+    else if (d >= 0) t.q_pos = given == 4 ? (int32_t)(base + d) : 0;
   }
   if (ctx >= 0 && r >= 0 && r < a.slots) {
     const int32_t d = a.depth ? a.depth[first + r] : r;
     if (d >= 0) {
       const int64_t at = ctx + i, p = at >> a.c.page_shift;
       const int32_t page = p < a.table_stride ? a.page_table[(int64_t)b * a.table_stride + p] : -1;
-      if (page >= 0 && page < a.c.num_pages && inside(first + r, base + d)) {
-        t.k_pos = given ? 0 : (int32_t)(base + d);
+      if (page >= 0 && page < a.c.num_pages && (given == 4 ? base + d < limit : given & 2)) {
+        t.k_pos = given == 4 ? (int32_t)(base + d) : 0;
         t.dst = page * a.c.page_stride + (at & (a.c.page_size - 1)) * a.c.token_stride;
       } else {
         bad = GRAFT_ERR_RANGE;
@@ -64,28 +73,25 @@ __device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r
   return t;
 }
 
-// Cosines and sines of N pairs from p on: of one row of the table, or, with positions of several axes, of the row of each
-// pair's own position (`row`: the token that has them).  Pairs of one axis take the same loads as without axes.
-template <int N, bool EXT>
-__device__ __forceinline__ void angles(const AppendArgs& a, int pos, int64_t row, int p, float* c, float* s) {
+// Cosines and sines of the N pairs of piece u: of one row of the table, or, with pairs of several axes in the piece, of the
+// row of each pair's own position.
+template <int N, bool AXES>
+__device__ __forceinline__ void angles(const AppendArgs& a, int pos, const int32_t* given, int u, float* c, float* s) {
   const int half = a.c.rot >> 1;
-  if (EXT && a.position) {
-    int axis = a.pair_axis[p];
-    bool one = true;
-#pragma unroll
-    for (int j = 1; j < N; ++j) one = one && a.pair_axis[p + j] == axis;
-    if (!one) {
+  if (AXES) {
+    const int axis = (int)(a.piece_axis >> 4 * u) & 15;
+    if (axis == kMixed) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float* cs = a.rope + (int64_t)a.position[a.pair_axis[p + j] * a.tokens + row] * a.c.rot + p + j;
+        const float* cs = a.rope + (int64_t)given[a.pair_axis[N * u + j]] * a.c.rot + N * u + j;
         c[j] = cs[0];
         s[j] = cs[half];
       }
       return;
     }
-    pos = a.position[axis * a.tokens + row];
+    pos = given[axis];
   }
-  const float* cs = a.rope + (int64_t)pos * a.c.rot + p;
+  const float* cs = a.rope + (int64_t)pos * a.c.rot + N * u;
 #pragma unroll
   for (int j = 0; j < N; j += 4) {
     const float4 x = *reinterpret_cast<const float4*>(cs + j), y = *reinterpret_cast<const float4*>(cs + half + j);
@@ -128,29 +134,45 @@ __device__ __forceinline__ void turn_pairs(const float* c, const float* s, float
 }
 
 // 8-bit caches: numbers over the head's scale, to the nearest e4m3 number (ties to even), at most 448 in magnitude.  The
-// quotient is a division, so that what is stored follows from the definition bit for bit; 1 x 32768 is as fast with a
-// product.
-__device__ __forceinline__ uint32_t codes(const float* f, float scale) {  // four, in their order
+// quotient is the correctly rounded one, so that what is stored follows from the definition bit for bit: with a correctly
+// rounded reciprocal a product is within an ulp of it, and q + (x - q scale) / scale from there is it (Markstein).  All of
+// that stays inside fp32 for scales from 2^-60 to 2^64 and quotients below 2^10, above which the result is 448 whatever the
+// last bit; other scales get there by a power of two, with x.  (1 x 32768: 160 us with a division for each.)
+struct Quotient {
+  float up, scale, inverse;
+  __device__ __forceinline__ explicit Quotient(float s) {
+    up = s < 0x1p-60f ? 0x1p100f : s > 0x1p60f ? 0x1p-64f : 1.f;
+    scale = s * up;
+    inverse = 1.f / scale;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    x *= up;
+    const float q = x * inverse;
+    // a zero keeps its sign
+    return fabsf(q) < 1024.f && q != 0.f ? fmaf(fmaf(-q, scale, x), inverse, q) : q;
+  }
+};
+__device__ __forceinline__ uint32_t codes(const float* f, const Quotient& by) {  // four, in their order
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(f[1], scale)), "f"(__fdiv_rn(f[0], scale)));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(f[3], scale)), "f"(__fdiv_rn(f[2], scale)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(by(f[1])), "f"(by(f[0])));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(by(f[3])), "f"(by(f[2])));
   return (uint32_t)hi << 16 | lo;
 }
-__device__ __forceinline__ uint8_t code(float x, float scale) {
+__device__ __forceinline__ uint8_t code(float x, const Quotient& by) {
   uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(__fdiv_rn(x, scale)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(by(x)));
   return (uint8_t)c;
 }
 
 // Any alignment and any rot_dim: one element, or one rotating pair (u < rot / 2).
-template <typename T, bool EXT, typename Put>
-__device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, int pos, int64_t row, int u, Put put) {
+template <typename T, bool AXES, typename Put>
+__device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, int pos, const int32_t* given, int u, Put put) {
   const int half = a.c.rot >> 1;
   if (u >= half) {
     put(u + half, Pair<T>::one(src[u + half]));
     return;
   }
-  if (EXT && a.position) pos = a.position[a.pair_axis[u] * a.tokens + row];
+  if (AXES) pos = given[a.pair_axis[u]];
   const float* cs = a.rope + (int64_t)pos * a.c.rot;
   const int i = a.c.interleaved ? 2 * u : u, j = a.c.interleaved ? 2 * u + 1 : u + half;
   const float x = Pair<T>::one(src[i]), y = Pair<T>::one(src[j]), c = cs[u], s = cs[half + u];
@@ -159,8 +181,8 @@ __device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, 
 }
 
 // One CTA a token.  A thread takes pieces of heads: those of q, of k and of v, in turn.
-template <typename T, bool HALVES, bool EXT>
-__global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
+template <typename T, bool HALVES, bool EIGHT, bool AXES>
+__global__ void __launch_bounds__(kThreads, EIGHT || AXES ? 8 : 0) k_kv_append(const __grid_constant__ AppendArgs a) {
   grid_dependents_launch();
   grid_dependency_wait();
   const int64_t n = blockIdx.x;
@@ -172,11 +194,13 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
   const int nq = a.q ? a.c.q_heads * ru : 0, nk = has_k ? a.c.kv_heads * ru : 0, nv = has_k ? a.c.kv_heads * vu : 0;
   const int64_t k_row = (int64_t)b * a.slots + r;
   constexpr int kPer = 2;  // pieces in flight
+  __shared__ Given s_given;
   Token t;
   bool located = false;
   for (int w0 = threadIdx.x; w0 < nq + nk + nv || !located; w0 += kPer * kThreads) {
     uint4 x[kPer], y[kPer];
     int kind[kPer], head[kPer], u[kPer];
+    float scale[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       int w = w0 + j * kThreads;
@@ -192,71 +216,82 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ 
       const int at = HALVES && kind[j] < 2 && u[j] >= pairs ? u[j] + pairs : u[j];
       x[j] = __ldcs(reinterpret_cast<const uint4*>(src) + at);
       if (HALVES && kind[j] < 2 && u[j] < pairs) y[j] = __ldcs(reinterpret_cast<const uint4*>(src) + u[j] + pairs);
+      if (EIGHT && kind[j] != 0) {  // the head's scale, on its way with the rows
+        const float* of = kind[j] == 1 ? a.k_scale : a.v_scale;
+        scale[j] = of ? of[head[j]] : 1.f;
+      }
     }
     if (!located) {
-      t = locate<EXT>(a, b, i, r);
+      t = AXES ? locate(a, b, i, r, read_given(a, n, k_row, has_k, s_given)) : locate(a, b, i, r);
       located = true;
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (kind[j] == 3 || (kind[j] == 0 ? t.q_pos : t.k_pos) < 0) continue;
-      const bool eight = EXT && a.c.eight && kind[j] != 0;
       const int64_t to = kind[j] == 0 ? n * a.q_out_stride + head[j] * dim : t.dst + head[j] * a.c.head_stride;
-      void* base = kind[j] == 0 ? a.q_out : kind[j] == 1 ? a.k_cache : a.v_cache;
-      const float scale = eight ? kv_scale(kind[j] == 1 ? a.k_scale : a.v_scale, head[j], a.err) : 1.f;
-      auto put = [&](int piece, const float* f) {
-        if (eight) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + to + 8 * piece) = make_uint2(codes(f, scale), codes(f + 4, scale));
-        else *reinterpret_cast<uint4*>(static_cast<T*>(base) + to + 8 * piece) = pack<T>(f);
-      };
-      auto keep = [&](int piece, const uint4& w) {  // as it is
-        if (eight) {
-          float f[8];
-          unpack<T>(w, f);
-          put(piece, f);
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<T*>(base) + to + 8 * piece) = w;
+      const int pos = kind[j] == 0 ? t.q_pos : t.k_pos;
+      const int32_t* given = kind[j] == 0 ? s_given.q : s_given.k;
+      float f[8], g[8], c[8], s[8];
+      if (EIGHT && kind[j] != 0) {
+        const Quotient by(checked_scale(scale[j], a.err));
+        uint8_t* base = static_cast<uint8_t*>(kind[j] == 1 ? a.k_cache : a.v_cache) + to;
+        auto put = [&](int piece, const float* f) { *reinterpret_cast<uint2*>(base + 8 * piece) = make_uint2(codes(f, by), codes(f + 4, by)); };
+        unpack<T>(x[j], f);
+        int at = u[j];
+        if (kind[j] == 1 && HALVES) {
+          if (u[j] < pairs) {
+            angles<8, AXES>(a, pos, given, u[j], c, s);
+            unpack<T>(y[j], g);
+            turn_halves(c, s, f, g);
+            put(u[j] + pairs, g);
+          } else {
+            at += pairs;
+          }
+        } else if (kind[j] == 1 && 8 * u[j] < a.c.rot) {
+          angles<4, AXES>(a, pos, given, u[j], c, s);
+          turn_pairs(c, s, f);
         }
-      };
-      if (kind[j] == 2) {
-        keep(u[j], x[j]);
+        put(at, f);
         continue;
       }
-      const int pos = kind[j] == 0 ? t.q_pos : t.k_pos;
-      const int64_t row = kind[j] == 0 ? n : k_row;
-      float f[8], g[8], c[8], s[8];
-      if (HALVES) {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(kind[j] == 0 ? a.q_out : kind[j] == 1 ? a.k_cache : a.v_cache) + to);
+      if (kind[j] == 2) {
+        out[u[j]] = x[j];
+      } else if (HALVES) {
         if (u[j] < pairs) {
-          angles<8, EXT>(a, pos, row, 8 * u[j], c, s);
+          angles<8, AXES>(a, pos, given, u[j], c, s);
           unpack<T>(x[j], f);
           unpack<T>(y[j], g);
           turn_halves(c, s, f, g);
-          put(u[j], f);
-          put(u[j] + pairs, g);
+          out[u[j]] = pack<T>(f);
+          out[u[j] + pairs] = pack<T>(g);
         } else {
-          keep(u[j] + pairs, x[j]);
+          out[u[j] + pairs] = x[j];
         }
-      } else if (8 * u[j] < a.c.rot) {
-        angles<4, EXT>(a, pos, row, 4 * u[j], c, s);
-        unpack<T>(x[j], f);
-        turn_pairs(c, s, f);
-        put(u[j], f);
       } else {
-        keep(u[j], x[j]);
+        if (8 * u[j] < a.c.rot) {
+          angles<4, AXES>(a, pos, given, u[j], c, s);
+          unpack<T>(x[j], f);
+          turn_pairs(c, s, f);
+          x[j] = pack<T>(f);
+        }
+        out[u[j]] = x[j];
       }
     }
   }
 }
 
 // The same by elements and rotating pairs, for any alignment and any rot_dim.
-template <typename T, bool EXT>
+template <typename T, bool EIGHT, bool AXES>
 __global__ void __launch_bounds__(kThreads) k_kv_append_elements(const __grid_constant__ AppendArgs a) {
   grid_dependents_launch();
   grid_dependency_wait();
   const int64_t n = blockIdx.x;
   const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
   const int r = a.rows ? a.rows[n] : i;
-  const Token t = locate<EXT>(a, b, i, r);
   const int64_t k_row = (int64_t)b * a.slots + r;
+  __shared__ Given s_given;
+  const Token t = AXES ? locate(a, b, i, r, read_given(a, n, k_row, r >= 0 && r < a.slots, s_given)) : locate(a, b, i, r);
   const int ru = dim - (a.c.rot >> 1);
   const int nq = t.q_pos >= 0 ? a.c.q_heads * ru : 0, nk = t.k_pos >= 0 ? a.c.kv_heads * ru : 0;
   const int nv = t.k_pos >= 0 ? a.c.kv_heads * dim : 0;
@@ -265,10 +300,10 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_elements(const __grid_co
     const int x = is_q ? w : is_v ? w - nq - nk : w - nq, head = x / (is_v ? dim : ru), u = x - head * (is_v ? dim : ru);
     const int64_t to = is_q ? n * a.q_out_stride + head * dim : t.dst + head * a.c.head_stride;
     void* base = is_q ? a.q_out : is_v ? a.v_cache : a.k_cache;
-    const bool eight = EXT && a.c.eight && !is_q;
-    const float scale = eight ? kv_scale(is_v ? a.v_scale : a.k_scale, head, a.err) : 1.f;
+    const bool eight = EIGHT && !is_q;
+    const Quotient by(eight ? kv_scale(is_v ? a.v_scale : a.k_scale, head, a.err) : 1.f);
     auto put = [&](int at, float f) {
-      if (eight) static_cast<uint8_t*>(base)[to + at] = code(f, scale);
+      if (eight) static_cast<uint8_t*>(base)[to + at] = code(f, by);
       else static_cast<T*>(base)[to + at] = Pair<T>::round(f);
     };
     if (is_v) {
@@ -278,23 +313,28 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_elements(const __grid_co
     } else {
       const T* src = is_q ? static_cast<const T*>(a.q) + n * a.q_stride + head * dim
                           : static_cast<const T*>(a.k) + k_row * a.k_stride + head * dim;
-      head_element<T, EXT>(a, src, is_q ? t.q_pos : t.k_pos, is_q ? n : k_row, u, put);
+      head_element<T, AXES>(a, src, is_q ? t.q_pos : t.k_pos, is_q ? s_given.q : s_given.k, u, put);
     }
   }
 }
 
-template <typename T, bool EXT>
+template <typename T, bool EIGHT, bool AXES>
 cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.batch * a.slots));
-  if (!a.vec) return launch_dependent(k_kv_append_elements<T, EXT>, grid, dim3(kThreads), 0, s, a);
-  return launch_dependent(a.c.interleaved ? k_kv_append<T, false, EXT> : k_kv_append<T, true, EXT>, grid, dim3(kThreads), 0, s, a);
+  if (!a.vec) return launch_dependent(k_kv_append_elements<T, EIGHT, AXES>, grid, dim3(kThreads), 0, s, a);
+  return launch_dependent(a.c.interleaved ? k_kv_append<T, false, EIGHT, AXES> : k_kv_append<T, true, EIGHT, AXES>, grid, dim3(kThreads), 0, s, a);
+}
+template <typename T>
+cudaError_t launch_type(const AppendArgs& a, cudaStream_t s) {
+  const bool axes = a.position && a.c.rot > 0;
+  if (a.c.eight) return axes ? launch<T, true, true>(a, s) : launch<T, true, false>(a, s);
+  return axes ? launch<T, false, true>(a, s) : launch<T, false, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-  if (a.c.eight || a.position) return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, true>(a, s) : launch<__half, true>(a, s);
-  return dtype == GRAFT_BF16 ? launch<__nv_bfloat16, false>(a, s) : launch<__half, false>(a, s);
+  return dtype == GRAFT_BF16 ? launch_type<__nv_bfloat16>(a, s) : launch_type<__half>(a, s);
 }
 
 }  // namespace graft

@@ -44,9 +44,12 @@ struct AppendArgs {
   int64_t tokens;           // batch * slots
   int32_t axes;
   uint8_t pair_axis[64];    // axis whose position turns a pair
+  uint64_t piece_axis;      // 4 bits for each 16-byte piece: the axis of its pairs (8 of halves, 4 of neighbours), or kMixed
   const float *k_scale, *v_scale;  // of 8-bit caches
   uint32_t* err;
 };
+
+constexpr int kMixed = 15;
 
 struct ReadArgs {
   KvLayout c;
@@ -134,12 +137,13 @@ struct Pair<__half> {
 };
 
 // A head's scale of an 8-bit cache; one that is no number above zero counts as 1.
-__device__ __forceinline__ float kv_scale(const float* scale, int head, uint32_t* err) {
-  if (!scale) return 1.f;
-  const float s = scale[head];
+__device__ __forceinline__ float checked_scale(float s, uint32_t* err) {
   if (s > 0.f && s < INFINITY) return s;
   atomicOr(err, GRAFT_ERR_RULE);
   return 1.f;
+}
+__device__ __forceinline__ float kv_scale(const float* scale, int head, uint32_t* err) {
+  return scale ? checked_scale(scale[head], err) : 1.f;
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
