@@ -180,16 +180,16 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 400, fixed_one = wide ? 280 : 450;
   int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
   const bool few = eight && R <= 16;
-  const int step_few = wide ? 40 : 25, fixed_few = 150;
+  const int step_few = R <= 8 ? (wide ? 47 : 29) : (wide ? 61 : 41), fixed_few = 280, item_few = R <= 8 ? 260 : 350, busy_few = wide ? 67 : 40;
   if (eight) {
-    two = wide ? 220 : 195;
-    one = wide ? 150 : 140;
+    two = wide ? 190 : 140;
+    one = wide ? 125 : 115;
     memory = wide ? 75 : 40;
     l2 = wide ? 40 : 20;
   }
   if (capped) {
-    two += wide ? 150 : 170;
-    one += wide ? 80 : 90;
+    two += wide ? 110 : 120;
+    one += wide ? 60 : 65;
   }
   AttendPlan best{};
   double best_t = 0;
@@ -231,11 +231,21 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
       t = whole;
     }
     if (few && packed) {
-      // the packed items' CTAs, as many as their share of the work
-      const double work_a = p.items_a * (p.fixed_a + (double)np * p.step_a);
-      p.split = std::min(num_sms - 1, std::max(1, (int)(num_sms * (work_a / work) + 0.5)));
-      const int64_t line = (int64_t)p.items_a * (p.fixed_a + (int64_t)np * p.step_a);
-      p.chunk_a = std::max((line + p.split - 1) / p.split, (int64_t)p.step_a);
+      // As many CTAs for the packed items as end with the others.  Beside CTAs that keep memory busy both are slower than
+      // alone: what the packed ones pay before and after their blocks was 10 to 27 us, an item of the others 2.6 us and 0.67 a
+      // block (64 x 1 behind 8192 + 1024: 59 us with 40 or 50 CTAs for the packed items, 74 with 30, 67 with 70; behind 2048 +
+      // 1024 50 with 40, 71 with 10; behind 8192 + 100 38 with 80, 58 with 30; behind 30000 + 500 76 with 100, 121 with 40).
+      const double line = p.items_a * (p.fixed_a + (double)np * p.step_a);
+      double best_end = 0;
+      for (int n = 1; n < num_sms; ++n) {
+        const double end = std::max(line / n + 2000, items_b * (item_few + (double)blocks * busy_few) / (num_sms - n));
+        if (best_end == 0 || end < best_end) {
+          best_end = end;
+          p.split = n;
+        }
+      }
+      t = best_end + join;
+      p.chunk_a = std::max(((int64_t)line + p.split - 1) / p.split, (int64_t)p.step_a);
     }
     if (best_t == 0 || t < best_t) {
       best_t = t;

@@ -201,9 +201,10 @@ class Pieces {
 
 struct Bars {
   unsigned long long full[8], empty[8], q_full[2], q_free[2], s_full[2], s_read[2], p_full[2], o_done[2], o_free;
-  unsigned long long dirty[8], clean[8], drain;
+  unsigned long long dirty[8], clean[8], q_ready[2], drain;
   unsigned long long bad[8];     // slots whose value holds an element that is not finite; pieces take turns
   unsigned long long bad_edge[8];  // such keys where the slots' windows begin, from the root's first on
+  uint8_t q_back[256];           // an 8-bit cache's queries: exponents of their rows' factors, of a shared tile by the piece's turn
   float2 ml[2][128];             // a shared tile's maxima and sums
   Line line;
   int few_loads[4];              // blocks up to and with the last that each copying warp of few rows asked for
@@ -485,25 +486,53 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
 }
 
 // ---- warps 12-15: an 8-bit cache's tiles as 16-bit ones ----------------------------------------------------------
-// A thread a row: 16 bytes at a time become 32 at the places where the products look for them.  e4m3 numbers are f16 and
-// bf16 numbers, so nothing is rounded; the head's scales join the scores and the results.  Values that no row may see are
-// made harmless on the way, as above; an e4m3 number that is not finite is a NaN.
-template <typename T>
+// A thread a row: 16 bytes at a time become 32 at the places where the products look for them.  e4m3 numbers are f16
+// numbers, so nothing is rounded; the head's scales join the scores and the results.  All products over an 8-bit cache are
+// of f16 numbers: the step to bf16 takes three more instructions a pair (two tiles of 128 rows 2.26 us a block, 1.9 with f16).
+// Values that no row may see are made harmless on the way, as above; an e4m3 number that is not finite is a NaN.
 __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {  // 8 numbers
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint16_t two = (uint16_t)((i < 2 ? lo : hi) >> 16 * (i & 1));
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    if (std::is_same<T, __half>::value) {
-      w[i] = h;
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      w[i] = Pair<T>::put(f.x, f.y);
-    }
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w[i]) : "h"(two));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The power of two, as an exponent, that brings a row's largest magnitude next to 2^11: its bf16 numbers down to 2^-28 of
+// that stay exact as f16 ones.  Rows of zeros and such as are not finite stay as they are.
+__device__ __forceinline__ int up_exponent(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23);
+  return e == 0 || e == 255 ? 127 : min(max(265 - e, 1), 253);
+}
+__device__ __forceinline__ float power(int exponent) { return __uint_as_float((uint32_t)exponent << 23); }
+
+// bf16 queries as f16 ones, in place; a thread a row.
+template <int D>
+__device__ __forceinline__ void convert_query(uint8_t* tile, int row, uint8_t* back) {
+  auto at = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)); };
+  uint32_t most = 0;  // magnitudes compare as whole numbers
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = *at(c);
+    most = __vmaxu2(__vmaxu2(most, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  const float top = __uint_as_float(max(most << 16, most & 0xFFFF0000u));
+  const int up = up_exponent(top);
+  const float by = power(up);
+  *back = (uint8_t)(254 - up);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = *at(c);
+    uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = Pair<__nv_bfloat16>::get(e[i]);
+      e[i] = Pair<__half>::put(p.x * by, p.y * by);
+    }
+    *at(c) = make_uint4(e[0], e[1], e[2], e[3]);
+  }
 }
 
 // kTeams teams of warps take the tiles in turn: a tile's way through a warp is latency (a wait, loads, stores, the word to
@@ -511,7 +540,7 @@ __device__ __forceinline__ uint4 widen(uint32_t lo, uint32_t hi) {  // 8 numbers
 constexpr int kTeams = 2, kTeamWarps = 2;
 
 template <typename T, int D, int SHAPED>
-__device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring, uint8_t* products) {
+__device__ void convert_role(const AttendArgs& a, Bars& sh, uint8_t* q, const uint8_t* ring, uint8_t* products) {
   using S = Smem<D, true>;
   constexpr int kChunks = D / 16, kRows = kTeamWarps * 32;  // 16-byte places of a row; rows that a team takes at a time
   const int lane = threadIdx.x & 31, team = (threadIdx.x / 32 - kConvertWarp) / kTeamWarps;
@@ -520,7 +549,23 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
   Pieces<SHAPED> pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); before += 2 * it.blocks, ++piece) {
+    // A shared tile's queries are there first; those of two tiles come after the first blocks, of which three tiles can be
+    // made ready without them.
+    bool queries = std::is_same<T, __half>::value;
+    auto convert_queries = [&]() -> bool {
+      queries = true;
+      if (!__all_sync(~0u, wait_bar(sh, a, &sh.q_full[piece & 1], (piece >> 1) & 1))) return false;
+      const int tile = it.nt == 1 ? piece & 1 : 0;
+      for (int r = first + team * kRows; r < it.nt * 128; r += kTeams * kRows)
+        convert_query<D>(q + (tile + (r >> 7)) * S::kTile, r & 127, &sh.q_back[tile * 128 + r]);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_ready[piece & 1]);
+      return true;
+    };
+    if (!queries && it.nt == 1 && !convert_queries()) return;
     for (int x = (team + kTeams - before % kTeams) % kTeams; x < 2 * it.blocks; x += kTeams) {
+      if (!queries && x >= kTeams && !convert_queries()) return;
       const int tile = tile_of(it.nt == 1, x, it.blocks), v = tile & 1, number = before + x;
       const int from = number % S::kStages, to = number % S::kReady;
       Block k{};
@@ -569,8 +614,8 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
           for (int c = 0; c < 4; ++c) {
             const int at = 2 * (c0 + c);  // 16-byte place in the 16-bit row, 8 of them a half
             uint8_t* half = dst + (at >> 3) * (128 * 128);
-            *reinterpret_cast<uint4*>(half + (((at & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].x, w[c].y);
-            *reinterpret_cast<uint4*>(half + ((((at + 1) & 7) ^ (row & 7)) << 4)) = widen<T>(w[c].z, w[c].w);
+            *reinterpret_cast<uint4*>(half + (((at & 7) ^ (row & 7)) << 4)) = widen(w[c].x, w[c].y);
+            *reinterpret_cast<uint4*>(half + ((((at + 1) & 7) ^ (row & 7)) << 4)) = widen(w[c].z, w[c].w);
           }
         }
         if (any && check && !zero) record_bad<SHAPED>(a, it, k, u, sh, piece, row);
@@ -582,6 +627,7 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
         mbar_arrive(&sh.clean[to]);
       }
     }
+    if (!queries && !convert_queries()) return;
   }
 }
 
@@ -593,7 +639,7 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring,
 template <typename T, int D, bool EIGHT, int SHAPED>
 __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ring) {
   using S = Smem<D, EIGHT>;
-  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kBf16 = !EIGHT && std::is_same<T, __nv_bfloat16>::value;  // 8-bit caches: f16, and queries made so
   constexpr uint32_t kQK = tc::instr_desc(kBf16, 128, BN, false), kPV = tc::instr_desc(kBf16, 128, D, true);
   constexpr int kTile16 = S::kTile / 16;
   // With room for P beside S (D = 64) a group's next scores are computed as soon as it has read its last ones, while it
@@ -655,7 +701,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       }
       return true;
     };
-    ok = wait_bar(sh, a, &sh.q_full[piece & 1], (piece >> 1) & 1);
+    ok = wait_bar(sh, a, EIGHT && std::is_same<T, __nv_bfloat16>::value ? &sh.q_ready[piece & 1] : &sh.q_full[piece & 1], (piece >> 1) & 1);
     for (int u = 0; u < 2 && u < units && ok; ++u) ok = qk(u);
     for (int u = 0; u < units && ok; ++u) {
       const int t = u & 1;
@@ -824,8 +870,18 @@ __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
 // A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
 // score; f^8 has to stay inside fp32), any other the exponential and one reciprocal for two scores, 1 / a = b / (a b): three
 // of the special-function unit's results for two of a plain block's.
-__device__ __forceinline__ void cap_scores(const AttendArgs& a, float g, float* s) {
-  const float cap = a.softcap * kLog2e, f = g / cap;
+template <bool EIGHT>
+__device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, float* s) {
+  const float cap = a.softcap * kLog2e;
+  if (EIGHT) {  // rows have factors of their own: out of the way, so that the coefficients are the same in every thread
+#pragma unroll
+    for (int c = 0; c < BN; c += 2) {
+      const float2 v = mul2(make_float2(s[c], s[c + 1]), both(to_log2));
+      s[c] = v.x;
+      s[c + 1] = v.y;
+    }
+  }
+  const float g = EIGHT ? 1.f : to_log2, f = g / cap;
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < BN; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
@@ -881,6 +937,7 @@ __device__ __forceinline__ void bias_scores(const Item& it, const Block& k, int 
 template <typename T, int D, bool EIGHT, int SHAPED>
 __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   using S = Smem<D, EIGHT>;
+  using P = typename std::conditional<EIGHT, __half, T>::type;  // of the weights
   const int tid = threadIdx.x, t = tid >> 7, lane_row = tid & 127;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;   // tensor-memory lanes of this warp
   const uint32_t tmem = sh.tmem + lanes;
@@ -915,7 +972,15 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const Row row = live ? row_of(a, it, r) : Row{0, 0};
   const uint64_t mask = live ? mask_of(a, row.token) : 0;
   // scores in units of log2; shaped ones get there before the softmax, whose own factor is 1 then
-  const float to_log2 = a.scale * kLog2e * (EIGHT ? kv_scale(a.k_scale, it.head, a.err) : 1.f);
+  bool ok = !dead;
+  float to_log2 = a.scale * kLog2e;
+  if (EIGHT) {
+    to_log2 *= kv_scale(a.k_scale, it.head, a.err);
+    if (std::is_same<T, __nv_bfloat16>::value && ok) {  // queries that were made f16
+      ok = __all_sync(~0u, wait_bar(sh, a, &sh.q_ready[piece & 1], (piece >> 1) & 1));
+      if (ok) to_log2 *= power(sh.q_back[(it.nt == 2 ? t : piece & 1) * 128 + lane_row]);
+    }
+  }
   const float scale = SHAPED >= kCapped ? 1.f : to_log2;
   float slope = 0.f;
   if (SHAPED == kBiased && live) {
@@ -929,7 +994,6 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const int units = it.nt == 2 ? it.blocks : (it.blocks + 1 - t) >> 1;
   float m = live ? -INFINITY : 0.f;                 // lanes without a row never wait
   float2 l2 = make_float2(0.f, 0.f);
-  bool ok = !dead;
   for (int n = 0; n < units && ok; ++n) {
     const Block k = block_of<SHAPED>(a, it, it.nt == 2 ? n : 2 * n + t);
     ok = __all_sync(~0u, wait_bar(sh, a, &sh.s_full[t], scores++ & 1));
@@ -953,9 +1017,9 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
       tc::wait_ld<BN>(s);
       if (D == 64) read_done();
-      if (SHAPED == kCapped) cap_scores(a, to_log2, reinterpret_cast<float*>(s));
+      if (SHAPED == kCapped) cap_scores<EIGHT>(a, to_log2, reinterpret_cast<float*>(s));
       if (SHAPED == kBiased) {
-        if (a.softcap > 0.f) cap_scores(a, to_log2, reinterpret_cast<float*>(s));
+        if (a.softcap > 0.f) cap_scores<EIGHT>(a, to_log2, reinterpret_cast<float*>(s));
         bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
       }
       if (k.masked) {
@@ -1036,8 +1100,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
             y = make_float2(ex2(y.x), ex2(y.y));
             sum0 = add2(sum0, x);
             sum1 = add2(sum1, y);
-            p[i / 2] = Pair<T>::put(x.x, x.y);
-            p[i / 2 + 1] = Pair<T>::put(y.x, y.y);
+            p[i / 2] = Pair<P>::put(x.x, x.y);
+            p[i / 2 + 1] = Pair<P>::put(y.x, y.y);
           }
           tc::st16(p_at + c / 2, p);
         }
@@ -1268,7 +1332,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       mbar_init(&sh.clean[i], EIGHT ? kTeamWarps : 3 - L);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); mbar_init(&sh.q_ready[i], kTeams * kTeamWarps); }
     mbar_init(&sh.o_free, 8);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 8; ++i) sh.bad[i] = sh.bad_edge[i] = 0;
@@ -1292,7 +1356,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       if (tc::elect()) mma_role<T, D, EIGHT, SHAPED>(a, sh, base, base + S::kProducts);
       __syncwarp();
     } else if (EIGHT) {
-      if (warp >= kConvertWarp) convert_role<T, D, SHAPED>(a, sh, base + S::kRing, base + S::kProducts);
+      if (warp >= kConvertWarp) convert_role<T, D, SHAPED>(a, sh, base, base + S::kRing, base + S::kProducts);
     } else clean_role<T, D, L, SHAPED>(a, sh, base + S::kRing);
   }
   tc::fence_before();

@@ -14,8 +14,7 @@
 //
 // A warp keeps a base, a sum and O of its own for each row; the base moves when a score exceeds it by 2^12 (as in the other
 // kernel), so there is no exchange between lanes in the loop.  Warps are joined at the piece's end, in their order.
-// Queries are turned to f16 at a power of two that brings a row's largest near 2^11: bf16 numbers down to 2^-28 of it stay
-// exact.
+// bf16 queries become f16 ones as in the other kernel.
 #pragma once
 
 namespace graft {
@@ -118,31 +117,52 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) value[i] = warp * 16 + key_of(2 * t + (i & 1)) + 8 * (i >> 1);
   auto chunk = [](int row, int c) { return row * D + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4); };
+  uint64_t* const masks = reinterpret_cast<uint64_t*>(sh.ml[1]);  // of the piece's rows, for the joint
   int number = 0, piece = 0;
   Pieces<SHAPED> pieces(a, sh.line);
-  Item it;
-  for (; pieces.next(it); ++piece) {
-    const float to_log2 = a.scale * kLog2e * kv_scale(a.k_scale, it.head, a.err);
+  // With 8 rows the next piece and its queries are asked for before the last one's results are joined (what a piece costs
+  // beside its blocks is the way to these and back: 3.2 -> 1.6 us); with 16 there are no registers left for that (16 x 4
+  // behind 4096 + 1024: 34 us, 41 with it).
+  Item it, next;
+  uint2 raw[NT][kSteps];
+  float k_scale = 1.f, v_scale = 1.f;
+  auto fetch = [&]() -> bool {
+    if (!pieces.next(next)) return false;
+    k_scale = kv_scale(a.k_scale, next.head, a.err);
+    v_scale = kv_scale(a.v_scale, next.head, a.err);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      const bool live = r < next.rows;
+      const Row row = live ? row_of(a, next, r) : Row{0, 0};
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row.token * a.q_stride + row.head * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = 16 * (t + 4 * (s >> 2)) + 4 * (s & 3);
+        raw[nt][s] = make_uint2(0, 0);
+        if (live) {
+          if (a.q_map) raw[nt][s] = *reinterpret_cast<const uint2*>(src + d);
+          else raw[nt][s] = make_uint2(src[d] | src[d + 1] << 16, src[d + 2] | src[d + 3] << 16);
+        }
+      }
+    }
+    return true;
+  };
+  for (bool more = fetch(); more; ++piece) {
+    it = next;
+    const float to_log2 = a.scale * kLog2e * k_scale, to_value = v_scale;
     // rows 2t and 2t + 1 of a tile of 8, whose scores and results this lane holds; and row g, whose queries it holds
     uint32_t qf[NT][kSteps][2];
     float f[NT][2], m[NT][2], l[NT][2], slope[NT][2], o[NT][kSteps][4];
     uint64_t mask[NT][2];
     View view[NT][2];
+    if (tid < 16) masks[tid] = tid < it.rows ? mask_of(a, row_of(a, it, tid).token) : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      const bool live = r < it.rows;
-      const Row row = live ? row_of(a, it, r) : Row{0, 0};
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row.token * a.q_stride + row.head * D;
       float x[kSteps][4], top = 0.f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int d = 16 * (t + 4 * (s >> 2)) + 4 * (s & 3);
-        uint2 w = make_uint2(0, 0);
-        if (live) {
-          if (a.q_map) w = *reinterpret_cast<const uint2*>(src + d);
-          else w = make_uint2(src[d] | src[d + 1] << 16, src[d + 2] | src[d + 3] << 16);
-        }
+        const uint2 w = raw[nt][s];
         const float2 lo = Pair<T>::get(w.x), hi = Pair<T>::get(w.y);
         x[s][0] = lo.x; x[s][1] = lo.y; x[s][2] = hi.x; x[s][3] = hi.y;
         if (std::is_same<T, __half>::value) {
@@ -157,10 +177,9 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       if (!std::is_same<T, __half>::value) {
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const int e = (int)(__float_as_uint(top) >> 23);
-        const int up = e == 0 || e == 255 ? 127 : min(max(265 - e, 1), 253);
-        const float by = __uint_as_float((uint32_t)up << 23);
-        back = __uint_as_float((uint32_t)(254 - up) << 23);
+        const int up = up_exponent(top);
+        const float by = power(up);
+        back = power(254 - up);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           qf[nt][s][0] = Pair<__half>::put(x[s][0] * by, x[s][1] * by);
@@ -195,30 +214,49 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
         for (int i = 0; i < 4; ++i) o[nt][s][i] = 0.f;
     }
     const float cap = SHAPED ? a.softcap * kLog2e : 0.f, of_cap = SHAPED && a.softcap > 0.f ? 1.f / cap : 0.f;
-    bool ok = true;
-    for (int j = 0; j < it.blocks && ok; ++j, ++number) {
-      const int stage = number % S::kStages;
-      const Block k = block_of<SHAPED>(a, it, j);
-      ok = __all_sync(~0u, wait_bar(sh, a, &sh.full[stage], (number / S::kStages) & 1));
-      if (!ok) break;
-      const uint8_t *keys = ring + stage * S::kBlock, *values = keys + S::kCopied;
-      uint32_t kw[kHalf][2][4], vw[4][kWords];
+    // A block's words are read ahead: its keys under the softmax of the block before, its values under its own scores.
+    uint32_t kw[kHalf][2][4], vw[4][kWords];
+    auto wait_block = [&](int n) { return (bool)__all_sync(~0u, wait_bar(sh, a, &sh.full[n % S::kStages], (n / S::kStages) & 1)); };
+    auto load_keys = [&](int n) {
+      const uint8_t* keys = ring + n % S::kStages * S::kBlock;
 #pragma unroll
       for (int h = 0; h < kHalf; ++h) {
         load_words<4>(keys + chunk(key, t + 4 * h), kw[h][0]);
         load_words<4>(keys + chunk(key + 8, t + 4 * h), kw[h][1]);
       }
+    };
+    auto load_values = [&](int n) {
+      const uint8_t* values = ring + n % S::kStages * S::kBlock + S::kCopied;
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_words<kWords>(values + chunk(value[i], D == 128 ? g : g >> 1) + (D == 128 ? 0 : (g & 1) * 8), vw[i]);
-      float s[NT][4];
+    };
+    bool ok = wait_block(number);
+    if (ok) load_keys(number);
+    for (int j = 0; j < it.blocks && ok; ++j, ++number) {
+      const int stage = number % S::kStages;
+      const Block k = block_of<SHAPED>(a, it, j);
+      load_values(number);
+      // two sums, of every other product, so that a product waits for the one before the last
+      float s[NT][4], s1[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = s1[nt][i] = 0.f;
 #pragma unroll
       for (int x = 0; x < kSteps; ++x) {
         const uint32_t w0 = kw[x >> 2][0][x & 3], w1 = kw[x >> 2][1][x & 3];
         const uint32_t a0 = halves(w0), a1 = halves(w1), a2 = halves(w0 >> 16), a3 = halves(w1 >> 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][x][0], qf[nt][x][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(x & 1 ? s1[nt] : s[nt], a0, a1, a2, a3, qf[nt][x][0], qf[nt][x][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] += s1[nt][i];
+      if (j + 1 < it.blocks) {
+        ok = wait_block(number + 1);
+        if (!ok) break;
+        load_keys(number + 1);
       }
       // s[nt][2 c + i]: key c of the lane's two, row i
 #pragma unroll
@@ -317,6 +355,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[stage]);
     }
+    if (NT == 1) more = ok && fetch();
     // the warps' results, by lane and product: element 2 x (+ 1) of the lane's D / 8, of row 2t (+ 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -341,7 +380,6 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       sh.bad[(piece + 6) & 7] = 0;
       if (SHAPED) sh.bad_edge[(piece + 6) & 7] = 0;
     }
-    const float v_scale = kv_scale(a.v_scale, it.head, a.err);
     for (int x = tid; x < it.rows * (D / 2); x += kFewWarps * 32) {
       const int r = x / (D / 2), d = 2 * (x - r * (D / 2)), nt = r >> 3;
       constexpr int kRun = D / 8;  // elements that a lane holds side by side
@@ -361,9 +399,9 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
         acc.y += v.y * by;
       }
       const Row row = row_of(a, it, r);
-      const uint64_t own = mask_of(a, row.token);
+      const uint64_t own = masks[r];
       const bool none = own == 0 || sum == 0.f;
-      const float inv = none ? 0.f : v_scale / sum;
+      const float inv = none ? 0.f : to_value / sum;
       acc.x = none ? 0.f : acc.x * inv;
       acc.y = none ? 0.f : acc.y * inv;
       View view = View{0, 0, own};
@@ -403,6 +441,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");  // what is joined has been read
+    if (NT > 1) more = fetch();
   }
 }
 
