@@ -869,9 +869,11 @@ __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
 }
 // A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
 // score; f^8 has to stay inside fp32), any other the exponential and one reciprocal for two scores, 1 / a = b / (a b): three
-// of the special-function unit's results for two of a plain block's.
+// of the special-function unit's results for two of a plain block's.  Scores of keys that a row does not see are zeros here,
+// and rows that see nothing do not vote: neither changes the choice, nor the score beside it.  A NaN is then of a key that the
+// row sees, and may spoil the one beside it.
 template <bool EIGHT>
-__device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, float* s) {
+__device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, bool votes, float* s) {
   const float cap = a.softcap * kLog2e;
   if (EIGHT) {  // rows have factors of their own: out of the way, so that the coefficients are the same in every thread
 #pragma unroll
@@ -885,6 +887,7 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, f
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < BN; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
+  if (!votes) top = 0.f;
   if (__all_sync(~0u, top * f <= kSmall) && f > 0x1p-15f && f < 0x1p15f) {
     const float f2 = f * f, f4 = f2 * f2;
     const float2 c3 = both(g * (kTanh3 * f2)), c2 = both(g * (kTanh2 * f4)), c1 = both(g * (kTanh1 * f4 * f2)), c0 = both(g * (kTanh0 * f4 * f4));
@@ -1017,13 +1020,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       for (int c = 0; c < BN; c += 32) tc::ld32(tmem + t * 128 + c, s + c);
       tc::wait_ld<BN>(s);
       if (D == 64) read_done();
-      if (SHAPED == kCapped) cap_scores<EIGHT>(a, to_log2, reinterpret_cast<float*>(s));
-      if (SHAPED == kBiased) {
-        if (a.softcap > 0.f) cap_scores<EIGHT>(a, to_log2, reinterpret_cast<float*>(s));
-        bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
-      }
+      uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};  // bit c: the row sees key c of the block
       if (k.masked) {
-        // bit c: the row sees key c of the block
         uint64_t lo, hi;
         const View view = SHAPED ? view_of(a, it, row.token, mask) : View{0, 0, mask};
         if (k.prefix) {
@@ -1037,14 +1035,23 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
           lo = cut >= 64 ? 0 : lo & ~0ull << cut;
           hi = cut >= 128 ? 0 : cut > 64 ? hi & ~0ull << (cut - 64) : hi;
         }
-        const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        w[0] = (uint32_t)lo; w[1] = (uint32_t)(lo >> 32); w[2] = (uint32_t)hi; w[3] = (uint32_t)(hi >> 32);
+      }
+      auto fill = [&](uint32_t value) {  // scores of keys that the row does not see
 #pragma unroll
         for (int c = 0; c < BN; c += 32) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!((w[c >> 5] >> i) & 1)) s[c + i] = 0xFF800000u;  // -inf
+            if (!((w[c >> 5] >> i) & 1)) s[c + i] = value;
         }
+      };
+      if (SHAPED == kCapped || (SHAPED == kBiased && a.softcap > 0.f)) {
+        if (k.masked) fill(0);
+        cap_scores<EIGHT>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
       }
+      if (SHAPED == kBiased)
+        bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
+      if (k.masked) fill(0xFF800000u);  // -inf
       const float* sf = reinterpret_cast<const float*>(s);
       float mx[4] = {sf[0], sf[1], sf[2], sf[3]};
 #pragma unroll

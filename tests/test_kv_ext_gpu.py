@@ -6,6 +6,7 @@ to the type, e = 2^-24 that of an fp32 operation; each test adds up the rounding
 """
 import math
 import time
+import time
 
 import numpy as np
 import pytest
@@ -555,6 +556,18 @@ def test_attend_ext_masks_that_leave_nothing():
 def test_attend_what_is_not_seen_has_no_effect(value, eight, window, dims):
     """Everything that no slot of a request sees is NaN or infinite (8-bit caches: NaN): the rest of its pages, keys before
     every window, the pads' slots, pages of nobody.  Pads' queries are too."""
+    unseen_has_no_effect(value, eight, dims, window=window)
+
+
+@pytest.mark.parametrize("eight,value", [(False, math.nan), (False, math.inf), (True, math.nan)])
+@pytest.mark.parametrize("shape", [dict(cap=0.5), dict(cap=300.0), dict(alibi=0.5), dict(cap=0.5, window=90, alibi=0.1)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+@pytest.mark.parametrize("dims", [(2, 9, 37, [130, 61]), (3, 1, 200, [20, 0, 100]), (1, 61, 0, [1000])])
+def test_attend_what_is_not_seen_has_no_effect_on_shaped_scores(eight, value, shape, dims):
+    unseen_has_no_effect(value, eight, dims, **shape)
+
+
+def unseen_has_no_effect(value, eight, dims, window=0, **shape):
     batch, slots, prefix, ctx = dims
 
     def tweak(rng, q, k, v, pre, table, ctx, mask, page):
@@ -571,8 +584,28 @@ def test_attend_what_is_not_seen_has_no_effect(value, eight, window, dims):
                     keep[p, o] = True
         for x in (k, v):
             x[~keep.cuda()] = 0x7F if eight else value
-    run_attend("bf16", batch, slots, prefix, ctx, 8, 2, 128, 16, "head", eight, window=window, tweak=tweak)
-    run_attend("f16", batch, slots, prefix, ctx, 8, 2, 64, 16, "token", eight, window=window, tweak=tweak)
+    run_attend("bf16", batch, slots, prefix, ctx, 8, 2, 128, 16, "head", eight, window=window, tweak=tweak, **shape)
+    run_attend("f16", batch, slots, prefix, ctx, 8, 2, 64, 16, "token", eight, window=window, tweak=tweak, **shape)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("slots", [3, 40])
+@pytest.mark.parametrize("shape", [dict(), dict(cap=0.5), dict(cap=300.0), dict(alibi=0.2), dict(cap=0.5, alibi=0.2, window=60)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+def test_attend_keys_that_are_no_numbers_reach_only_those_that_see_them(eight, slots, shape):
+    """A slot's key that is a NaN spoils the rows that see it and leaves every bit of the others."""
+    seen = {}
+
+    def spoil(rng, q, k, v, pre, table, ctx, mask, page):
+        j = slots // 2
+        at = int(ctx[0]) + j
+        k[table[0, at // page], at % page, 0, 7] = 0x7F if eight else math.nan
+        seen["rows"] = torch.tensor([int(m) >> j & 1 for m in mask[0]], dtype=torch.bool, device="cuda")
+    args = ("bf16", 1, slots, 0, [150], 8, 2, 128, 16, "head", eight)
+    clean = run_attend(*args, **shape)[0].view(slots, 8, 128)
+    out = run_attend(*args, **shape, tweak=spoil, check=False)[0].view(slots, 8, 128)
+    assert torch.equal(out[:, 4:], clean[:, 4:]) and torch.equal(out[~seen["rows"]], clean[~seen["rows"]])
+    assert seen["rows"].any() and not torch.isfinite(out[seen["rows"]][:, :4]).any()
 
 
 @pytest.mark.parametrize("eight", [False, True])
@@ -838,3 +871,90 @@ def test_ext_refusals_of_live_handles():
     kv.attend(0, 4, x, c8, c8, table[:0], ctx[:0], 0, x)
     kv.read(0, 4, c8, c8, table[:0], ctx[:0], ctx[:0], k, k)
     assert kv.sync() == 0 and kv.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("eight,slots,page,dim,shape", [
+    (True, 1, 64, 128, {}), (True, 1, 8, 64, {}), (True, 3, 16, 128, dict(softcap=5.0, window=300)), (True, 12, 16, 128, {}),
+    (True, 12, 8, 64, {}), (True, 40, 64, 128, {}), (True, 40, 16, 64, dict(window=200)), (False, 1, 16, 128, dict(window=300)),
+    (False, 40, 64, 128, dict(softcap=5.0)), (False, 40, 16, 64, dict(softcap=5.0, window=99)),
+])
+def test_attend_ext_waits_are_bounded(eight, slots, page, dim, shape):
+    """With limits of a few polls waits run out: the call ends at once, says so, and the handle works on.  With and without
+    a prefix that the requests' rows are packed against."""
+    rng, gen = np.random.default_rng(6), torch.Generator(device="cuda").manual_seed(6)
+    pre, table, pages = tables(rng, 20, 700 + slots, 900, page)
+    caches = [make_cache(gen, pages, 2, page, dim, torch.bfloat16, "head", eight) for _ in range(2)]
+    kv = g.GraftKV(g.graft_kv_default_config(8, 2, dim, page, pages, 20, slots, cache="e4m3" if eight else None))
+    table, pre, at = cuda(table), cuda(pre), cuda((np.arange(20) * 37 % 700).astype(np.int32))
+    q = torch.randn((20 * slots, 8 * dim), generator=gen, device="cuda", dtype=torch.bfloat16) * 0.1
+    for prefix in (0, 900):
+        want, out = torch.zeros_like(q), torch.zeros_like(q)
+        call = lambda o: kv.attend(20, slots, q, *caches, table, at, 700, o, prefix_pages=pre if prefix else None,  # noqa: E731
+                                   prefix_len=prefix, **shape)
+        call(want)
+        assert kv.sync() == 0
+        expired = 0
+        for limit in [1, 2, 3] * 5:
+            kv.set_wait_limit(limit)
+            start = time.perf_counter()
+            call(out)
+            flags = kv.sync(raise_on_error=False)
+            assert time.perf_counter() - start < 0.5
+            assert flags in (0, gb.GRAFT_ERR_TIMEOUT)
+            assert flags or torch.equal(out, want)
+            expired += flags != 0
+        # CTAs of few rows wait for copies alone, which may all land within one poll
+        assert expired or (eight and slots * 4 <= 16)
+        kv.set_wait_limit(0)
+        out.zero_()
+        call(out)
+        assert kv.sync() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 1e-38, 3e-19, 2.0 ** -60, 0.0117, 1 / 3, 448.0, 2.0 ** 60, 5e19, 3e38])
+def test_append_quotients_are_correctly_rounded(scale):
+    """Codes are those of the correctly rounded fp32 quotient, whatever the scale: next to every middle between neighbours,
+    and over magnitudes from the smallest to the largest."""
+    rng = np.random.default_rng(1)
+    s = np.float32(scale)
+    middles = np.concatenate([(NUMBERS[:126] + NUMBERS[1:127]) / 2, [464.0, 448.0, 2.0 ** -10]])
+    x = np.concatenate([middles * float(s) * (1 + k * 2.0 ** -8) for k in (-2, -1, 0, 1, 2)] +
+                       [2.0 ** rng.uniform(-130, 127, 3000), float(s) * 2.0 ** rng.uniform(-14, 12, 3000)])
+    x = np.clip(np.concatenate([x, -x, np.zeros(-2 * len(x) % 64)]), -3e38, 3e38)
+    rows = cuda(x).to(torch.bfloat16).view(-1, 64)
+    n = rows.shape[0]
+    pages = -(-n // 128)
+    kv = g.GraftKV(g.graft_kv_default_config(1, 1, 64, 128, pages, 1, 1, cache="e4m3", rot_dim=0))
+    caches = [torch.zeros((pages, 1, 128, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    given = torch.tensor([s], device="cuda")
+    kv.append(1, n, None, rows, rows, None, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1),
+              torch.zeros(1, dtype=torch.int32, device="cuda"), *caches, None, k_scale=given, v_scale=given)
+    assert kv.sync() == 0
+    with np.errstate(over="ignore"):
+        want = nearest((rows.float().cpu().numpy() / s).astype(np.float32))
+    for c in caches:
+        assert np.array_equal(NUMBERS[c.view(-1, 64)[:n].cpu().numpy()], want)
+
+
+def test_append_quotients_over_rotated_keys():
+    """fp32 values of every last bit (sums of two products) over scales that are no powers of two: the codes are those of
+    the fp32 rotation and the quotient, each within half an ulp, so no further than the next fp32 number's."""
+    rng, gen = np.random.default_rng(3), torch.Generator(device="cuda").manual_seed(3)
+    n, hk, dim = 3000, 4, 64
+    k = torch.randn((n, hk * dim), generator=gen, device="cuda", dtype=torch.bfloat16)
+    rope = torch.rand((n, dim), generator=gen, device="cuda") * 2 - 1
+    pages = -(-n // 128)
+    kv = g.GraftKV(g.graft_kv_default_config(hk, hk, dim, 128, pages, 1, 1, cache="e4m3"))
+    caches = [torch.zeros((pages, hk, 128, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scale = head_scales(rng, hk) * 0.77
+    kv.append(1, n, None, k, k, rope, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1),
+              torch.zeros(1, dtype=torch.int32, device="cuda"), *caches, None, k_scale=scale, v_scale=scale)
+    assert kv.sync() == 0
+    x, cs = k.double().cpu().numpy().reshape(n, hk, dim), rope.double().cpu().numpy()[:, None]
+    a, b, c, s = x[..., :32], x[..., 32:], cs[..., :32], cs[..., 32:]
+    z = np.concatenate([a * c - b * s, b * c + a * s], -1)
+    off = 2 * E * np.concatenate([np.abs(a * c) + np.abs(b * s), np.abs(b * c) + np.abs(a * s)], -1)
+    by = scale.double().cpu().numpy()[:, None]
+    low, high = (z - off) / by, (z + off) / by
+    got = NUMBERS[caches[0].cpu().numpy()].transpose(0, 2, 1, 3).reshape(-1, hk, dim)[:n]
+    assert np.all(got >= nearest(low - E * np.abs(low))) and np.all(got <= nearest(high + E * np.abs(high)))
