@@ -379,6 +379,9 @@ int graft_kv_append_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d
                         const int32_t* d_ctx_len, void* d_q_out, int64_t q_out_stride, void* d_k_cache,
                         void* d_v_cache, const graft_kv_scales* scales, void* stream) {
   NvtxRange nvtx("graft_kv_append_ext");
+  if (!h) return GRAFT_EINVAL;
+  h->last_launches = 0;
+  if (const int rc = check_device(h)) return rc;
   return append(h, batch, slots, d_q, q_stride, d_k, k_stride, d_v, v_stride, d_depth, d_rows, d_position, d_rope, rope_len,
                 prefix_len, d_page_table, table_stride, d_ctx_len, d_q_out, q_out_stride, d_k_cache, d_v_cache, scales, stream);
 }
@@ -438,6 +441,9 @@ int graft_kv_attend_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d
                         void* d_out, int64_t out_stride, float* d_lse, const graft_kv_scales* scales,
                         const graft_kv_scores* scores, void* stream) {
   NvtxRange nvtx("graft_kv_attend_ext");
+  if (!h) return GRAFT_EINVAL;
+  h->last_launches = 0;
+  if (const int rc = check_device(h)) return rc;
   return attend(h, batch, slots, d_q, q_stride, d_k_cache, d_v_cache, d_prefix_pages, prefix_len, d_page_table, table_stride,
                 d_ctx_len, max_ctx, d_tree_mask, scale, d_out, out_stride, d_lse, scales, scores, stream);
 }

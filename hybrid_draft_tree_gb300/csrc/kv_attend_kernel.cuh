@@ -42,6 +42,12 @@
 //       the latency from scores to weights to products (2700 cycles a unit of 128 x
 //       128, two units in flight), pieces' ends (4 us each);
 //   1 x 1 behind 117                           6.9 us: latency.
+//
+// An 8-bit cache (EIGHT): four more warps turn copied tiles into 16-bit ones; items of
+// few rows go another way, in CTAs of their own (kv_few.cuh).  Scores may be capped,
+// windowed or biased (SHAPED).  Measured: 8 bits, 16 x 61 behind 12001 + 2048 224 us (1.9 us
+// a block of 256 rows, 1.3 of 128, by shared memory); a block of 256 rows under a window as
+// without, with biases 1.9 us, capped 2.4 (small scores) to 3.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -360,21 +366,12 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
       }
       return page;
     };
-    int next = page_of(0), last = -1, before = -1;  // pages of the keys to come, of the last ones, of those before
-    for (int x = 0; x < 2 * it.blocks && ok; ++x) {
-      const int tile = tile_of(EIGHT && !two, x, it.blocks), j = tile >> 1, v = tile & 1;
-      if (x == 2 * q_at) ok = queries();
-      if (!ok) break;
-      if (!v) {
-        before = last;
-        last = next;
-        if (j + 1 < it.blocks) next = page_of(j + 1);
-      }
-      const int from = EIGHT && !two && v && j + 1 < it.blocks ? before : last;
+    // a tile, from this lane's page
+    auto load = [&](int j, int v, int from) {
       const int stage = loads % S::kStages;
       ok = loads < S::kStages || wait_bar(sh, a, &sh.empty[stage], ((loads / S::kStages) - 1) & 1);
       ok = __all_sync(~0u, ok);
-      if (!ok) break;
+      if (!ok) return;
       if (lane == 0) mbar_expect_tx(&sh.full[stage], S::kCopied / L);  // this warp's copies
       __syncwarp();
       if (from >= 0)
@@ -383,6 +380,29 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
       // values to clean: said once the stage's phase is this block's
       if (!EIGHT && v == 1 && lane == 0 && own == 0 && block_of<SHAPED>(a, it, j).masked) mbar_arrive(&sh.dirty[stage]);
       ++loads;
+    };
+    int next = page_of(0);
+    if (!EIGHT || two) {
+      for (int j = 0; j < it.blocks && ok; ++j) {
+        if (j == q_at) ok = queries();
+        if (!ok) break;
+        const int here = next;
+        if (j + 1 < it.blocks) next = page_of(j + 1);
+        for (int v = 0; v < 2 && ok; ++v) load(j, v, here);
+      }
+    } else {
+      int last = -1, before = -1;  // pages of the last keys, and of those before: values come a block behind
+      for (int x = 0; x < 2 * it.blocks && ok; ++x) {
+        const int tile = tile_of(true, x, it.blocks), j = tile >> 1, v = tile & 1;
+        if (x == 2 * q_at) ok = queries();
+        if (!ok) break;
+        if (!v) {
+          before = last;
+          last = next;
+          if (j + 1 < it.blocks) next = page_of(j + 1);
+        }
+        load(j, v, v && j + 1 < it.blocks ? before : last);
+      }
     }
     last_two = two;
   }
@@ -869,13 +889,18 @@ __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
 }
 // A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
 // score; f^8 has to stay inside fp32), any other the exponential and one reciprocal for two scores, 1 / a = b / (a b): three
-// of the special-function unit's results for two of a plain block's.  Scores of keys that a row does not see are zeros here,
+// of the special-function unit's results for two of a plain block's (19 x 61 behind 6144: 134 and 160 us, 163 with a
+// reciprocal a score, 88 without a cap).  Scores of keys that a row does not see are zeros here,
 // and rows that see nothing do not vote: neither changes the choice, nor the score beside it.  A NaN is then of a key that the
 // row sees, and may spoil the one beside it.
 template <bool EIGHT>
 __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, bool votes, float* s) {
   const float cap = a.softcap * kLog2e;
-  if (EIGHT) {  // rows have factors of their own: out of the way, so that the coefficients are the same in every thread
+  float g = to_log2, f = g / cap;
+  // factors of the rows' own (an 8-bit cache's queries) or beyond the coefficients' range go into the scores
+  if (EIGHT || !(f > 0x1p-15f && f < 0x1p15f)) {
+    g = 1.f;
+    f = 1.f / cap;
 #pragma unroll
     for (int c = 0; c < BN; c += 2) {
       const float2 v = mul2(make_float2(s[c], s[c + 1]), both(to_log2));
@@ -883,7 +908,6 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, b
       s[c + 1] = v.y;
     }
   }
-  const float g = EIGHT ? 1.f : to_log2, f = g / cap;
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < BN; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
