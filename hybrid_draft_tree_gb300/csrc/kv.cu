@@ -206,7 +206,7 @@ int append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q
   a.position = d_position; a.tokens = (int64_t)batch * slots; a.axes = h->axes;
   std::memcpy(a.pair_axis, h->pair_axis, sizeof a.pair_axis);
   const int per = c.interleaved ? 4 : 8;
-  for (int i = 0; i < c.rot / 2; i += per) {
+  for (int i = 0; d_position && i < c.rot / 2; i += per) {
     uint64_t axis = a.pair_axis[i];
     for (int j = 1; j < per && i + j < c.rot / 2; ++j) axis = a.pair_axis[i + j] == axis ? axis : graft::kMixed;
     a.piece_axis |= axis << 4 * (i / per);

@@ -705,6 +705,16 @@ class GraftKV:
         positions: int32 [axes, batch, slots], rotated by in place of prefix_len +
         ctx_len + pos; k_scale, v_scale: float32 [kv_heads], of an 8-bit cache."""
         if self.eight or positions is not None or k_scale is not None or v_scale is not None:
+            f = self._append_ext
+            if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
+                rc = f.module.append_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32,
+                                         self._cache_dtype(k_cache), self.q_width, self.kv_width, self.rot_dim, self.span,
+                                         self.cfg.kv_heads, self.axes, batch, slots, prefix_len, q, k, v, rope, page_table,
+                                         ctx_len, k_cache, v_cache, q_out, pos, rows, positions, k_scale, v_scale)
+                if rc == 0:
+                    return
+                if rc is not NotImplemented:
+                    return self._check(rc)
             return self._append_more(batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len,
                                      pos, rows, stream, positions, k_scale, v_scale)
         f = self._append
@@ -732,14 +742,7 @@ class GraftKV:
 
     def _append_more(self, batch, slots, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, prefix_len, pos, rows,
                      stream, positions, k_scale, v_scale):
-        f, dc = self._append_ext, self._cache_dtype(k_cache)
-        if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
-            rc = f.module.append_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, dc, self.q_width,
-                                     self.kv_width, self.rot_dim, self.span, self.cfg.kv_heads, self.axes, batch, slots,
-                                     prefix_len, q, k, v, rope, page_table, ctx_len, k_cache, v_cache, q_out, pos, rows,
-                                     positions, k_scale, v_scale)
-            if rc is not NotImplemented:
-                return self._check(rc)
+        dc = self._cache_dtype(k_cache)
         b, dt, i32 = max(batch, 0), self.dtype, _T.int32
         n = b * slots
         scales = self._scales(k_scale, v_scale)
@@ -794,6 +797,17 @@ class GraftKV:
         a row sees, its own among them (0: all); k_scale, v_scale: float32
         [kv_heads], of an 8-bit cache."""
         if self.eight or softcap or window or slopes is not None or k_scale is not None or v_scale is not None:
+            f = self._attend_ext
+            if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
+                rc = f.module.attend_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, _T.int64,
+                                         self._cache_dtype(k_cache), self.q_width, self.q_heads, self.page_size, self.span,
+                                         self.cfg.kv_heads, batch, slots, prefix_len, max_ctx, window,
+                                         self.scale if scale is None else scale, softcap, q, k_cache, v_cache, page_table,
+                                         ctx_len, out, prefix_pages, tree_mask, lse, slopes, k_scale, v_scale)
+                if rc == 0:
+                    return
+                if rc is not NotImplemented:
+                    return self._check(rc)
             return self._attend_more(batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages,
                                      prefix_len, tree_mask, scale, lse, stream, softcap, window, slopes, k_scale, v_scale)
         f = self._attend
@@ -820,15 +834,8 @@ class GraftKV:
 
     def _attend_more(self, batch, slots, q, k_cache, v_cache, page_table, ctx_len, max_ctx, out, prefix_pages, prefix_len,
                      tree_mask, scale, lse, stream, softcap, window, slopes, k_scale, v_scale):
-        f, dc = self._attend_ext, self._cache_dtype(k_cache)
+        dc = self._cache_dtype(k_cache)
         scale = self.scale if scale is None else scale
-        if f is not None and f.module is not None and (self.eight or (k_scale is None and v_scale is None)):
-            rc = f.module.attend_ext(f.at, f.handle, _stream_addr(stream), self.dtype, _T.float32, _T.int32, _T.int64, dc,
-                                     self.q_width, self.q_heads, self.page_size, self.span, self.cfg.kv_heads, batch, slots,
-                                     prefix_len, max_ctx, window, scale, softcap, q, k_cache, v_cache, page_table, ctx_len,
-                                     out, prefix_pages, tree_mask, lse, slopes, k_scale, v_scale)
-            if rc is not NotImplemented:
-                return self._check(rc)
         b, dt, i32 = max(batch, 0), self.dtype, _T.int32
         n = b * slots
         scales = self._scales(k_scale, v_scale)
