@@ -45,7 +45,7 @@
 //
 // An 8-bit cache (EIGHT): four more warps turn copied tiles into 16-bit ones; items of
 // few rows go another way, in CTAs of their own (kv_few.cuh).  Scores may be capped,
-// windowed or biased (SHAPED).  Measured: 8 bits, 16 x 61 behind 12001 + 2048 224 us (1.9 us
+// windowed or biased (SHAPED).  Measured: 8 bits, 16 x 61 behind 12001 + 2048 218 us (1.9 us
 // a block of 256 rows, 1.3 of 128, by shared memory); a block of 256 rows under a window as
 // without, with biases 1.9 us, capped 2.4 (small scores) to 3.
 #pragma once
@@ -505,8 +505,8 @@ __device__ void clean_role(const AttendArgs& a, Bars& sh, uint8_t* ring) {
   }
 }
 
-// ---- warps 12-15: an 8-bit cache's tiles as 16-bit ones ----------------------------------------------------------
-// A thread a row: 16 bytes at a time become 32 at the places where the products look for them.  e4m3 numbers are f16
+// ---- an 8-bit cache's tiles and queries as f16 ones ---------------------------------------------------------------
+// Tiles, a thread a row: 16 bytes at a time become 32 at the places where the products look for them.  e4m3 numbers are f16
 // numbers, so nothing is rounded; the head's scales join the scores and the results.  All products over an 8-bit cache are
 // of f16 numbers: the step to bf16 takes three more instructions a pair (two tiles of 128 rows 2.26 us a block, 1.9 with f16).
 // Values that no row may see are made harmless on the way, as above; an e4m3 number that is not finite is a NaN.
@@ -559,8 +559,31 @@ __device__ __forceinline__ void convert_query(uint8_t* tile, int row, uint8_t* b
 // the products), of which there are then as many under way.
 constexpr int kTeams = 2, kTeamWarps = 2;
 
+// ---- warp 11, and 10 with large pages: an 8-bit cache's bf16 queries ---------------------------------------------
+// Warps that have nothing else to do.  When the converting warps did this beside a piece's first tiles, 16 x 61 behind
+// 12001 + 2048 took 224 us, 218 so, and 19 x 12 behind 6132 80, 75 so; contexts of a block or two lose by fewer threads
+// (15 x 17 behind 91 12.9 us, 13.8 so).
+template <int D, int L, int SHAPED>
+__device__ void query_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
+  constexpr int kFirst = L == 2 ? kCleanWarp : kSpareWarp, kThreadsHere = (kCleanWarp + 1 - kFirst) * 32;
+  const int lane = threadIdx.x & 31, thread = threadIdx.x - kFirst * 32;
+  int piece = 0;
+  Pieces<SHAPED> pieces(a, sh.line);
+  Item it;
+  for (; pieces.next(it); ++piece) {
+    if (!__all_sync(~0u, wait_bar(sh, a, &sh.q_full[piece & 1], (piece >> 1) & 1))) return;
+    const int tile = it.nt == 1 ? piece & 1 : 0;
+    for (int r = thread; r < it.nt * 128; r += kThreadsHere)
+      convert_query<D>(q + (tile + (r >> 7)) * Smem<D, true>::kTile, r & 127, &sh.q_back[tile * 128 + r]);
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_ready[piece & 1]);
+  }
+}
+
+// ---- warps 12-15: an 8-bit cache's tiles as 16-bit ones ----------------------------------------------------------
 template <typename T, int D, int SHAPED>
-__device__ void convert_role(const AttendArgs& a, Bars& sh, uint8_t* q, const uint8_t* ring, uint8_t* products) {
+__device__ void convert_role(const AttendArgs& a, Bars& sh, const uint8_t* ring, uint8_t* products) {
   using S = Smem<D, true>;
   constexpr int kChunks = D / 16, kRows = kTeamWarps * 32;  // 16-byte places of a row; rows that a team takes at a time
   const int lane = threadIdx.x & 31, team = (threadIdx.x / 32 - kConvertWarp) / kTeamWarps;
@@ -569,23 +592,7 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, uint8_t* q, const ui
   Pieces<SHAPED> pieces(a, sh.line);
   Item it;
   for (; pieces.next(it); before += 2 * it.blocks, ++piece) {
-    // A shared tile's queries are there first; those of two tiles come after the first blocks, of which three tiles can be
-    // made ready without them.
-    bool queries = std::is_same<T, __half>::value;
-    auto convert_queries = [&]() -> bool {
-      queries = true;
-      if (!__all_sync(~0u, wait_bar(sh, a, &sh.q_full[piece & 1], (piece >> 1) & 1))) return false;
-      const int tile = it.nt == 1 ? piece & 1 : 0;
-      for (int r = first + team * kRows; r < it.nt * 128; r += kTeams * kRows)
-        convert_query<D>(q + (tile + (r >> 7)) * S::kTile, r & 127, &sh.q_back[tile * 128 + r]);
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_ready[piece & 1]);
-      return true;
-    };
-    if (!queries && it.nt == 1 && !convert_queries()) return;
     for (int x = (team + kTeams - before % kTeams) % kTeams; x < 2 * it.blocks; x += kTeams) {
-      if (!queries && x >= kTeams && !convert_queries()) return;
       const int tile = tile_of(it.nt == 1, x, it.blocks), v = tile & 1, number = before + x;
       const int from = number % S::kStages, to = number % S::kReady;
       Block k{};
@@ -647,7 +654,6 @@ __device__ void convert_role(const AttendArgs& a, Bars& sh, uint8_t* q, const ui
         mbar_arrive(&sh.clean[to]);
       }
     }
-    if (!queries && !convert_queries()) return;
   }
 }
 
@@ -1363,7 +1369,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       mbar_init(&sh.clean[i], EIGHT ? kTeamWarps : 3 - L);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); mbar_init(&sh.q_ready[i], kTeams * kTeamWarps); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); mbar_init(&sh.q_ready[i], 3 - L); }
     mbar_init(&sh.o_free, 8);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 8; ++i) sh.bad[i] = sh.bad_edge[i] = 0;
@@ -1387,7 +1393,8 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       if (tc::elect()) mma_role<T, D, EIGHT, SHAPED>(a, sh, base, base + S::kProducts);
       __syncwarp();
     } else if (EIGHT) {
-      if (warp >= kConvertWarp) convert_role<T, D, SHAPED>(a, sh, base, base + S::kRing, base + S::kProducts);
+      if (warp >= kConvertWarp) convert_role<T, D, SHAPED>(a, sh, base + S::kRing, base + S::kProducts);
+      else if (std::is_same<T, __nv_bfloat16>::value) query_role<D, L, SHAPED>(a, sh, base);
     } else clean_role<T, D, L, SHAPED>(a, sh, base + S::kRing);
   }
   tc::fence_before();
