@@ -894,12 +894,14 @@ __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
   return fabsf(x) <= kSmall ? near : far;
 }
 // A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
-// score; f^8 has to stay inside fp32), any other the exponential and one reciprocal for two scores, 1 / a = b / (a b): three
-// of the special-function unit's results for two of a plain block's (19 x 61 behind 6144: 134 and 160 us, 163 with a
-// reciprocal a score, 88 without a cap).  Scores of keys that a row does not see are zeros here,
-// and rows that see nothing do not vote: neither changes the choice, nor the score beside it.  A NaN is then of a key that the
-// row sees, and may spoil the one beside it.
-template <bool EIGHT>
+// score; f^8 has to stay inside fp32), any other the exponential and a reciprocal: one for two scores, 1 / a = b / (a b), in
+// 16-bit caches' heads of 128, else one for each, which takes fewer instructions but more of the special-function unit (19 x 61
+// behind 6083, pairs and each: 161 and 174 us; heads of 64 157 and 157, 120 and 115 under a window; 8 bits 167 and 161.
+// Without a cap the first takes 88, with small scores 136).  An exponential by multiply-adds for a quarter of the scores costs
+// more than it saves (179), and so does a reciprocal for four (8 bits 172).  Scores of keys that a row does not see are zeros
+// here, and rows that see nothing do not vote: neither changes the choice, nor the score beside it.  A NaN is then of a key
+// that the row sees, and may spoil the one beside it.
+template <int D, bool EIGHT>
 __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, bool votes, float* s) {
   const float cap = a.softcap * kLog2e;
   float g = to_log2, f = g / cap;
@@ -934,11 +936,18 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, b
 #pragma unroll
   for (int c = 0; c < BN; c += 2) {
     const float2 y = mul2(make_float2(s[c], s[c + 1]), to_e);
-    // beyond 2^60 the quotient is 0 in all of the cap's bits; the product of two stays inside fp32
-    const float2 e = add2(make_float2(ex2(min_nan(y.x, 60.f)), ex2(min_nan(y.y, 60.f))), both(1.f));
-    const float r = rcp(e.x * e.y) * (-2.f * cap);
-    s[c] = fmaf(r, e.y, cap);
-    s[c + 1] = fmaf(r, e.x, cap);
+    if (EIGHT || D == 64) {
+      const float2 e = add2(make_float2(ex2(y.x), ex2(y.y)), both(1.f));  // of infinity: 0
+      const float2 v = fma2(make_float2(rcp(e.x), rcp(e.y)), both(-2.f * cap), both(cap));
+      s[c] = v.x;
+      s[c + 1] = v.y;
+    } else {
+      // beyond 2^60 the quotient is 0 in all of the cap's bits; the product of two stays inside fp32
+      const float2 e = add2(make_float2(ex2(min_nan(y.x, 60.f)), ex2(min_nan(y.y, 60.f))), both(1.f));
+      const float r = rcp(e.x * e.y) * (-2.f * cap);
+      s[c] = fmaf(r, e.y, cap);
+      s[c + 1] = fmaf(r, e.x, cap);
+    }
   }
 }
 // The bias takes distances as whole numbers, from the block's last key on: it is exact next to the row's own key whatever
@@ -1077,7 +1086,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       };
       if (SHAPED == kCapped || (SHAPED == kBiased && a.softcap > 0.f)) {
         if (k.masked) fill(0);
-        cap_scores<EIGHT>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
+        cap_scores<D, EIGHT>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
       }
       if (SHAPED == kBiased)
         bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
