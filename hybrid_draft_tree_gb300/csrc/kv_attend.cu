@@ -172,6 +172,9 @@ int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int6
 // Both sides, in us: packed 60 and joined 226 (64 x 1 behind 8192 + 1024), 86 and 100 (64 x 17 behind 2048 + 777, heads
 // of 64), 179 and 167 (16 x 61 behind 12001 + 2048); two tiles and one 167 and 195 in the last, 43 and 61 (1 x 61 behind
 // 32768); whole and cut 6.9 and 10.4 (1 x 1 behind 117).
+//
+// The kernels hold an item's length in 32 bits.  Where costs of 10 ns would pass them (some 1.8e9 keys and more, at up to 300
+// a block), the plan that is chosen counts in a larger unit.
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int window, bool eight, bool capped, int num_sms) {
   const int64_t R = (int64_t)slots * group, all = batch * R;
@@ -245,12 +248,19 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
         }
       }
       t = best_end + join;
-      p.chunk_a = std::max(((int64_t)line + p.split - 1) / p.split, (int64_t)p.step_a);
     }
     if (best_t == 0 || t < best_t) {
       best_t = t;
       best = p;
     }
+  }
+  // an item's length and a block more, which a place is rounded up by
+  auto longest = [&](int64_t fixed, int64_t step) { return fixed + ((int64_t)np + no + 1) * step; };
+  while (std::max(longest(best.fixed_a, best.step_a), longest(best.fixed_b, best.step_b)) > UINT32_MAX)
+    for (int32_t* cost : {&best.fixed_a, &best.step_a, &best.fixed_b, &best.step_b}) *cost = (*cost + 1) / 2;
+  if (best.split) {
+    const int64_t line = best.items_a * (best.fixed_a + (int64_t)np * best.step_a);
+    best.chunk_a = std::max((line + best.split - 1) / best.split, (int64_t)best.step_a);
   }
   return best;
 }

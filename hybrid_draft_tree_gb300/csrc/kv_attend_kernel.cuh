@@ -123,8 +123,8 @@ constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 constexpr int kPlain = 0, kWindowed = 1, kCapped = 2, kBiased = 3;
 
 // The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
-// `fixed` units before its first block's.  An item is shorter than 2^32 units: prefix, context and tree together are below
-// 2^31 keys (graft_kv_attend), so its key blocks below 2^24 + 2, of at most 152 units.
+// `fixed` units before its first block's.  An item and a block are shorter than 2^32 units together (plan_kv_attend sees to
+// it; prefix, context and tree together are below 2^31 keys, so key blocks below 2^24 + 2).
 struct Line {
   int64_t lo, hi;      // this CTA's part
   int64_t at;          // start of its first item
