@@ -267,7 +267,7 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
 
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s) {
-  const int form = a.slope ? kBiased : a.softcap > 0.f ? kCapped : a.window > 0 ? kWindowed : kPlain;
+  const int form = a.slope || a.softcap * kLog2e > kWide ? kBiased : a.softcap > 0.f ? kCapped : a.window > 0 ? kWindowed : kPlain;
   const cudaError_t e = kForms[a.c.eight != 0][form]->launch(a, qmap, kmap, vmap, dtype, s);
   if (e != cudaSuccess || !a.plan.cut) return e;
   if (a.c.dim == 128) return dtype == GRAFT_BF16 ? join<__nv_bfloat16, 128>(a, s) : join<__half, 128>(a, s);

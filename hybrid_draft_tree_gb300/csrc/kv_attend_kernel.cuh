@@ -119,8 +119,11 @@ constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 
 // What becomes of scores, a kernel each (what the loop over the blocks does not use costs it registers and instruction
 // fetches: 19 x 61 behind 2048 under a window takes 41 us in a kernel of its own, 45 in one that can do all of it).  Each can
-// do what those before it can; windows are in all but the first.
+// do what those before it can; windows are in all but the first, caps above kWide (in units of log2) in the last alone, whose
+// slopes may be none: what these take would cost smaller caps 6% in the third (16 x 61 behind 8192 under a window
+// of 4096: 148 us, 158 with it).
 constexpr int kPlain = 0, kWindowed = 1, kCapped = 2, kBiased = 3;
+constexpr float kWide = 256.f;
 
 // The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
 // `fixed` units before its first block's.  An item and a block are shorter than 2^32 units together (plan_kv_attend sees to
@@ -885,7 +888,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
 // cap tanh(x), x = s / softcap and cap in units of log2, as factors of a product: x = s f, cap tanh(x) = s g tanh(x) / x.
 // Small x: tanh(x) / x by a polynomial in x^2 (fitted to |x| <= 1/2, off by 2^-25 of it).  Others: 1 - 2 / (1 + e^2x), off by
 // some 2^-22 of the cap wherever x lies, which at a half of it and above is no more than such a score's own rounding steps
-// (tanh.approx is off by 2^-11).
+// (tanh.approx is off by 2^-11).  Under caps of up to kWide the same holds of small x: there 2^-22 of the cap is 2^-14 and less.
 constexpr float kSmall = 0.5f, kTanh0 = 0.017135f, kTanh1 = -0.05298607f, kTanh2 = 0.13324779f, kTanh3 = -0.33333069f;
 __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
   const float x = s * f, z = x * x;
@@ -894,14 +897,15 @@ __device__ __forceinline__ float capped(float s, float f, float g, float cap) {
   return fabsf(x) <= kSmall ? near : far;
 }
 // A block's.  A warp whose scores are all small takes the polynomial, with f and g in its coefficients (6 multiply-adds a
-// score; f^8 has to stay inside fp32), any other the exponential and a reciprocal: one for two scores, 1 / a = b / (a b), in
-// 16-bit caches' heads of 128, else one for each, which takes fewer instructions but more of the special-function unit (19 x 61
-// behind 6083, pairs and each: 161 and 174 us; heads of 64 157 and 157, 120 and 115 under a window; 8 bits 167 and 161.
-// Without a cap the first takes 88, with small scores 136).  An exponential by multiply-adds for a quarter of the scores costs
-// more than it saves (179), and so does a reciprocal for four (8 bits 172).  Scores of keys that a row does not see are zeros
-// here, and rows that see nothing do not vote: neither changes the choice, nor the score beside it.  A NaN is then of a key
-// that the row sees, and may spoil the one beside it.
-template <int D, bool EIGHT>
+// score; f^8 has to stay inside fp32: beyond caps of 2^15 the scores are x themselves).  Any other takes the exponential and a
+// reciprocal: one for two scores, 1 / a = b / (a b), in 16-bit caches' heads of 128, else one for each, which takes fewer
+// instructions but more of the special-function unit (19 x 61 behind 6083, pairs and each: 161 and 174 us; heads of 64 157 and
+// 157, 120 and 115 under a window; 8 bits 167 and 161.  Without a cap the first takes 88, with small scores 136); under caps
+// above kWide each score by its own size, so that small ones lose nothing by larger ones in the rows beside them.  An
+// exponential by multiply-adds for a quarter of the scores costs more than it saves (179), and so does a reciprocal for four (8
+// bits 172).  Scores of keys that a row does not see are zeros here, and rows that see nothing do not vote: neither changes the
+// choice, nor the score beside it.  A NaN is then of a key that the row sees, and may spoil the one beside it.
+template <int D, bool EIGHT, bool WIDE>
 __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, bool votes, float* s) {
   const float cap = a.softcap * kLog2e;
   float g = to_log2, f = g / cap;
@@ -916,11 +920,21 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, b
       s[c + 1] = v.y;
     }
   }
+  if (WIDE && !(f > 0x1p-15f)) {  // the cap is beyond 2^15: what scores are in units of it
+#pragma unroll
+    for (int c = 0; c < BN; c += 2) {
+      const float2 v = mul2(make_float2(s[c], s[c + 1]), both(f));
+      s[c] = v.x;
+      s[c + 1] = v.y;
+    }
+    g = cap;
+    f = 1.f;
+  }
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < BN; c += 2) top = max3(top, fabsf(s[c]), fabsf(s[c + 1]));
   if (!votes) top = 0.f;
-  if (__all_sync(~0u, top * f <= kSmall) && f > 0x1p-15f && f < 0x1p15f) {
+  if (__all_sync(~0u, top * f <= kSmall) && f < 0x1p15f) {
     const float f2 = f * f, f4 = f2 * f2;
     const float2 c3 = both(g * (kTanh3 * f2)), c2 = both(g * (kTanh2 * f4)), c1 = both(g * (kTanh1 * f4 * f2)), c0 = both(g * (kTanh0 * f4 * f4));
 #pragma unroll
@@ -930,6 +944,11 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, b
       s[c] = p.x;
       s[c + 1] = p.y;
     }
+    return;
+  }
+  if (WIDE && cap > kWide) {
+#pragma unroll
+    for (int c = 0; c < BN; ++c) s[c] = capped(s[c], f, g, cap);
     return;
   }
   const float2 to_e = both(f * (2.f * kLog2e));
@@ -1026,7 +1045,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   const float scale = SHAPED >= kCapped ? 1.f : to_log2;
   float slope = 0.f;
   if (SHAPED == kBiased && live) {
-    slope = a.slope[row.head] * kLog2e;
+    slope = a.slope ? a.slope[row.head] * kLog2e : 0.f;
     if (!(fabsf(slope) < INFINITY)) {
       slope = 0.f;
       atomicOr(a.err, GRAFT_ERR_RULE);
@@ -1086,7 +1105,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       };
       if (SHAPED == kCapped || (SHAPED == kBiased && a.softcap > 0.f)) {
         if (k.masked) fill(0);
-        cap_scores<D, EIGHT>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
+        cap_scores<D, EIGHT, SHAPED == kBiased>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
       }
       if (SHAPED == kBiased)
         bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));

@@ -200,7 +200,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
         if (SHAPED && on) {
           view[nt][i] = view_of(a, it, own.token, mask[nt][i]);
           if (SHAPED == kBiased) {
-            slope[nt][i] = a.slope[own.head] * kLog2e;
+            slope[nt][i] = a.slope ? a.slope[own.head] * kLog2e : 0.f;
             if (!(fabsf(slope[nt][i]) < INFINITY)) {
               slope[nt][i] = 0.f;
               atomicOr(a.err, GRAFT_ERR_RULE);

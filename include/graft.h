@@ -603,7 +603,10 @@ int graft_kv_read(graft_kv* h, int32_t batch, int32_t slots, const void* d_k_cac
  * position in the sequence that a row sees (the prefix and the context in order,
  * then the slots of its mask in order, as if its path had been emitted token by
  * token; the row's own is the last of these), in this order:
- *   softcap  > 0: s = softcap * tanh(s / softcap); finite
+ *   softcap  > 0: s = softcap * tanh(s / softcap); finite.  Off by a few roundings of
+ *            s and, under caps of up to 177, by 2^-20 of the cap: which of these
+ *            depends on the scores of the rows beside a row, so that its last bits
+ *            may change with them (with the same inputs they are the same)
  *   d_slope  DEVICE float [q_heads] or NULL: s -= d_slope[h] * (pos_i - pos_j);
  *            one that is not finite counts as 0 and sets GRAFT_ERR_RULE
  *   window   > 0: keys with pos_i - pos_j >= window are not seen */

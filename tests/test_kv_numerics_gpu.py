@@ -1,0 +1,123 @@
+"""Where attention's numbers are stretched: caps far above the scores, and rows of very different scores beside each other.  Against the definition in 64 bits; tolerances add up the
+roundings, e = 2^-24 an fp32 operation's, u = 2^-8 (bf16) or 2^-11 (f16) the type's."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import hybrid_draft_tree_gb300 as g  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+GDT = {"bf16": g.GRAFT_BF16, "f16": g.GRAFT_F16}
+U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+E = 2.0 ** -24
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(autouse=True)
+def _cuda(cuda_ok):
+    torch.cuda.set_device(0)
+
+
+def held(x, eight, dtype):
+    """What a cache holds of x, as numbers and as it is."""
+    kept = x.clamp(-448, 448).to(E4M3) if eight else x.to(DT[dtype])
+    return kept.double(), kept
+
+
+def attend(dtype, eight, q, k, v, prefix=0, page=32, **scores):
+    """Rows q [batch, slots, hq, dim] after k, v [batch, keys, hk, dim], whose last `slots` are the rows' own, under causal
+    masks; the first `prefix` keys are the first request's for all.  The result, its lse, the definition of both in 64 bits,
+    the sum of weight times |v|, the largest weight times the sum of |v|, and the row's largest sum of |q k| and capped score."""
+    (batch, slots, hq, dim), (keys, hk) = q.shape, k.shape[1:3]
+    ctx = keys - slots - prefix
+    q = q.to(DT[dtype])
+    (kn, kc), (vn, vc) = held(k, eight, dtype), held(v, eight, dtype)
+    pre, own = -(-prefix // page), -(-(keys - prefix) // page)
+    pages = pre + batch * own
+
+    def paged(x):
+        cache = torch.zeros((pages * page, hk, dim), dtype=torch.uint8 if eight else x.dtype, device="cuda")
+        x = x.view(torch.uint8) if eight else x
+        cache[:prefix] = x[0, :prefix]
+        for b in range(batch):
+            at = (pre + b * own) * page
+            cache[at:at + keys - prefix] = x[b, prefix:]
+        return cache.view(pages, page, hk, dim).transpose(1, 2).contiguous()
+    caches = paged(kc), paged(vc)
+    if prefix:
+        kn, vn = (torch.cat([x[:1, :prefix].expand(batch, -1, -1, -1), x[:, prefix:]], 1) for x in (kn, vn))
+    kv = g.GraftKV(g.graft_kv_default_config(hq, hk, dim, page, pages, batch, slots, GDT[dtype], cache="e4m3" if eight else None))
+    rows = q.reshape(batch * slots, hq * dim).contiguous()
+    out, lse = torch.zeros_like(rows), torch.zeros((batch * slots, hq), device="cuda")
+    table = torch.arange(pre, pages, dtype=torch.int32, device="cuda").view(batch, own)
+    kv.attend(batch, slots, rows, *caches, table, torch.full((batch,), ctx, dtype=torch.int32, device="cuda"), ctx, out,
+              prefix_pages=torch.arange(pre, dtype=torch.int32, device="cuda") if prefix else None, prefix_len=prefix, lse=lse, **scores)
+    assert kv.sync() == 0
+    place = torch.arange(keys, device="cuda")
+    distance = (keys - slots + torch.arange(slots, device="cuda"))[:, None] - place
+    want = {n: [] for n in ("out", "lse", "spread", "top", "reach", "score")}
+    for b in range(batch):
+        qd = q[b].double().view(slots, hk, hq // hk, dim)
+        s = torch.einsum("shgd,nhd->shgn", qd, kn[b]) * dim ** -0.5
+        reach = torch.einsum("shgd,nhd->shgn", qd.abs(), kn[b].abs()).amax(-1) * dim ** -0.5
+        cap = scores.get("softcap", 0.0)
+        if cap:
+            s = cap * torch.tanh(s / cap)
+        size = s.abs().amax(-1)
+        if scores.get("slopes") is not None:
+            s = s - scores["slopes"].double().view(hk, -1, 1) * distance[:, None, None]
+        s = s.masked_fill((distance < 0)[:, None, None], -math.inf)
+        z = torch.logsumexp(s, -1)
+        w = torch.exp(s - z[..., None])
+        want["out"].append(torch.einsum("shgn,nhd->shgd", w, vn[b]))
+        want["spread"].append(torch.einsum("shgn,nhd->shgd", w, vn[b].abs()))
+        want["top"].append(w.amax(-1)[..., None] * vn[b].abs().sum(0)[None, :, None])
+        want["lse"].append(z)
+        want["reach"].append(reach)
+        want["score"].append(size)
+    want = {n: torch.stack(x).reshape(batch * slots, hq, *x[0].shape[3:]) for n, x in want.items()}
+    return out.double().view(batch * slots, hq, dim), lse.double(), want
+
+
+def check(dtype, eight, got, lse, want, keys, dim, cap=0.0, slack=0.0):
+    """A score's fp32 sum of dim products, its scalings and the exponent's argument: (dim + 8) e of sum |q k|.  A capped one is
+    off by 16 e of itself and, next to a cap of up to 256 in units of log2 (178), of the cap.  A weight is rounded to the
+    type: u (f16 over 8-bit caches, no more than that)."""
+    score = (dim + 8) * E * (want["reach"] + 16) + (16 * E * min(cap, 178.0) + 40 * E * want["score"] if cap else 0.0)
+    off = (U[dtype] + 2 * score[..., None] + (keys + 64) * E) * want["spread"] + U[dtype] * want["out"].abs() + slack + 2.0 ** -24
+    assert torch.all((lse - want["lse"]).abs() <= score + (keys + 16) * E + 2 * E * want["lse"].abs())
+    assert torch.all((got - want["out"]).abs() <= off)
+
+
+CAPS = [2.2e4, 2.4e4, 1e6, 1e9, 8e37]
+
+
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("dtype,eight,slots,hq,hk,dim", [
+    ("bf16", False, 1, 4, 2, 128), ("f16", False, 19, 4, 1, 64), ("bf16", False, 61, 8, 2, 128), ("f16", False, 61, 4, 1, 128),
+    ("bf16", True, 1, 4, 2, 128), ("f16", True, 3, 4, 1, 64), ("bf16", True, 19, 4, 2, 64), ("f16", True, 61, 8, 2, 128)])
+def test_a_cap_far_above_the_scores_changes_next_to_nothing(cap, dtype, eight, slots, hq, hk, dim):
+    gen = torch.Generator(device="cuda").manual_seed(slots + dim)
+    q = torch.randn((2, slots, hq, dim), generator=gen, device="cuda") * 6
+    k, v = (torch.randn((2, 700 + slots, hk, dim), generator=gen, device="cuda") for _ in range(2))
+    got, lse, want = attend(dtype, eight, q, k, v, softcap=cap)
+    check(dtype, eight, got, lse, want, 700 + slots, dim, cap)
+
+
+@pytest.mark.parametrize("cap", [30.0, 150.0, 400.0, 3000.0, 2e4])
+@pytest.mark.parametrize("dtype,eight,slots,hq,hk,dim", [
+    ("f16", False, 19, 4, 1, 64), ("f16", False, 61, 8, 2, 128), ("f16", True, 4, 4, 1, 64), ("f16", True, 61, 8, 2, 128),
+    ("bf16", True, 61, 4, 1, 64)])
+def test_rows_of_small_scores_beside_rows_at_the_cap(cap, dtype, eight, slots, hq, hk, dim):
+    """Every other row's scores come near the cap, those beside it are of about 3: none loses by its neighbour."""
+    gen = torch.Generator(device="cuda").manual_seed(slots + dim)
+    if dtype == "bf16":                 # whose queries may be larger
+        cap *= 50
+    q = torch.randn((2, slots, hq, dim), generator=gen, device="cuda") * 3
+    k, v = (torch.randn((2, 700 + slots, hk, dim), generator=gen, device="cuda") for _ in range(2))
+    q[:, ::2] *= cap / 9
+    got, lse, want = attend(dtype, eight, q, k, v, softcap=cap)
+    check(dtype, eight, got, lse, want, 700 + slots, dim, cap)
