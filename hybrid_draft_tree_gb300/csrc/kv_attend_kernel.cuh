@@ -14,10 +14,11 @@
 // turn, and their results are joined at the end.
 //
 // The online softmax keeps, per row, a base m, l = sum 2^(s-m) and O = sum
-// 2^(s-m) v, s in units of log2.  m is the maximum of the row's first keys and
-// moves only when a later one exceeds it by 2^12: until then weights above 1 are
-// as exact as below, O, which lives in tensor memory, is not read and written
-// back for every block, and the weights need not wait for the block's maximum.
+// 2^(s-m) v, s in units of log2.  m is the maximum of the row's first keys (2^6
+// below it with f16 weights) and moves only when a later one exceeds it by 2^12
+// (2^15.75): until then weights above 1 are as exact as below, O, which lives in
+// tensor memory, is not read and written back for every block, and the weights
+// need not wait for the block's maximum.
 //
 // Rows of all requests against the prefix are packed into the same tiles
 // ("packed"), so a prefix block is read once for up to 256 rows, when a
@@ -69,9 +70,16 @@ template <bool EIGHT> constexpr int kOtherRegs = EIGHT ? 48 : 56;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kSpareWarp = 10, kCleanWarp = 11, kConvertWarp = 12;
 constexpr int BN = 128;                   // keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
-// log2 of how far a maximum may run ahead of the base: weights stay inside f16.  A sum of n values of at most |v| reaches
-// 2^12 n |v|, so it stays inside fp32 while n |v| < 2^115 (f16's values always do).
-constexpr float kGrow = 12.f;
+// log2 of how far a maximum lies above its base when it sets it, and of how far a later one may run ahead before the base
+// moves, by the weights' type.  f16 weights (f16 models, 8-bit caches) use f16's whole range: the maximum's is 2^6, what lies
+// down to 2^20 below it has all of its 11 bits, and further down a weight is off by 2^-31 of it at most.  A first key that
+// outweighs the rest by that much is common, and its value often next to nothing: with the base at the maximum the rest lost
+// 6 bits more.  Further down still, rows whose first keys say little of their largest would move their bases in many blocks (8
+// bits, 16 x 61 behind 12001 with 0, 6 and 8: 216.4, 218.0 and 225 us; f16, 64 x 17, heads of 64: 85.6, 85.8 and 89).  A sum of n
+// values of at most |v| reaches 2^16 n |v|, which stays inside fp32 for f16's values and e4m3's.  bf16 weights keep their 8 bits
+// at any size; 2^12 n |v| stays inside fp32 while n |v| < 2^115.
+template <typename P> constexpr float kLead = std::is_same<P, __half>::value ? 6.f : 0.f;
+template <typename P> constexpr float kGrow = std::is_same<P, __half>::value ? 15.75f : 12.f;
 
 // Shared memory: two query tiles, the ring, where results pass on their way out, and the barriers.  A tile is stored in
 // column halves of 64 elements (128 bytes).  With D = 128 results pass through a query tile, 4 KB a warp: a shared tile's
@@ -1129,7 +1137,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
       float2 sum0, sum1;
       for (;;) {
         if (!known) {
-          const float next = top > m + kGrow ? top : m;
+          const float next = top > m + kGrow<P> ? top - kLead<P> : m;
           const float f = next == -INFINITY ? 1.f : ex2(m - next);
           m = next;
           l2.x *= f;
@@ -1170,7 +1178,7 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
           }
           tc::st16(p_at + c / 2, p);
         }
-        if (!known || !__any_sync(~0u, live && top > m + kGrow)) break;
+        if (!known || !__any_sync(~0u, live && top > m + kGrow<P>)) break;
         tc::wait_st();  // two stores to one place keep no order of their own
         known = false;
       }

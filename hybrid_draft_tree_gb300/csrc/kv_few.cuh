@@ -12,8 +12,8 @@
 // The order of d within a product is free as long as both operands have the same, and so is that of the keys: both are
 // taken so that a lane's share is 16 consecutive bytes, and lanes that read together read other banks.
 //
-// A warp keeps a base, a sum and O of its own for each row; the base moves when a score exceeds it by 2^12 (as in the other
-// kernel), so there is no exchange between lanes in the loop.  Warps are joined at the piece's end, in their order.
+// A warp keeps a base, a sum and O of its own for each row; the base moves as in the other
+// kernel, so there is no exchange between lanes in the loop.  Warps are joined at the piece's end, in their order.
 // bf16 queries become f16 ones as in the other kernel.
 #pragma once
 
@@ -314,7 +314,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) grown = grown || s[nt][i] > m[nt][i & 1] + kGrow;
+        for (int i = 0; i < 4; ++i) grown = grown || s[nt][i] > m[nt][i & 1] + kGrow<__half>;
       if (__any_sync(~0u, grown)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -322,7 +322,7 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
           for (int i = 0; i < 2; ++i) {
             float top = fmaxf(s[nt][i], s[nt][2 + i]);
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-            const float next = top > m[nt][i] + kGrow ? top : m[nt][i];
+            const float next = top > m[nt][i] + kGrow<__half> ? top - kLead<__half> : m[nt][i];
             const float by = next == -INFINITY || next == m[nt][i] ? 1.f : ex2(m[nt][i] - next);
             m[nt][i] = next;
             l[nt][i] *= by;

@@ -540,7 +540,9 @@ int graft_kv_append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, 
  *   d_lse         float [batch * slots][q_heads], or NULL
  * The cache buffers must start on 16-byte boundaries.  Products are exact in
  * fp32 and summed there, as are the softmax statistics; a key's weight is
- * rounded to the cache's type for its product with the value.  Sums stay finite
+ * rounded to the 16-bit type (over an 8-bit cache always to f16) for its product
+ * with the value: an f16 weight below 2^-20 of the row's largest keeps fewer than
+ * its 11 bits, and is off by 2^-31 of the largest at most.  Sums stay finite
  * while the number of keys times the largest |v_j| is below 2^115.  A ctx_len
  * outside [0, max_ctx] is clamped to it, and a page outside the cache reads as
  * zeros; both set GRAFT_ERR_RANGE.  Asynchronous; one or two kernels. */

@@ -1,4 +1,5 @@
-"""Where attention's numbers are stretched: caps far above the scores, and rows of very different scores beside each other.  Against the definition in 64 bits; tolerances add up the
+"""Where attention's numbers are stretched: caps far above the scores, rows of very different scores beside each other, and a
+first key that outweighs the others by far and counts for nothing.  Against the definition in 64 bits; tolerances add up the
 roundings, e = 2^-24 an fp32 operation's, u = 2^-8 (bf16) or 2^-11 (f16) the type's."""
 import math
 
@@ -121,3 +122,27 @@ def test_rows_of_small_scores_beside_rows_at_the_cap(cap, dtype, eight, slots, h
     q[:, ::2] *= cap / 9
     got, lse, want = attend(dtype, eight, q, k, v, softcap=cap)
     check(dtype, eight, got, lse, want, 700 + slots, dim, cap)
+
+
+@pytest.mark.parametrize("gap", [12.0, 16.0, 18.0, 20.0])
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+@pytest.mark.parametrize("dtype,eight", [("bf16", True), ("f16", True), ("f16", False), ("bf16", False)])
+@pytest.mark.parametrize("batch,slots,prefix,hq,hk,dim", [
+    (80, 1, 0, 8, 2, 64), (80, 4, 0, 4, 2, 128), (80, 9, 0, 8, 2, 64), (80, 40, 0, 8, 2, 128),     # an item whole, or nearly
+    (1, 61, 0, 8, 2, 128), (40, 2, 3000, 8, 4, 128), (20, 61, 3000, 4, 1, 64)])
+def test_a_first_key_that_outweighs_the_others(gap, spread, dtype, eight, batch, slots, prefix, hq, hk, dim):
+    """Key 0 scores `gap` above thousands of others (in logarithms of weights), all alike or spread, and its value is zero, so
+    the result is made of weights that are small next to the largest.  f16 weights (8-bit caches, f16 models) that are
+    subnormal are off by 2^-25 at most, with the first maximum's at 2^6: 2^-31 of the row's largest."""
+    keys = 4000 + slots
+    gen = torch.Generator(device="cuda").manual_seed(slots + dim)
+    q, k, v = (torch.randn(s, generator=gen, device="cuda") for s in ((batch, slots, hq, dim), (batch, keys, hk, dim), (batch, keys, hk, dim)))
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k *= spread
+    k[:, 0] = 0.0
+    k[:, 0, :, 0] = gap * dim ** 0.5 / 8
+    v = v + 1
+    v[:, 0] = 0.0
+    got, lse, want = attend(dtype, eight, q, k, v, prefix)
+    half = dtype == "f16" or eight
+    check(dtype, eight, got, lse, want, keys, dim, slack=2.0 ** -31 * want["top"] if half else 0.0)
