@@ -22,6 +22,7 @@ struct graft_kv {
   uint32_t wait_polls = 0;
   int32_t axes = 1;             // of positions that the caller gives
   uint8_t pair_axis[64] = {0};  // axis whose position turns a pair
+  uint32_t prepared = 0;        // forms of the attention, a bit each
   int32_t last_launches = 0;
   char msg[256] = {0};
 };
@@ -169,6 +170,21 @@ void free_all(graft_kv* h) {
   cudaFree(h->line);
 }
 
+// The kernels of a form are loaded when a handle first needs them: the plain form's with the handle, a shaped one's in its
+// first call, which may be under capture (a process' first handle takes 1.2 ms so over 16-bit caches and 1.6 over 8-bit ones; with
+// every form of every type and head size 4.5 and 23).
+cudaError_t prepare(graft_kv* h, int form) {
+  if (h->prepared >> form & 1) return cudaSuccess;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  e = graft::prepare_kv_attend(form, h->cfg.dtype, h->layout.dim, h->layout.eight != 0);
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e == cudaSuccess) e = back;
+  if (e == cudaSuccess) h->prepared |= 1u << form;
+  return e;
+}
+
 // graft_kv_append and graft_kv_append_ext
 int append(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride,
            const void* d_v, int64_t v_stride, const int32_t* d_depth, const int32_t* d_rows, const int32_t* d_position,
@@ -282,6 +298,7 @@ int attend(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q
     return fail(h, GRAFT_ECUDA, "the driver refused the queries' tensor map");
   if (!cache_map(c, h->cfg.dtype, d_k_cache, &kmap) || !cache_map(c, h->cfg.dtype, d_v_cache, &vmap))
     return fail(h, GRAFT_ECUDA, "the driver refused the cache's tensor map");
+  if (const cudaError_t e = prepare(h, graft::kv_attend_form(a.slope, a.softcap, a.window))) return cuda_fail(h, e, "loading the attention");
   const cudaError_t e = graft::launch_kv_attend(a, qmap, kmap, vmap, h->cfg.dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(h, e, "graft_kv_attend launch");
   h->last_launches = a.plan.cut ? 2 : 1;
@@ -335,7 +352,7 @@ int graft_kv_init(const graft_kv_config* cfg, graft_kv** out) {
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->line), ((size_t)cfg->max_batch + 1 + h->num_sms) * 8);
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ENOMEM; }
   e = cudaMemset(h->err, 0, 16);
-  if (e == cudaSuccess) e = graft::prepare_kv_attend(c.eight != 0);
+  if (e == cudaSuccess) e = prepare(h, 0);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) { free_all(h); delete h; return GRAFT_ECUDA; }
   *out = h;

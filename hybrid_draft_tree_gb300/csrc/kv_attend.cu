@@ -155,11 +155,10 @@ const AttendForm* const kForms[2][4] = {{&kAttendPlain, &kAttendWindowed, &kAtte
                                         {&kAttendEightPlain, &kAttendEightWindowed, &kAttendEightCapped, &kAttendEightBiased}};
 }  // namespace
 
-cudaError_t prepare_kv_attend(bool eight) {
-  for (const AttendForm* f : kForms[eight])
-    if (const cudaError_t e = f->prepare()) return e;
-  return cudaSuccess;
+int kv_attend_form(const float* slope, float softcap, int window) {
+  return slope || softcap * kLog2e > kWide ? kBiased : softcap > 0.f ? kCapped : window > 0 ? kWindowed : kPlain;
 }
+cudaError_t prepare_kv_attend(int form, int dtype, int dim, bool eight) { return kForms[eight][form]->prepare(dtype, dim); }
 
 int64_t kv_attend_part_rows(int64_t rows, int num_sms) { return 2 * rows + (int64_t)num_sms * 256; }
 
@@ -267,7 +266,7 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
 
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s) {
-  const int form = a.slope || a.softcap * kLog2e > kWide ? kBiased : a.softcap > 0.f ? kCapped : a.window > 0 ? kWindowed : kPlain;
+  const int form = kv_attend_form(a.slope, a.softcap, a.window);
   const cudaError_t e = kForms[a.c.eight != 0][form]->launch(a, qmap, kmap, vmap, dtype, s);
   if (e != cudaSuccess || !a.plan.cut) return e;
   if (a.c.dim == 128) return dtype == GRAFT_BF16 ? join<__nv_bfloat16, 128>(a, s) : join<__half, 128>(a, s);

@@ -1469,12 +1469,9 @@ cudaError_t prepare_one() {
   return e != cudaSuccess ? e : cudaFuncSetAttribute(k_kv_attend<T, D, 2, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
 }
 template <bool EIGHT, int SHAPED>
-cudaError_t prepare_form() {
-  cudaError_t e = prepare_one<__nv_bfloat16, 128, EIGHT, SHAPED>();
-  if (e == cudaSuccess) e = prepare_one<__nv_bfloat16, 64, EIGHT, SHAPED>();
-  if (e == cudaSuccess) e = prepare_one<__half, 128, EIGHT, SHAPED>();
-  if (e == cudaSuccess) e = prepare_one<__half, 64, EIGHT, SHAPED>();
-  return e;
+cudaError_t prepare_form(int dtype, int dim) {
+  if (dim == 128) return dtype == GRAFT_BF16 ? prepare_one<__nv_bfloat16, 128, EIGHT, SHAPED>() : prepare_one<__half, 128, EIGHT, SHAPED>();
+  return dtype == GRAFT_BF16 ? prepare_one<__nv_bfloat16, 64, EIGHT, SHAPED>() : prepare_one<__half, 64, EIGHT, SHAPED>();
 }
 
 }  // namespace

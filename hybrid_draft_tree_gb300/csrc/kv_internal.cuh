@@ -148,7 +148,8 @@ __device__ __forceinline__ float kv_scale(const float* scale, int head, uint32_t
 
 cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t s);
-cudaError_t prepare_kv_attend(bool eight);
+int kv_attend_form(const float* slope, float softcap, int window);  // which of the forms below a call takes, 0 the plain one
+cudaError_t prepare_kv_attend(int form, int dtype, int dim, bool eight);
 int64_t kv_attend_part_rows(int64_t rows, int num_sms);
 AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim, int prefix_len, int max_ctx,
                           int window, bool eight, bool capped, int num_sms);
@@ -157,7 +158,7 @@ cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const
 // Its forms, a translation unit each: what becomes of scores (kPlain to kBiased) over a cache in the model's type and over an
 // 8-bit one.
 struct AttendForm {
-  cudaError_t (*prepare)();
+  cudaError_t (*prepare)(int dtype, int dim);
   cudaError_t (*launch)(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         int dtype, cudaStream_t s);
 };
