@@ -977,10 +977,12 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, float to_log2, b
     }
   }
 }
-// The bias takes distances as whole numbers, from the block's last key on: it is exact next to the row's own key whatever
-// the slope, and no further off than the bias of the block's nearest key is rounded.
+// The bias takes distances as whole numbers, of a block that lies before the row's own key from its last key on: it is no
+// further off than the bias of the block's nearest key is rounded, and exact next to the row's own key whatever the slope.
+// Blocks that end inside, a prefix' last among them, take each key's own distance: from a last key that is none, and lies
+// behind the row's own, a steep slope would lead beyond fp32.
 __device__ __forceinline__ void bias_scores(const Item& it, const Block& k, int place, uint64_t mask, float slope, float factor, float* s) {
-  const int d = k.prefix ? BN : it.ctx - k.base;  // keys before the tree
+  const int d = k.prefix ? k.valid : it.ctx - k.base;  // keys before the tree
   if (d >= BN) {
     const float near = slope * (float)(k.place + (BN - 1) - place);
 #pragma unroll

@@ -146,3 +146,16 @@ def test_a_first_key_that_outweighs_the_others(gap, spread, dtype, eight, batch,
     got, lse, want = attend(dtype, eight, q, k, v, prefix)
     half = dtype == "f16" or eight
     check(dtype, eight, got, lse, want, keys, dim, slack=2.0 ** -31 * want["top"] if half else 0.0)
+
+
+@pytest.mark.parametrize("slope", [0.3, 50.0, 1e37])
+@pytest.mark.parametrize("prefix,own", [(5, 0), (5, 3), (130, 1), (100, 300)])
+@pytest.mark.parametrize("dtype,eight,slots,hq,hk,dim", [
+    ("bf16", False, 1, 4, 2, 128), ("f16", False, 20, 4, 2, 64), ("bf16", True, 40, 4, 1, 128), ("f16", True, 2, 4, 1, 64)])
+def test_slopes_behind_a_prefix_that_ends_inside_a_block(slope, prefix, own, dtype, eight, slots, hq, hk, dim):
+    """However steep, a slope leaves a row its own key."""
+    keys = prefix + own + slots
+    gen = torch.Generator(device="cuda").manual_seed(keys + dim)
+    q, k, v = (torch.randn(s, generator=gen, device="cuda") for s in ((1, slots, hq, dim), (1, keys, hk, dim), (1, keys, hk, dim)))
+    got, lse, want = attend(dtype, eight, q, k, v, prefix, slopes=torch.full((hq,), slope, device="cuda"))
+    check(dtype, eight, got, lse, want, keys, dim)
