@@ -253,6 +253,7 @@ static PyObject* attend_ext(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) { PyErr_Clear(); GIVE_UP; }
   if (!small(batch) || !small(slots) || !small(prefix) || !small(max_ctx) || !small(window) || batch < 0 || slots < 1 || prefix < 0)
     GIVE_UP;
+  if (softcap != 0.0 && (float)softcap == 0.f) GIVE_UP; /* would be no cap at all */
   const long long rows = batch * slots;
   void *q, *kc, *vc, *pt, *ctx, *out, *pre, *mask, *lse, *slope, *sk, *sv;
   int64_t qs, os;

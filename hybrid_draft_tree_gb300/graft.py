@@ -845,6 +845,8 @@ class GraftKV:
         pages = -(-max(prefix_len, 0) // self.page_size)
         if not -2 ** 31 <= window < 2 ** 31:
             raise GraftError(GRAFT_EINVAL, f"window {window}: beyond 32 bits")
+        if softcap != 0 and ctypes.c_float(softcap).value == 0:
+            raise GraftError(GRAFT_EINVAL, f"softcap {softcap}: zero in 32 bits, which is no cap")
         scores = graft_kv_scores(softcap, window, _addr(slopes, "slopes", _T.float32, self.q_heads))
         self._check(self.L.graft_kv_attend_ext(self.h, batch, slots, pq, qs, _cache(k_cache, "k_cache", dc, self.span),
                                                _cache(v_cache, "v_cache", dc, self.span),
