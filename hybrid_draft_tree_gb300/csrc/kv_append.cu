@@ -48,8 +48,9 @@ __device__ __forceinline__ uint32_t read_given(const AppendArgs& a, int64_t q_ro
   return (uint32_t)all_q | (uint32_t)all_k << 1;
 }
 
-// given: 4, or the verdict on positions of the caller's, which take the place of base + depth.
-__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r, uint32_t given = 4) {
+// GIVEN: `given` is the verdict on positions of the caller's, which take the place of base + depth.
+template <bool GIVEN>
+__device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r, uint32_t given = 0) {
   Token t{0, -1, -1};
   const int64_t first = (int64_t)b * a.slots;
   const int64_t ctx = a.ctx_len[b];
@@ -58,17 +59,16 @@ __device__ __forceinline__ Token locate(const AppendArgs& a, int b, int i, int r
   uint32_t bad = ctx < 0 || r >= a.slots ? GRAFT_ERR_RANGE : 0;
   if (ctx >= 0 && a.q) {
     const int32_t d = a.depth ? a.depth[first + i] : i;
-    const bool in = given == 4 ? base + d < limit : given & 1;
-    if (d >= 0 && !in) bad = GRAFT_ERR_RANGE;
-    else if (d >= 0) t.q_pos = given == 4 ? (int32_t)(base + d) : 0;
+    if (d >= 0 && (GIVEN ? !(given & 1) : base + d >= limit)) bad = GRAFT_ERR_RANGE;
+    else if (d >= 0) t.q_pos = GIVEN ? 0 : (int32_t)(base + d);
   }
   if (ctx >= 0 && r >= 0 && r < a.slots) {
     const int32_t d = a.depth ? a.depth[first + r] : r;
     if (d >= 0) {
       const int64_t at = ctx + i, p = at >> a.c.page_shift;
       const int32_t page = p < a.table_stride ? a.page_table[(int64_t)b * a.table_stride + p] : -1;
-      if (page >= 0 && page < a.c.num_pages && (given == 4 ? base + d < limit : given & 2)) {
-        t.k_pos = given == 4 ? (int32_t)(base + d) : 0;
+      if (page >= 0 && page < a.c.num_pages && (GIVEN ? (given & 2) != 0 : base + d < limit)) {
+        t.k_pos = GIVEN ? 0 : (int32_t)(base + d);
         t.dst = page * a.c.page_stride + (at & (a.c.page_size - 1)) * a.c.token_stride;
       } else {
         bad = GRAFT_ERR_RANGE;
@@ -187,8 +187,10 @@ __device__ __forceinline__ void head_element(const AppendArgs& a, const T* src, 
 }
 
 // One CTA a token.  A thread takes pieces of heads: those of q, of k and of v, in turn.
+// Into an 8-bit cache, by positions of several axes, or both: more to compute and to hold, so eight CTAs an SM, or registers
+// leave seven (1 x 32768 in 8 bits 138 us, 144 then).
 template <typename T, bool HALVES, bool EIGHT, bool AXES>
-__device__ __forceinline__ void append_token(const AppendArgs& a) {
+__global__ void __launch_bounds__(kThreads, 8) k_kv_append_ext(const __grid_constant__ AppendArgs a) {
   grid_dependents_launch();
   grid_dependency_wait();
   const int64_t n = blockIdx.x;
@@ -228,7 +230,7 @@ __device__ __forceinline__ void append_token(const AppendArgs& a) {
       }
     }
     if (!located) {
-      t = AXES ? locate(a, b, i, r, read_given(a, n, k_row, has_k, s_given)) : locate(a, b, i, r);
+      t = AXES ? locate<true>(a, b, i, r, read_given(a, n, k_row, has_k, s_given)) : locate<false>(a, b, i, r);
       located = true;
     }
 #pragma unroll
@@ -287,17 +289,104 @@ __device__ __forceinline__ void append_token(const AppendArgs& a) {
   }
 }
 
-template <typename T, bool HALVES>
-__global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
-  append_token<T, HALVES, false, false>(a);
+// The same on pieces as they come, from the angles' row.
+template <typename T>
+__device__ __forceinline__ void turn_packed_halves(const float* cs, int half, int u, uint4& x, uint4& y) {
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + 8 * u), c1 = *reinterpret_cast<const float4*>(cs + 8 * u + 4);
+  const float4 s0 = *reinterpret_cast<const float4*>(cs + half + 8 * u);
+  const float4 s1 = *reinterpret_cast<const float4*>(cs + half + 8 * u + 4);
+  uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = Pair<T>::get(xw[j]), q = Pair<T>::get(yw[j]);
+    xw[j] = Pair<T>::put(p.x * c[2 * j] - q.x * s[2 * j], p.y * c[2 * j + 1] - q.y * s[2 * j + 1]);
+    yw[j] = Pair<T>::put(q.x * c[2 * j] + p.x * s[2 * j], q.y * c[2 * j + 1] + p.y * s[2 * j + 1]);
+  }
+  x = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+  y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
 }
-// More to compute and to hold: eight CTAs an SM, or registers leave seven (1 x 32768 in 8 bits 138 us, 144 then).
-template <typename T, bool HALVES, bool EIGHT, bool AXES>
-__global__ void __launch_bounds__(kThreads, 8) k_kv_append_ext(const __grid_constant__ AppendArgs a) {
-  append_token<T, HALVES, EIGHT, AXES>(a);
+template <typename T>
+__device__ __forceinline__ void turn_packed_pairs(const float* cs, int half, int u, uint4& x) {
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + 4 * u), s0 = *reinterpret_cast<const float4*>(cs + half + 4 * u);
+  const float c[4] = {c0.x, c0.y, c0.z, c0.w}, s[4] = {s0.x, s0.y, s0.z, s0.w};
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = Pair<T>::get(w[j]);
+    w[j] = Pair<T>::put(p.x * c[j] - p.y * s[j], p.y * c[j] + p.x * s[j]);
+  }
+  x = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The same by elements and rotating pairs, for any alignment and any rot_dim.
+// Into a cache in the model's type, by the one position of a token: a kernel with a body of its own (1 x 32768: 127 us; as an
+// instance of the body above 131).
+template <typename T, bool HALVES>
+__global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ AppendArgs a) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const int64_t n = blockIdx.x;
+  const int b = a.by_slots.div((int)n), i = (int)n - b * a.slots, dim = a.c.dim;
+  const int r = a.rows ? a.rows[n] : i;
+  const int half = a.c.rot >> 1, pairs = HALVES ? half >> 3 : 0;
+  const int ru = (dim >> 3) - pairs, vu = dim >> 3;  // pieces of a rotating head, each with its partner, and of a value head
+  const bool has_k = r >= 0 && r < a.slots;
+  const int nq = a.q ? a.c.q_heads * ru : 0, nk = has_k ? a.c.kv_heads * ru : 0, nv = has_k ? a.c.kv_heads * vu : 0;
+  const int64_t k_row = (int64_t)b * a.slots + r;
+  constexpr int kPer = 2;  // pieces in flight
+  Token t;
+  bool located = false;
+  for (int w0 = threadIdx.x; w0 < nq + nk + nv || !located; w0 += kPer * kThreads) {
+    uint4 x[kPer], y[kPer];
+    int kind[kPer], head[kPer], u[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      int w = w0 + j * kThreads;
+      kind[j] = w < nq ? 0 : w < nq + nk ? 1 : w < nq + nk + nv ? 2 : 3;
+      if (kind[j] == 3) continue;
+      const Divisor& by = kind[j] == 2 ? a.by_value : a.by_turn;
+      w -= kind[j] == 0 ? 0 : kind[j] == 1 ? nq : nq + nk;
+      head[j] = by.div(w);
+      u[j] = w - head[j] * (int)by.d;
+      const T* src = kind[j] == 0 ? static_cast<const T*>(a.q) + n * a.q_stride
+                                  : kind[j] == 1 ? static_cast<const T*>(a.k) + k_row * a.k_stride : static_cast<const T*>(a.v) + k_row * a.v_stride;
+      src += head[j] * dim;
+      const int at = HALVES && kind[j] < 2 && u[j] >= pairs ? u[j] + pairs : u[j];
+      x[j] = __ldcs(reinterpret_cast<const uint4*>(src) + at);
+      if (HALVES && kind[j] < 2 && u[j] < pairs) y[j] = __ldcs(reinterpret_cast<const uint4*>(src) + u[j] + pairs);
+    }
+    if (!located) {
+      t = locate<false>(a, b, i, r);
+      located = true;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (kind[j] == 3 || (kind[j] == 0 ? t.q_pos : t.k_pos) < 0) continue;
+      T* dst = kind[j] == 0 ? static_cast<T*>(a.q_out) + n * a.q_out_stride + head[j] * dim
+                            : static_cast<T*>(kind[j] == 1 ? a.k_cache : a.v_cache) + t.dst + head[j] * a.c.head_stride;
+      uint4* out = reinterpret_cast<uint4*>(dst);
+      if (kind[j] == 2) {
+        out[u[j]] = x[j];
+        continue;
+      }
+      const float* cs = a.rope + (int64_t)(kind[j] == 0 ? t.q_pos : t.k_pos) * a.c.rot;
+      if (HALVES) {
+        if (u[j] < pairs) {
+          turn_packed_halves<T>(cs, half, u[j], x[j], y[j]);
+          out[u[j]] = x[j];
+          out[u[j] + pairs] = y[j];
+        } else {
+          out[u[j] + pairs] = x[j];
+        }
+      } else {
+        if (8 * u[j] < a.c.rot) turn_packed_pairs<T>(cs, half, u[j], x[j]);
+        out[u[j]] = x[j];
+      }
+    }
+  }
+}
+// Both by elements and rotating pairs, for any alignment and any rot_dim.
 template <typename T, bool EIGHT, bool AXES>
 __global__ void __launch_bounds__(kThreads) k_kv_append_elements(const __grid_constant__ AppendArgs a) {
   grid_dependents_launch();
@@ -307,7 +396,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_elements(const __grid_co
   const int r = a.rows ? a.rows[n] : i;
   const int64_t k_row = (int64_t)b * a.slots + r;
   __shared__ Given s_given;
-  const Token t = AXES ? locate(a, b, i, r, read_given(a, n, k_row, r >= 0 && r < a.slots, s_given)) : locate(a, b, i, r);
+  const Token t = AXES ? locate<true>(a, b, i, r, read_given(a, n, k_row, r >= 0 && r < a.slots, s_given)) : locate<false>(a, b, i, r);
   const int ru = dim - (a.c.rot >> 1);
   const int nq = t.q_pos >= 0 ? a.c.q_heads * ru : 0, nk = t.k_pos >= 0 ? a.c.kv_heads * ru : 0;
   const int nv = t.k_pos >= 0 ? a.c.kv_heads * dim : 0;
