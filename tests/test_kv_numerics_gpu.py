@@ -70,7 +70,7 @@ def attend(dtype, eight, q, k, v, prefix=0, page=32, **scores):
         size = s.abs().amax(-1)
         if scores.get("slopes") is not None:
             s = s - scores["slopes"].double().view(hk, -1, 1) * distance[:, None, None]
-        s = s.masked_fill((distance < 0)[:, None, None], -math.inf)
+        s = s.masked_fill(((distance < 0) | (distance >= (scores.get("window") or keys)))[:, None, None], -math.inf)
         z = torch.logsumexp(s, -1)
         w = torch.exp(s - z[..., None])
         want["out"].append(torch.einsum("shgn,nhd->shgd", w, vn[b]))
@@ -106,6 +106,23 @@ def test_a_cap_far_above_the_scores_changes_next_to_nothing(cap, dtype, eight, s
     k, v = (torch.randn((2, 700 + slots, hk, dim), generator=gen, device="cuda") for _ in range(2))
     got, lse, want = attend(dtype, eight, q, k, v, softcap=cap)
     check(dtype, eight, got, lse, want, 700 + slots, dim, cap)
+
+
+@pytest.mark.parametrize("more", [dict(prefix=300), dict(prefix=300, window=500), dict(window=90), dict(prefix=40, slopes=0.2)],
+                         ids=lambda m: "-".join(m))
+@pytest.mark.parametrize("cap", [300.0, 1e6])
+@pytest.mark.parametrize("dtype,eight,slots,hq,hk,dim", [
+    ("bf16", False, 2, 4, 2, 64), ("f16", False, 61, 8, 2, 128), ("f16", True, 1, 4, 1, 128), ("bf16", True, 40, 8, 2, 64)])
+def test_wide_caps_with_all_else(cap, more, dtype, eight, slots, hq, hk, dim):
+    gen = torch.Generator(device="cuda").manual_seed(slots + dim)
+    q = torch.randn((3, slots, hq, dim), generator=gen, device="cuda") * 6
+    k, v = (torch.randn((3, 800 + slots, hk, dim), generator=gen, device="cuda") for _ in range(2))
+    more = dict(more)
+    if "slopes" in more:
+        more["slopes"] = torch.full((hq,), more["slopes"], device="cuda")
+    got, lse, want = attend(dtype, eight, q, k, v, softcap=cap, **more)
+    # the bias adds 4 e of itself to a score: at most 0.2 times the keys, where a weight counts far less
+    check(dtype, eight, got, lse, want, 800 + slots, dim, cap, slack=2 * 4 * E * 0.2 * 900 * want["spread"] if "slopes" in more else 0.0)
 
 
 @pytest.mark.parametrize("cap", [30.0, 150.0, 400.0, 3000.0, 2e4])
