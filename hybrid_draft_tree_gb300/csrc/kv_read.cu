@@ -1,6 +1,6 @@
 // Keys and values out of the paged cache: rows in the model's type, of 8-bit
-// caches the numbers that the codes stand for (code times the head's scale, one
-// rounding).  Bound by memory: 1 x 32768, 8 heads of 128, 33.4 us, 6.0 TB/s, 89%
+// caches the numbers that the codes stand for (code times the head's scale, in
+// fp32, then rounded to the type).  Bound by memory: 1 x 32768, 8 heads of 128, 33.4 us, 6.0 TB/s, 89%
 // of the copy rate.
 #include "kv_internal.cuh"
 

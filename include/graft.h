@@ -577,9 +577,9 @@ int graft_kv_set_axes(graft_kv* h, int32_t axes, const int32_t* pair_axis);
  *                and pads stay as they are there.  One outside d_rope on any
  *                axis skips that write and sets GRAFT_ERR_RANGE
  *   scales       of an 8-bit cache, or NULL.  The stored number is the nearest
- *                e4m3 number to x / scale (ties to even), x the rotated key or
- *                the value in fp32, and 448 in magnitude beyond that, for an
- *                infinite x too; a NaN is kept */
+ *                e4m3 number (ties to even) to the fp32 number next to
+ *                x / scale, x the rotated key or the value in fp32, and 448 in
+ *                magnitude beyond that, for an infinite x too; a NaN is kept */
 int graft_kv_append_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride, const void* d_k,
                         int64_t k_stride, const void* d_v, int64_t v_stride, const int32_t* d_depth,
                         const int32_t* d_rows, const int32_t* d_position, const float* d_rope, int32_t rope_len,
@@ -590,7 +590,7 @@ int graft_kv_append_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d
 /* Read back: the key and value of place d_first[b] + i of request b, for i <
  * d_count[b], into row b * slots + i of d_k_out and d_v_out (kv_heads * head_dim
  * elements of the 16-bit type; row strides in elements); of an 8-bit cache, code
- * times scale, rounded once.  Rows from d_count[b] on are not written.
+ * times scale, rounded to fp32 and then to the type.  Rows from d_count[b] on are not written.
  *   d_first, d_count   int32 [batch], first >= 0, count in [0, slots] (outside:
  *                      clamped, with GRAFT_ERR_RANGE; a negative first reads
  *                      nothing)
@@ -610,7 +610,8 @@ int graft_kv_read(graft_kv* h, int32_t batch, int32_t slots, const void* d_k_cac
  *            depends on the scores of the rows beside a row, so that its last bits
  *            may change with them (with the same inputs they are the same)
  *   d_slope  DEVICE float [q_heads] or NULL: s -= d_slope[h] * (pos_i - pos_j);
- *            one that is not finite counts as 0 and sets GRAFT_ERR_RULE
+ *            one that is not finite (in units of log2: up to 2.3e38) counts as 0
+ *            and sets GRAFT_ERR_RULE
  *   window   > 0: keys with pos_i - pos_j >= window are not seen */
 typedef struct {
   float softcap;
@@ -621,7 +622,8 @@ typedef struct {
 /* graft_kv_attend on either kind of cache, with scales (of an 8-bit one) and
  * shaped scores; either may be NULL.  On an 8-bit cache
  *   s_j = scale * k_scale[h] * (q . code of k_j),  out = v_scale[h] * sum exp(s_j - lse) (code of v_j).
- * scale * k_scale[h] has to stay within fp32; otherwise as there. */
+ * scale * k_scale[h] has to stay within fp32, and v_scale[h] to be 2^-79 at
+ * least, so that its quotient by the sum of weights does; otherwise as there. */
 int graft_kv_attend_ext(graft_kv* h, int32_t batch, int32_t slots, const void* d_q, int64_t q_stride,
                         const void* d_k_cache, const void* d_v_cache, const int32_t* d_prefix_pages,
                         int32_t prefix_len, const int32_t* d_page_table, int32_t table_stride,

@@ -176,3 +176,27 @@ def test_slopes_behind_a_prefix_that_ends_inside_a_block(slope, prefix, own, dty
     q, k, v = (torch.randn(s, generator=gen, device="cuda") for s in ((1, slots, hq, dim), (1, keys, hk, dim), (1, keys, hk, dim)))
     got, lse, want = attend(dtype, eight, q, k, v, prefix, slopes=torch.full((hq,), slope, device="cuda"))
     check(dtype, eight, got, lse, want, keys, dim)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_what_is_read_back_is_the_fp32_product_rounded_to_the_type(dtype):
+    """Bit for bit: every code under scales of every last bit, products beyond the type's range and below its smallest among
+    them."""
+    heads = 300
+    gen = torch.Generator().manual_seed(5)
+    scale = torch.exp2(torch.rand(heads, generator=gen) * 60 - 40)
+    codes = torch.arange(256, dtype=torch.uint8)
+    cache = codes.view(1, 1, 4, 64).repeat(1, heads, 2, 1).cuda()       # one page of 8 tokens
+    kv = g.GraftKV(g.graft_kv_default_config(heads, heads, 64, 8, 1, 1, 1, GDT[dtype], cache="e4m3"))
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.empty((4, heads * 64), dtype=DT[dtype], device="cuda") for _ in range(2)]
+    kv.read(1, 4, cache, cache, zero.view(1, 1), zero, zero + 4, *outs, k_scale=scale.cuda(), v_scale=scale.cuda())
+    assert kv.sync() == 0
+    number = codes.view(E4M3).float()
+    want = (scale[:, None] * number).to(DT[dtype]).view(heads, 4, 64).transpose(0, 1)
+    finite = ~torch.isnan(want)
+    assert finite.sum() == heads * 254
+    for o in outs:
+        got = o.cpu().view(4, heads, 64)
+        assert torch.equal(torch.isnan(got), ~finite)
+        assert torch.equal(got.view(torch.int16)[finite], want.contiguous().view(torch.int16)[finite])
