@@ -182,7 +182,8 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
   int two = wide ? 152 : 130, one = wide ? 85 : 130, fixed_two = wide ? 650 : 400, fixed_one = wide ? 280 : 450;
   int memory = wide ? 120 : 65, l2 = wide ? 70 : 35;
   const bool few = eight && R <= 16;
-  const int step_few = R <= 8 ? (wide ? 47 : 29) : (wide ? 61 : 41), fixed_few = 280, item_few = R <= 8 ? 260 : 350, busy_few = wide ? 67 : 40;
+  const int step_few = R <= 8 ? (wide ? 47 : 29) : (wide ? 61 : 41), fixed_few = 280;
+  const int item_few = R <= 8 ? 260 : wide ? 720 : 600, busy_few = R <= 8 ? (wide ? 67 : 40) : (wide ? 74 : 31);
   if (eight) {
     two = wide ? 190 : 140;
     one = wide ? 125 : 115;
@@ -234,9 +235,17 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
     }
     if (few && packed) {
       // As many CTAs for the packed items as end with the others.  Beside CTAs that keep memory busy both are slower than
-      // alone: what the packed ones pay before and after their blocks was 10 to 27 us, an item of the others 2.6 us and 0.67 a
-      // block (64 x 1 behind 8192 + 1024: 59 us with 40 or 50 CTAs for the packed items, 74 with 30, 67 with 70; behind 2048 +
-      // 1024 50 with 40, 71 with 10; behind 8192 + 100 38 with 80, 58 with 30; behind 30000 + 500 76 with 100, 121 with 40).
+      // alone: what the packed ones pay before and after their blocks was 9 to 27 us, an item of the others up to 8 rows 2.6 us
+      // and 0.67 a block, up to 16 rows 7.2 and 0.74 (heads of 64 6 and 0.3: it waits for its queries where the other asks for
+      // them ahead).  In us, by the number of CTAs for the packed items:
+      //   64 x 1 behind 8192 + 1024, 32/8 heads of 128   55.8 with 40, 57.3 with 47 (the rule), 55.3 with 60, 72 with 30, 64 with 80
+      //   16 x 1 behind 8192 + 4000                      41.8 with 40 or 60, 42.7 with 55 (the rule), 62 with 30 or 80
+      //   64 x 1 behind 8192 + 100, heads of 64          29.6 with 70, 36.4 with 96 (the rule), 44 with 30
+      //   64 x 1 behind 2000 + 4000, heads of 64         58.5 with 10, 67 with 7 (the rule), 71 with 40
+      //   64 x 3 behind 8192 + 1024                      97.3 with 50, 96.6 with 60 (the rule 57), 136 with 30, 110 with 80
+      //   the same, heads of 64                          60.0 with 70 (the rule 69), 72 with 50, 66 with 80
+      //   64 x 4 behind 8192 + 100                       81 with 80, 97 with 60 or 100 (the rule 90)
+      //   16 x 3 behind 8192 + 2000                      47.2 with 70, 51.6 with 80 (the rule 78), 71 with 50
       const double line = p.items_a * (p.fixed_a + (double)np * p.step_a);
       double best_end = 0;
       for (int n = 1; n < num_sms; ++n) {
