@@ -570,14 +570,14 @@ __device__ __forceinline__ void convert_query(uint8_t* tile, int row, uint8_t* b
 // the products), of which there are then as many under way.
 constexpr int kTeams = 2, kTeamWarps = 2;
 
-// ---- warp 11, and 10 with large pages: an 8-bit cache's bf16 queries ---------------------------------------------
+// ---- warps 10 and 11: an 8-bit cache's bf16 queries --------------------------------------------------------------
 // Warps that have nothing else to do.  When the converting warps did this beside a piece's first tiles, 16 x 61 behind
 // 12001 + 2048 took 224 us, 218 so, and 19 x 12 behind 6132 80, 75 so; contexts of a block or two lose by fewer threads
 // (15 x 17 behind 91 12.9 us, 13.8 so).
-template <int D, int L, int SHAPED>
+template <int D, int SHAPED>
 __device__ void query_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
-  constexpr int kFirst = L == 2 ? kCleanWarp : kSpareWarp, kThreadsHere = (kCleanWarp + 1 - kFirst) * 32;
-  const int lane = threadIdx.x & 31, thread = threadIdx.x - kFirst * 32;
+  constexpr int kThreadsHere = (kCleanWarp + 1 - kSpareWarp) * 32;
+  const int lane = threadIdx.x & 31, thread = threadIdx.x - kSpareWarp * 32;
   int piece = 0;
   Pieces<SHAPED> pieces(a, sh.line);
   Item it;
@@ -1407,7 +1407,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       mbar_init(&sh.clean[i], EIGHT ? kTeamWarps : 3 - L);
     }
     for (int t = 0; t < 2; ++t) { mbar_init(&sh.s_full[t], 1); mbar_init(&sh.s_read[t], 4); mbar_init(&sh.p_full[t], 4); mbar_init(&sh.o_done[t], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); mbar_init(&sh.q_ready[i], 3 - L); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_free[i], 8); mbar_init(&sh.q_ready[i], 2); }
     mbar_init(&sh.o_free, 8);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < 8; ++i) sh.bad[i] = sh.bad_edge[i] = 0;
@@ -1432,7 +1432,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       __syncwarp();
     } else if (EIGHT) {
       if (warp >= kConvertWarp) convert_role<T, D, SHAPED>(a, sh, base + S::kRing, base + S::kProducts);
-      else if (std::is_same<T, __nv_bfloat16>::value) query_role<D, L, SHAPED>(a, sh, base);
+      else if (std::is_same<T, __nv_bfloat16>::value) query_role<D, SHAPED>(a, sh, base);
     } else clean_role<T, D, L, SHAPED>(a, sh, base + S::kRing);
   }
   tc::fence_before();
@@ -1449,12 +1449,16 @@ static_assert(kSmem<64, false> <= 227 * 1024 && kSmem<128, false> <= 227 * 1024 
 
 // Small pages' copies take two warps where items have one tile and blocks little else to do (8 x 1 behind 700, pages of
 // 16: 12.6 us, 15.1 with one warp; 8 x 17 behind 300 + 600, heads of 64, pages of 32: 11.7 and 12.3); the ring's warps
-// are in the way of more work (64 x 17 behind 2048 + 777, pages of 16: 88 us, 85.5 with one warp).
+// are in the way of more work (64 x 17 behind 2048 + 777, pages of 16: 88 us, 85.5 with one warp).  Over an 8-bit cache, whose
+// pages are a copy each, one warp: the second is worth more to its queries (8 x 17 behind 300, pages of 16: 14.1 us, 16.3 with
+// two; 8 x 17 behind 3000 38.5 and 41.1; 1 x 20 behind 8000, pages of 8: 24.9 and 27.2; but heads of 64, pages of 8, 8 x 17
+// behind 3000: 32.4 and 31.2).
 template <typename T, int D, bool EIGHT, int SHAPED>
 cudaError_t launch_one(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  const bool two_loaders = a.c.page_size <= 32 && !a.plan.packed && a.plan.nt_b == 1;
-  return launch_dependent(two_loaders ? k_kv_attend<T, D, 2, EIGHT, SHAPED> : k_kv_attend<T, D, 1, EIGHT, SHAPED>, dim3(a.plan.ctas),
-                          dim3(kThreads<EIGHT>), kSmem<D, EIGHT>, s, a, qmap, kmap, vmap);
+  auto* kernel = k_kv_attend<T, D, 1, EIGHT, SHAPED>;
+  if constexpr (!EIGHT)
+    if (a.c.page_size <= 32 && !a.plan.packed && a.plan.nt_b == 1) kernel = k_kv_attend<T, D, 2, EIGHT, SHAPED>;
+  return launch_dependent(kernel, dim3(a.plan.ctas), dim3(kThreads<EIGHT>), kSmem<D, EIGHT>, s, a, qmap, kmap, vmap);
 }
 template <bool EIGHT, int SHAPED>
 cudaError_t launch_form(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, cudaStream_t s) {
@@ -1467,8 +1471,10 @@ cudaError_t launch_form(const AttendArgs& a, const CUtensorMap& qmap, const CUte
 
 template <typename T, int D, bool EIGHT, int SHAPED>
 cudaError_t prepare_one() {
-  const cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, 1, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_kv_attend<T, D, 2, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
+  cudaError_t e = cudaFuncSetAttribute(k_kv_attend<T, D, 1, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
+  if constexpr (!EIGHT)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv_attend<T, D, 2, EIGHT, SHAPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, EIGHT>);
+  return e;
 }
 template <bool EIGHT, int SHAPED>
 cudaError_t prepare_form(int dtype, int dim) {
