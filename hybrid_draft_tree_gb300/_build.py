@@ -19,8 +19,8 @@ FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ("api.cu", "assemble.cu", "scan.cu", "umax.cu", "select.cu", "coverage.cu", "sample.cu", "scan_tma.cu", "noalloc.cu",
            "cluster_select.cu", "logit_rules.cu", "kv.cu", "kv_append.cu", "kv_read.cu", "kv_attend.cu",
-           "kv_attend_windowed.cu", "kv_attend_capped.cu", "kv_attend_biased.cu", "kv_attend_eight.cu",
-           "kv_attend_eight_windowed.cu", "kv_attend_eight_capped.cu", "kv_attend_eight_biased.cu")
+           "kv_attend_windowed.cu", "kv_attend_capped.cu", "kv_attend_biased.cu", "kv_attend_any.cu", "kv_attend_eight.cu",
+           "kv_attend_eight_windowed.cu", "kv_attend_eight_capped.cu", "kv_attend_eight_biased.cu", "kv_attend_eight_any.cu")
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -151,12 +151,14 @@ cudaError_t join(const AttendArgs& a, cudaStream_t s) {
 const AttendForm kAttendPlain = {prepare_form<false, kPlain>, launch_form<false, kPlain>};
 
 namespace {
-const AttendForm* const kForms[2][4] = {{&kAttendPlain, &kAttendWindowed, &kAttendCapped, &kAttendBiased},
-                                        {&kAttendEightPlain, &kAttendEightWindowed, &kAttendEightCapped, &kAttendEightBiased}};
+const AttendForm* const kForms[2][5] = {
+    {&kAttendPlain, &kAttendWindowed, &kAttendCapped, &kAttendBiased, &kAttendAny},
+    {&kAttendEightPlain, &kAttendEightWindowed, &kAttendEightCapped, &kAttendEightBiased, &kAttendEightAny}};
 }  // namespace
 
 int kv_attend_form(const float* slope, float softcap, int window) {
-  return slope || softcap * kLog2e > kWide ? kBiased : softcap > 0.f ? kCapped : window > 0 ? kWindowed : kPlain;
+  if (softcap > 0.f) return slope || softcap * kLog2e > kWide ? kAny : kCapped;
+  return slope ? kBiased : window > 0 ? kWindowed : kPlain;
 }
 cudaError_t prepare_kv_attend(int form, int dtype, int dim, bool eight) { return kForms[eight][form]->prepare(dtype, dim); }
 

@@ -126,11 +126,11 @@ struct Item {
 constexpr int kFinal = 0, kItemPart = 1, kCtaPart = 2;
 
 // What becomes of scores, a kernel each (what the loop over the blocks does not use costs it registers and instruction
-// fetches: 19 x 61 behind 2048 under a window takes 41 us in a kernel of its own, 45 in one that can do all of it).  Each can
-// do what those before it can; windows are in all but the first, caps above kWide (in units of log2) in the last alone, whose
-// slopes may be none: what these take would cost smaller caps 6% in the third (16 x 61 behind 8192 under a window
-// of 4096: 148 us, 158 with it).
-constexpr int kPlain = 0, kWindowed = 1, kCapped = 2, kBiased = 3;
+// fetches: 19 x 61 behind 2048 under a window takes 41 us in a kernel of its own, 45 in one that can do all of it): nothing;
+// windows, which the others can do too; caps up to kWide, in units of log2; slopes; caps with slopes, or of any size (with what
+// the latter take 16 x 61 behind 8192 under a window of 4096 and a cap of 50 is at 158 us, 148 without; 19 x 61 over 8 bits
+// behind 6144 with slopes alone at 144, 132 without).
+constexpr int kPlain = 0, kWindowed = 1, kCapped = 2, kBiased = 3, kAny = 4;
 constexpr float kWide = 256.f;
 
 // The line of items.  Packed items come first, then each request's, tile by tile and head by head.  An item takes
@@ -243,7 +243,7 @@ struct Block {
 template <int SHAPED>
 __device__ __forceinline__ Block block_of(const AttendArgs& a, const Item& it, int j) {
   // with slopes the nearest keys first: their scores are the largest, so that bases are set once
-  const int x = (SHAPED ? it.skip : 0) + it.first + (SHAPED == kBiased ? it.blocks - 1 - j : j);
+  const int x = (SHAPED ? it.skip : 0) + it.first + (SHAPED >= kBiased ? it.blocks - 1 - j : j);
   Block k;
   k.prefix = x < it.np;
   k.base = (k.prefix ? x : x - it.np) * BN;
@@ -752,7 +752,7 @@ __device__ void mma_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* rin
       if (!two || t == 0) {
         ok = wait_bar(sh, a, &ready[vs], vp);
         int j = two ? u >> 1 : u;
-        if (SHAPED == kBiased) j = it.blocks - 1 - j;
+        if (SHAPED >= kBiased) j = it.blocks - 1 - j;
         if (!EIGHT && ok && (j >= tree || j == part_full || (SHAPED && j < edge))) {
           ok = wait_bar(sh, a, &sh.clean[vs], (cleaned >> vs) & 1);
           cleaned ^= 1u << vs;
@@ -1054,8 +1054,8 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
   }
   const float scale = SHAPED >= kCapped ? 1.f : to_log2;
   float slope = 0.f;
-  if (SHAPED == kBiased && live) {
-    slope = a.slope ? a.slope[row.head] * kLog2e : 0.f;
+  if (SHAPED >= kBiased && live) {
+    slope = SHAPED == kAny && !a.slope ? 0.f : a.slope[row.head] * kLog2e;
     if (!(fabsf(slope) < INFINITY)) {
       slope = 0.f;
       atomicOr(a.err, GRAFT_ERR_RULE);
@@ -1113,12 +1113,12 @@ __device__ void softmax_role(const AttendArgs& a, Bars& sh, uint8_t* q) {
             if (!((w[c >> 5] >> i) & 1)) s[c + i] = value;
         }
       };
-      if (SHAPED == kCapped || (SHAPED == kBiased && a.softcap > 0.f)) {
+      if (SHAPED == kCapped || SHAPED == kAny) {
         if (k.masked) fill(0);
-        cap_scores<D, EIGHT, SHAPED == kBiased>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
+        cap_scores<D, EIGHT, SHAPED == kAny>(a, to_log2, live && mask != 0, reinterpret_cast<float*>(s));
       }
-      if (SHAPED == kBiased)
-        bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, a.softcap > 0.f ? 1.f : to_log2, reinterpret_cast<float*>(s));
+      if (SHAPED == kBiased || (SHAPED == kAny && a.slope))
+        bias_scores(it, k, view_of(a, it, row.token, mask).place, mask, slope, SHAPED == kAny ? 1.f : to_log2, reinterpret_cast<float*>(s));
       if (k.masked) fill(0xFF800000u);  // -inf
       const float* sf = reinterpret_cast<const float*>(s);
       float mx[4] = {sf[0], sf[1], sf[2], sf[3]};

@@ -199,8 +199,8 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
         slope[nt][i] = 0.f;
         if (SHAPED && on) {
           view[nt][i] = view_of(a, it, own.token, mask[nt][i]);
-          if (SHAPED == kBiased) {
-            slope[nt][i] = a.slope ? a.slope[own.head] * kLog2e : 0.f;
+          if (SHAPED >= kBiased) {
+            slope[nt][i] = SHAPED == kAny && !a.slope ? 0.f : a.slope[own.head] * kLog2e;
             if (!(fabsf(slope[nt][i]) < INFINITY)) {
               slope[nt][i] = 0.f;
               atomicOr(a.err, GRAFT_ERR_RULE);
@@ -263,10 +263,10 @@ __device__ void few_compute(const AttendArgs& a, Bars& sh, const uint8_t* ring, 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (SHAPED >= kCapped && a.softcap > 0.f) s[nt][i] = capped(s[nt][i], f[nt][i & 1] * of_cap, f[nt][i & 1], cap);
+          if (SHAPED == kCapped || SHAPED == kAny) s[nt][i] = capped(s[nt][i], f[nt][i & 1] * of_cap, f[nt][i & 1], cap);
           else s[nt][i] *= f[nt][i & 1];
         }
-      if (SHAPED == kBiased) {
+      if (SHAPED == kBiased || (SHAPED == kAny && a.slope)) {
         const int d = k.prefix ? BN : it.ctx - k.base;  // keys before the tree
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -155,14 +155,14 @@ AttendPlan plan_kv_attend(int batch, int slots, int group, int kv_heads, int dim
                           int window, bool eight, bool capped, int num_sms);
 cudaError_t launch_kv_attend(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int dtype, cudaStream_t s);
-// Its forms, a translation unit each: what becomes of scores (kPlain to kBiased) over a cache in the model's type and over an
+// Its forms, a translation unit each: what becomes of scores (kPlain to kAny) over a cache in the model's type and over an
 // 8-bit one.
 struct AttendForm {
   cudaError_t (*prepare)(int dtype, int dim);
   cudaError_t (*launch)(const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         int dtype, cudaStream_t s);
 };
-extern const AttendForm kAttendPlain, kAttendWindowed, kAttendCapped, kAttendBiased;
-extern const AttendForm kAttendEightPlain, kAttendEightWindowed, kAttendEightCapped, kAttendEightBiased;
+extern const AttendForm kAttendPlain, kAttendWindowed, kAttendCapped, kAttendBiased, kAttendAny;
+extern const AttendForm kAttendEightPlain, kAttendEightWindowed, kAttendEightCapped, kAttendEightBiased, kAttendEightAny;
 
 }  // namespace graft
