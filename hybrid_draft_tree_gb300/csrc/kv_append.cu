@@ -16,7 +16,7 @@
 // Into an 8-bit cache keys and values are rounded to e4m3 over their head's
 // scale on the way; with positions of several axes each pair turns by the angle
 // of its own axis' position, which the CTA reads and judges once.  Bound by
-// instructions then: 1 x 32768 in 8 bits 138 to 143 us (5.3 TB/s), three axes in 16 bits
+// instructions then: 1 x 32768 in 8 bits 138 us (5.5 TB/s), three axes in 16 bits
 // 145 us, both 158; 16 x 61 with both 8 us.
 #include "kv_internal.cuh"
 

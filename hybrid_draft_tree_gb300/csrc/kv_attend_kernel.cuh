@@ -35,9 +35,9 @@
 //   16 x 61 slots behind 12001 + 2048 keys   166 us, 1290 TFLOP/s (176 us in seconds
 //       of it, at the power limit): a block of 256 rows takes 1.5 us, its operands'
 //       way through shared memory (256 KB);
-//   64 x 1 behind 8192 + 1024                 60 us, 3.9 TB/s: memory, then the
+//   64 x 1 behind 8192 + 1024                 58 us, 4.0 TB/s: memory, then the
 //       start (4.5 us to the first scores) and the join (5 us);
-//   1 x 61 behind 32768, pages of 16          43 us, 3.1 TB/s: the copies' issue
+//   1 x 61 behind 32768, pages of 16          44.5 us, 3.0 TB/s: the copies' issue
 //       (one warp: 5.4 TB/s of 4 KB rows), start, ends and join;
 //   64 x 17 behind 2048 + 777, 40/8 heads of 64, f16, pages of 16   86 us:
 //       the latency from scores to weights to products (2700 cycles a unit of 128 x
@@ -48,7 +48,7 @@
 // few rows go another way, in CTAs of their own (kv_few.cuh).  Scores may be capped,
 // windowed or biased (SHAPED).  Measured: 8 bits, 16 x 61 behind 12001 + 2048 218 us (1.9 us
 // a block of 256 rows, 1.3 of 128, by shared memory); a block of 256 rows under a window as
-// without, with biases 1.9 us, capped 2.4 (small scores) to 3.
+// without, with biases 1.9 us, capped 2.4 (small scores) to 3, both 3.6.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -393,6 +393,8 @@ __device__ void load_role(const AttendArgs& a, Bars& sh, uint8_t* q, uint8_t* ri
       ++loads;
     };
     int next = page_of(0);
+    // Keys and values in a loop of two, which the compiler leaves one: 64 x 1 behind 8192 + 1024 58.2 us, 59.6 unrolled; 1 x 61
+    // behind 32768, pages of 16 44.6 and 43.4; 64 x 17, heads of 64, pages of 16 86.0 and 85.6.
     if (!EIGHT || two) {
       for (int j = 0; j < it.blocks && ok; ++j) {
         if (j == q_at) ok = queries();
